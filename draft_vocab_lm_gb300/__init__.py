@@ -478,3 +478,10 @@ def read_ranks_txt(path: str) -> np.ndarray:
 def write_ranks_txt(path: str, ids) -> None:
     with open(path, "w") as f:
         f.writelines(f"{int(x)}\n" for x in ids)
+
+
+from . import step as _step  # noqa: E402  (uses this module's stream and workspace helpers)
+from .step import (KVCache, add_rmsnorm, attention_workspace, beam_reorder, beam_select,  # noqa: E402
+                   beam_workspace, paged_attention)
+
+__all__ += _step.__all__

@@ -19,6 +19,12 @@ DVL_MAX_TOPK = 4
 DVL_K_MULTIPLE = 64
 DVL_MAX_K = 24576
 DVL_HEAD_STATIC = 1
+DVL_F32 = 3
+DVL_MAX_QUERY = 8
+DVL_MAX_QUERY_ROWS = 64
+DVL_MAX_HEAD_DIM = 256
+DVL_MAX_BEAMS = 32
+DVL_MAX_STATES = 8
 
 STATUS_NAMES = {
     0: "DVL_OK", 1: "DVL_ERR_INVALID_ARG", 2: "DVL_ERR_OUT_OF_RANGE",
@@ -33,6 +39,8 @@ EXPORTS = (
     "dvl_draft_argmax", "dvl_draft_topk", "dvl_draft_argmax_noalloc", "dvl_noalloc_status",
     "dvl_draft_plan",
     "dvl_score_ids",
+    "dvl_add_rmsnorm", "dvl_attention_workspace_bytes", "dvl_paged_attention",
+    "dvl_beam_workspace_bytes", "dvl_beam_select", "dvl_beam_reorder",
     "dvl_trim_head", "dvl_learn_rows", "dvl_learn_missing", "dvl_quantize_head",
     "dvl_histogram",
     "dvl_build_ranks", "dvl_union_sorted",
@@ -52,6 +60,71 @@ class DvlHead(ctypes.Structure):
         ("global_scale", ctypes.c_float),
         ("reserved2", ctypes.c_int32),
         ("d2t", ctypes.c_void_p),
+    ]
+
+
+class DvlNorm(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("K", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("group", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("x", ctypes.c_void_p),
+        ("x_stride", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("residual_stride", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p),
+        ("residual_out_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p),
+        ("out_stride", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("codes_stride", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+    ]
+
+
+class DvlKVCache(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32),
+        ("pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_page_stride", ctypes.c_int64),
+        ("k_token_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_page_stride", ctypes.c_int64),
+        ("v_token_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+    ]
+
+
+class DvlState(ctypes.Structure):
+    _fields_ = [
+        ("src", ctypes.c_void_p),
+        ("dst", ctypes.c_void_p),
+        ("row_bytes", ctypes.c_int64),
+        ("src_stride", ctypes.c_int64),
+        ("dst_stride", ctypes.c_int64),
+    ]
+
+
+class DvlBeamPages(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p),
+        ("table_out", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+        ("lengths_out", ctypes.c_void_p),
+        ("spare", ctypes.c_void_p),
+        ("width", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
 
@@ -96,6 +169,17 @@ def lib():
         L.dvl_noalloc_status.argtypes = [p, p]
         L.dvl_draft_plan.argtypes = [hp, i32, i32, p, p]
         L.dvl_score_ids.argtypes = [hp, p, i32, p, i32, p, p]
+        cp = ctypes.POINTER(DvlKVCache)
+        L.dvl_add_rmsnorm.argtypes = [ctypes.POINTER(DvlNorm), p]
+        L.dvl_attention_workspace_bytes.argtypes = [cp, i32, i32]
+        L.dvl_attention_workspace_bytes.restype = sz
+        L.dvl_paged_attention.argtypes = [cp, p, i64, i64, i64, i32, i32, i32, p, i64, i32, p,
+                                          ctypes.c_float, p, p, p, sz, p]
+        L.dvl_beam_workspace_bytes.argtypes = [i32, i32, i32]
+        L.dvl_beam_workspace_bytes.restype = sz
+        L.dvl_beam_select.argtypes = [p, i32, i64, i64, p, i32, i32, i32, i32, p, p, p, p, p, sz, p]
+        L.dvl_beam_reorder.argtypes = [ctypes.POINTER(DvlState), i32, ctypes.POINTER(DvlBeamPages), cp,
+                                       p, i32, i32, i32, p]
         L.dvl_trim_head.argtypes = [hp, p, i32, p, p, p, p, p]
         L.dvl_learn_rows.argtypes = [hp, p, i32, i32, p, p, p, p]
         L.dvl_learn_missing.argtypes = [hp, p, i32, p, p, i32, p, p, p, p, p, p]
@@ -106,6 +190,7 @@ def lib():
         for fn in ("dvl_workspace_init", "dvl_workspace_status", "dvl_draft_argmax", "dvl_draft_topk",
                    "dvl_draft_argmax_noalloc", "dvl_noalloc_status",
                    "dvl_draft_plan", "dvl_score_ids",
+                   "dvl_add_rmsnorm", "dvl_paged_attention", "dvl_beam_select", "dvl_beam_reorder",
                    "dvl_trim_head", "dvl_learn_rows", "dvl_learn_missing", "dvl_quantize_head", "dvl_histogram", "dvl_build_ranks", "dvl_union_sorted"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L

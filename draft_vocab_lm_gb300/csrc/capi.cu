@@ -23,15 +23,13 @@ std::map<int, DeviceInfo> g_dev;
 std::map<std::tuple<const void *, int, size_t>, int> g_occ;
 std::map<std::pair<const void *, int>, size_t> g_smem_limit;  // per kernel and device
 thread_local cudaError_t t_last_error = cudaSuccess;
+}  // namespace
 
 dvl_status cuda_failed(cudaError_t e)
 {
     t_last_error = e;
     return DVL_ERR_CUDA;
 }
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-}  // namespace
 
 cudaError_t device_info(DeviceInfo *out)
 {

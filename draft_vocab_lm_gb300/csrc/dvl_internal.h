@@ -50,6 +50,14 @@ struct DeviceInfo {
 };
 cudaError_t device_info(DeviceInfo *out);
 
+// Record the error behind dvl_last_error and return DVL_ERR_CUDA.
+dvl_status cuda_failed(cudaError_t e);
+
+inline bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
 // Blocks of a streaming kernel that keeps per_sm blocks resident per SM:
 // all of them, except that with two or more per SM a few SMs (one in 38, at
 // least one) get one block fewer.  Measured on GB300 (152 SMs, so 300

@@ -271,6 +271,200 @@ dvl_status dvl_score_ids(const dvl_head *head, const void *h, int32_t M,
                          const int32_t *ids, int32_t c, float *logits, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* The drafting step around the head                                      */
+/*                                                                        */
+/* What a drafter's own layer runs between two draft calls: attention of  */
+/* the new tokens over its paged cache, the residual addition and norm in */
+/* front of a projection or of the head, the choice of the next beams     */
+/* from the head's logits, and the reordering of what belongs to a beam.  */
+/* The pages describe the step (M = 1 for a draft step, 3 for an MTP2     */
+/* verify step, a concurrent batch of 8), not these operators.            */
+/* ---------------------------------------------------------------------- */
+
+/* Limits of these operators. */
+#define DVL_F32 3             /* fp32 activations (dvl_norm.residual_dtype, beam logits) */
+#define DVL_MAX_QUERY 8       /* new tokens per sequence (T)                    */
+#define DVL_MAX_QUERY_ROWS 64 /* T * query heads per cached head                */
+#define DVL_MAX_HEAD_DIM 256  /* D                                              */
+#define DVL_MAX_BEAMS 32      /* beams in, and beams selected, per request      */
+#define DVL_MAX_STATES 8      /* state tensors of one reordering                */
+
+/* Arguments of dvl_add_rmsnorm.  Every pointer is device memory; strides are
+ * in elements of the tensor they belong to, between consecutive rows. */
+typedef struct dvl_norm {
+    int64_t rows;             /* >= 0; 0 enqueues nothing                          */
+    int32_t K;                /* row width, 1 .. DVL_MAX_K                         */
+    int32_t residual_dtype;   /* DVL_BF16 or DVL_F32: residual and residual_out    */
+    int32_t group;            /* values per scale of codes: 16, 32, 64, 128, 256,
+                                 or 0 for one scale per row                        */
+    float eps;                /* added to the mean square, >= 0                    */
+    const void *x;            /* bf16 [rows][K]                                    */
+    int64_t x_stride;
+    const void *weight;       /* bf16 [K]                                          */
+    const void *residual;     /* [rows][K], or NULL                                */
+    int64_t residual_stride;
+    void *residual_out;       /* [rows][K] (out); NULL goes with residual NULL; may
+                                 be residual itself, or x when residual is bf16    */
+    int64_t residual_out_stride;
+    void *out;                /* bf16 [rows][K] (out), or NULL                     */
+    int64_t out_stride;
+    uint8_t *codes;           /* E4M3 [rows][K] (out), or NULL                     */
+    int64_t codes_stride;
+    float *scales;            /* fp32 [rows][ceil(K / group)] contiguous (out);
+                                 with codes only                                   */
+} dvl_norm;
+
+/* Residual addition and root-mean-square norm of each row, in fp32:
+ *   u = x + residual (u = x without one);  residual_out = u rounded to its type;
+ *   y = u * weight / sqrt(mean(u^2) + eps)      (u before that rounding);
+ *   out = y rounded to bf16;
+ *   per group of a row: a = max |y|, scale = a / 448,
+ *   code = RNE_e4m3(y * (448 / a)), saturating at 448,
+ * so y ~ code * scale.  A group with a < 2^-119 has scale a / 448 and codes 0
+ * (1 / scale is no fp32 number there).  A NaN or an infinity in a row shows:
+ * the values it reaches are NaN, in scale and codes too.
+ * Any K and any strides run; rows whose tensors all start on 16-byte
+ * boundaries with K % 8 == 0 use 16-byte accesses.  No workspace.
+ * Errors: DVL_ERR_INVALID_ARG (NULL x or weight; neither out nor codes; codes
+ * without scales or the reverse; residual without residual_out or the
+ * reverse; rows, K, group, eps, dtype out of range; with more than one row a
+ * negative input stride or an output stride below K; a pointer not aligned to
+ * its element), DVL_ERR_CUDA. */
+dvl_status dvl_add_rmsnorm(const dvl_norm *args, void *stream);
+
+/* A paged key-value cache.  Strides are in elements; the D values of a head
+ * are consecutive.  Every (page, token, head) row starts on a 16-byte
+ * boundary. */
+typedef struct dvl_kv_cache {
+    int32_t dtype;            /* DVL_BF16, or DVL_FP8 (E4M3 codes, one scale each) */
+    int32_t pages;            /* pages of the pool                                 */
+    int32_t page_size;        /* tokens per page, >= 1                             */
+    int32_t heads;            /* key-value heads                                   */
+    int32_t D;                /* head width: a multiple of 16, <= DVL_MAX_HEAD_DIM */
+    int32_t reserved;         /* must be 0                                         */
+    void *k, *v;              /* [pages][page_size][heads][D]                      */
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    float k_scale, v_scale;   /* value of code 1 (DVL_FP8); 1 for bf16             */
+} dvl_kv_cache;
+
+/* Bytes of device workspace a dvl_paged_attention call with this cache, T new
+ * tokens and Hq query heads needs on the current device, whatever the batch
+ * and its lengths.  0 for arguments outside the limits or without a device.
+ * Zero it once (dvl_workspace_init); dvl_workspace_status reads its status
+ * word. */
+size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32_t Hq);
+
+/* Attention of the T newest tokens of each of B sequences over their cached
+ * keys and values (their own included: lengths counts them).  With
+ * G = Hq / heads, query head h reads cached head h / G, and token t sees
+ * n = max(0, length - (T - 1 - t)) positions:
+ *   s_j = scale * k_scale * (q . k_j),  m = max_j s_j,  j < n
+ *   out = v_scale * sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
+ *   lse = m + ln(sum_j exp(s_j - m))
+ * n = 0 gives out 0 and lse -inf.  Positions at or above n are not read into
+ * the result, whatever the cache holds there.  Products are exact, sums and
+ * softmax statistics fp32; the weights exp(s_j - m) are rounded to the
+ * matrix instruction's operand type (bf16, or f16 with an FP8 cache) before
+ * they meet V.  The result does not depend on timing: the same call on the
+ * same device gives the same bits.
+ *   q:        device bf16 [B][T][Hq][D]; strides in elements for the first
+ *             three, the last is 1; 16-byte aligned rows.
+ *   table:    device int32 [B][table_width], row stride table_stride: the
+ *             page of each page_size tokens.  Entries past a sequence's
+ *             length are not read.  An entry outside [0, pages) reads as
+ *             zeros and sets the status bit DVL_ERR_OUT_OF_RANGE.
+ *   lengths:  device int32 [B].  Below 0 counts as 0; above
+ *             table_width * page_size is cut to that, with the same bit.
+ *   out:      device bf16 [B][T][Hq][D] contiguous, 16-byte aligned.
+ *   lse:      device fp32 [B][T][Hq] contiguous, or NULL.
+ *   ws:       dvl_attention_workspace_bytes, from dvl_workspace_init.
+ * Errors: DVL_ERR_INVALID_ARG (NULL or misaligned, B or T or Hq < 1, T above
+ * DVL_MAX_QUERY, Hq not a multiple of heads, T * G above DVL_MAX_QUERY_ROWS,
+ * D not a multiple of 16 or above DVL_MAX_HEAD_DIM, page_size * table_width
+ * above 2^31 - 1, scale not finite), DVL_ERR_WORKSPACE, DVL_ERR_CUDA. */
+dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t q_batch_stride,
+                               int64_t q_token_stride, int64_t q_head_stride, int32_t B, int32_t T,
+                               int32_t Hq, const int32_t *table, int64_t table_stride,
+                               int32_t table_width, const int32_t *lengths, float scale, void *out,
+                               float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Bytes of device workspace a dvl_beam_select call needs; 0 for arguments
+ * outside the limits.  Zero it once (dvl_workspace_init); every call leaves
+ * it as it found it. */
+size_t dvl_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t N);
+
+/* Beam search's choice of the next beams.  For request b, beam j and row n of
+ * the head:
+ *   score(j, n) = scores[b][j] + (logits[b][j][n] - lse(b, j)),
+ *   lse(b, j) = ln sum_n exp(logits[b][j][n])        (in fp32),
+ * and the k best candidates of the request, best first.  Equal scores: the
+ * lower beam first; within a beam the larger logit, then the lower row.  A
+ * score of -inf or NaN is no candidate (a dead beam's -inf score, a banned
+ * row's -inf logit; a beam whose logits hold a NaN or +inf, or nothing but
+ * -inf, has none).  Slots left over get score -inf, parent -1, token -1.
+ *   logits:     device [batch][beams][N], dtype DVL_BF16 or DVL_F32, rows
+ *               contiguous, batch and beam strides in elements, aligned to
+ *               the element.
+ *   scores:     device fp32 [batch][beams] contiguous.
+ *   batch:      >= 0 (0 enqueues nothing).  beams, k: 1 .. DVL_MAX_BEAMS.
+ *   N:          1 .. 2^31 - 65,536.
+ *   d2t:        device int32 [N], or NULL (token = n).
+ *   out_scores: device fp32 [batch][k], parents and tokens: device int32
+ *               [batch][k] (out).
+ *   ws:         dvl_beam_workspace_bytes(batch, beams, N) bytes, from
+ *               dvl_workspace_init.
+ * Errors: DVL_ERR_INVALID_ARG, DVL_ERR_WORKSPACE, DVL_ERR_CUDA. */
+dvl_status dvl_beam_select(const void *logits, int32_t dtype, int64_t batch_stride,
+                           int64_t beam_stride, const float *scores, int32_t batch, int32_t beams,
+                           int32_t N, int32_t k, const int32_t *d2t, float *out_scores,
+                           int32_t *parents, int32_t *tokens, void *ws, size_t ws_bytes,
+                           void *stream);
+
+/* One tensor of per-beam rows: src [batch][beams] rows, dst [batch][k] rows,
+ * each row row_bytes consecutive bytes.  src and dst do not overlap. */
+typedef struct dvl_state {
+    const void *src;
+    void *dst;
+    int64_t row_bytes;  /* >= 1 */
+    int64_t src_stride; /* bytes from one beam's row to the next (beams * src_stride per request) */
+    int64_t dst_stride;
+} dvl_state;
+
+/* The page tables of beams that share a paged cache. */
+typedef struct dvl_beam_pages {
+    const int32_t *table;   /* [batch][beams][width] contiguous                   */
+    int32_t *table_out;     /* [batch][k][width] contiguous (out)                 */
+    const int32_t *lengths; /* [batch][beams]: cached tokens of each beam         */
+    int32_t *lengths_out;   /* [batch][k] (out)                                   */
+    const int32_t *spare;   /* [batch][k]: a page of the pool for each new beam,
+                               each different and in no table                     */
+    int32_t width;
+    int32_t reserved;       /* must be 0                                          */
+} dvl_beam_pages;
+
+/* Reorder what belongs to a beam after a selection: new beam i of request b
+ * takes the rows of its parent,
+ *   dst[b][i] = src[b][parents[b][i]]   for every state,
+ * and zeros where the parent is outside [0, beams) (an unused slot).  With
+ * pages, table_out and lengths_out take the parent's rows the same way, and
+ * the new beam gets a page of its own for the token it will append: with
+ * L = the parent's length, s = L / page_size and r = L % page_size, page
+ * spare[b][i] receives the first r tokens of the parent's page s (keys and
+ * values) and table_out[b][i][s] = spare[b][i] (when s < width).  Full pages
+ * stay shared.  One launch.
+ *   states:  HOST array of n_states (0 .. DVL_MAX_STATES), device pointers.
+ *   pages:   HOST struct, or NULL; cache goes with it.
+ *   parents: device int32 [batch][k].
+ *   batch:   >= 0 (0 enqueues nothing).  beams, k: 1 .. DVL_MAX_BEAMS.
+ * A page id outside the pool (a parent's or a spare one) copies nothing.
+ * Outputs may not overlap inputs: the rows are copied in no order.
+ * Errors: DVL_ERR_INVALID_ARG, DVL_ERR_CUDA. */
+dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl_beam_pages *pages,
+                            const dvl_kv_cache *cache, const int32_t *parents, int32_t batch,
+                            int32_t beams, int32_t k, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Load time                                                              */
 /* ---------------------------------------------------------------------- */
 
