@@ -8,30 +8,45 @@
 // time.  The rows of one cached head share every load: they are the M rows
 // of the matrix products (16 per MMA).
 //
-// Work split.  The unit is a tile of 64 tokens of one (sequence, cached
-// head); all units in a row (by sequence, head, tile) are cut into one equal
-// share per block of a grid that is resident at once, so unequal lengths
-// balance by themselves and the host needs to know none of them.  A block
-// walks its share through a ring of tiles in shared memory, filled by
-// 16-byte asynchronous copies that run ahead across sequence boundaries.  A
-// (sequence, head) that lies in one share is finished by its block; the
-// parts of one that was cut go to the workspace as (unnormalised sums,
-// maximum, sum of weights), and the join kernel adds them in order of the
-// shares, so the result does not depend on timing.
+// Work split.  The unit is a tile of TOK G tokens of one (sequence, cached
+// head).  The blocks of a grid that is resident at once form lanes, one per
+// head of a set of up to eight; a lane's units in a row (by sequence, set,
+// tile) are cut into one equal share per block, so unequal lengths balance by
+// themselves and the host needs to know none of them, and the blocks of one
+// share index walk the same tokens of neighbouring heads at the same time
+// (in the usual layout the heads of a token are neighbours in memory: 64
+// sequences of up to 16,381 tokens, 8 FP8 heads of 64, all lanes apart: 195
+// us; heads first in memory: 131).  A block walks its share through a ring of
+// chunks in shared memory, filled by 16-byte asynchronous copies that run
+// ahead across sequence boundaries.
 //
-// One tile, four warps:
-//   1. scores: warp w takes tokens 16 w .. 16 w + 15 against all rows;
-//   2. the warps' row maxima meet in shared memory (barrier), every thread
-//      keeps the running maximum of its rows and scales sums by 2^(old-new);
-//   3. the weights go to shared memory in the MMA operand type (barrier): a
-//      16-bit weight is the tensor cores' operand; its rounding (2^-9
-//      relative for bf16, 2^-12 for f16) is random per position and averages
-//      over the positions that matter, while the sums stay fp32;
-//   4. values: warp w takes columns D / 4 w .. of V for all 64 tokens, so
-//      the output sums of a row are spread over the block and never have to
-//      be added across warps.
-// Scores are kept in units of log2 (the scale carries log2 e), so a weight
-// is one ex2.
+// Joining.  A (sequence, head) that lies in one share is finished by its
+// block.  The parts of one that was cut go to the workspace as
+// (unnormalised sums, maximum, sum of weights); the last block of every
+// kJoin consecutive parts (by a wrapping ticket, as in the reducing
+// kernels) adds them in order of the shares, and where there are more, the
+// last of those adds the groups' sums, so the result does not depend on
+// timing and no second launch is needed.
+//
+// Warps.  A group of warps (one per 16 query rows) owns TOK consecutive tokens
+// of every tile: it finds their pages, copies their rows, and runs its own
+// softmax over them -- running maximum, sum and output rows stay in
+// registers, the weights go from the score accumulators straight into the
+// operand registers of the second product -- so no warp waits for another
+// within a (sequence, head); the groups' results meet in shared memory at its
+// end.  (Sharing a tile across the block, each warp with a slice of the
+// columns, took three block barriers per tile.)  The group's ring holds keys
+// and values of P + 1 chunks less one entry, keys and values as entries of
+// their own: the next chunk's keys load while this chunk's scores are formed,
+// its values while the values are used, which keeps P chunks per group in
+// flight in the least shared memory, hence the most warps per SM.
+// Up to 8 query rows (RT = 0) the upper half of every MMA is padding: its
+// softmax is left out and its accumulators are not kept.
+//
+// Weights are rounded to the MMA operand type: 2^-9 relative for bf16, 2^-12
+// for f16, independent per position, so it averages out over the positions
+// that matter; sums and statistics stay fp32.  Scores are kept in units of
+// log2 (the scale carries log2 e), so a weight is one ex2.
 //
 // Operands.  bf16 cache: mma m16n8k16 bf16, K and V by ldmatrix (V
 // transposed).  FP8 cache: E4M3 pairs are widened to f16 (exact) in
@@ -46,9 +61,10 @@
 // Masks.  Row t sees n = length - (T - 1 - t) positions.  Scores at or past
 // n are replaced, not added to, so nothing a masked key holds can show; a
 // row without positions keeps the sum 0 and gives 0.  Positions that only
-// some rows see (the last T - 1) stay out of the V tile (zeros there) and
-// are added value by value for the rows that see them: 0 times a NaN or an
-// infinity in V would otherwise reach the rows that do not.
+// some rows see (the last T - 1) are added value by value for the rows that
+// see them, and their V rows zeroed before the MMA: 0 times a NaN or an
+// infinity in V would otherwise reach the rows that do not.  Rows past the
+// length are zeros from the copy.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -60,9 +76,8 @@
 namespace dvl {
 namespace attn {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kJoin = 32;  // parts joined at once; its square bounds the shares
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -106,6 +121,18 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr)
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint16_t lds8(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
 __device__ __forceinline__ uint16_t lds16(uint32_t addr)
 {
     uint16_t v;
@@ -130,6 +157,21 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same where only rows g (NJ = 1) or rows g and g + 8 are kept.
+template <bool F16, int NJ>
+__device__ __forceinline__ void mma_rows(float (&o)[2 * NJ], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1)
+{
+    float c[4] = {o[0], o[1], NJ == 2 ? o[2 * NJ - 2] : 0.f, NJ == 2 ? o[2 * NJ - 1] : 0.f};
+    mma16<F16>(c, a, b0, b1);
+    o[0] = c[0];
+    o[1] = c[1];
+    if constexpr (NJ == 2) {
+        o[2] = c[2];
+        o[3] = c[3];
+    }
+}
+
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -152,12 +194,21 @@ __device__ __forceinline__ float unpack1(uint16_t x)
     }
 }
 
-// Two E4M3 bytes -> two f16 (exact).
+// Two E4M3 bytes -> two f16 (exact); four bytes -> two such pairs.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t x)
 {
     uint32_t r;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
     return r;
+}
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    asm("{\n\t.reg .b16 l, h;\n\t"
+        "mov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(x));
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -167,234 +218,435 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Cached tokens of sequence b, cut to what its table row can name.
-__device__ __forceinline__ int seq_len(const AttnArgs &a, int b)
-{
-    const int n = a.lengths[b];
-    return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
-}
-__device__ __forceinline__ int seq_tiles(const AttnArgs &a, int b)
-{
-    return (seq_len(a, b) + kTile - 1) / kTile;
-}
-
-// Walks the units from (b, h, t) on.
+// Walks a lane's units from (sequence b, head h, tile t) on.
+template <int TILE>
 struct Cursor {
     int b, h, t, len, tiles;
     __device__ __forceinline__ void next(const AttnArgs &a)
     {
-        if (++t < tiles)
+        if (b >= a.B || ++t < tiles)
             return;
         t = 0;
-        if (++h < a.heads)
+        h += a.lanes;
+        if (h < a.heads)
             return;
-        h = 0;
+        h %= a.lanes;
         do {
             if (++b >= a.B)
-                return;  // past the last unit: never loaded
+                return;  // past the last unit
             len = seq_len(a, b);
         } while (len == 0);
-        tiles = (len + kTile - 1) / kTile;
+        tiles = (len + TILE - 1) / TILE;
     }
 };
 
-template <int DP, bool FP8, int MT, int STAGES>
+// DP: head width padded to 64, 128 or 256.  RT: 16-row tiles of query rows; 0
+// for at most 8 rows.  TOK: tokens per group and tile.  P: chunks in flight.
+// G: groups, so G TOK tokens per tile.
+constexpr int max_of(int x, int y) { return x > y ? x : y; }
+
+template <int DP, bool FP8, int RT, int TOK, int P, int G>
 struct Shape {
     static constexpr int kElem = FP8 ? 1 : 2;
-    // Pitches keep the rows that one access phase touches on distinct banks:
-    // ldmatrix (8 rows of 16 bytes), 8-byte loads of 4 rows, 4-byte loads of
-    // every other row.
-    static constexpr int kKPitch = FP8 ? DP + 32 : DP * 2 + 16;
-    static constexpr int kVPitch = FP8 ? DP + 16 : DP * 2 + 16;
+    static constexpr int kTile = TOK * G;
+    static constexpr int kGroup = RT == 0 ? 32 : 32 * RT;  // threads
+    static constexpr int kThreads = kGroup * G;
+    // Rows that one access phase touches lie on distinct banks.  bf16: the
+    // 16-byte units of a row are permuted by its lowest three bits (8 rows of
+    // an ldmatrix).  FP8: padded pitches (8-byte loads of 4 rows for K, 4-byte
+    // loads of every other row for V).
+    static constexpr int kKPitch = FP8 ? DP + 32 : DP * 2;
+    static constexpr int kVPitch = FP8 ? DP + 16 : DP * 2;
     static constexpr int kQPitch = DP * 2 + 16;
-    static constexpr int kPPitch = kTile * 2 + 16;
-    static constexpr int kRows = 16 * MT;
-    static constexpr int kStage = kTile * (kKPitch + kVPitch);
-    static constexpr int kQ = STAGES * kStage;
-    static constexpr int kP = kQ + kRows * kQPitch;
-    static constexpr int kRed = kP + kRows * kPPitch;              // float[kWarps][kRows]
-    static constexpr int kSum = kRed + kWarps * kRows * 4;         // float[kWarps][kRows]
-    static constexpr int kScale = kSum + kWarps * kRows * 4;       // float[kRows]
-    static constexpr int kBytes = kScale + kRows * 4;
+    static constexpr int kRows = RT == 0 ? 8 : 16 * RT;    // query rows kept
+    static constexpr int kQRows = RT == 0 ? 16 : 16 * RT;  // rows of the operand
+    static constexpr int kMPitch = DP + 4;                 // floats per merged row
+    static constexpr int kEntry = TOK * kKPitch;           // one ring entry
+    static constexpr int kEntries = 2 * P + 1;
+    static constexpr int kRing = kEntries * kEntry;        // per group
+    static constexpr int kQ = G * kRing;                   // Q; the merged rows at a pair's end
+    static constexpr int kJoinBytes = 2 * (kJoin + 1) * kRows * 4;  // weights of a join
+    static constexpr int kQBytes =
+        max_of(kQRows * kQPitch, max_of(kRows * kMPitch * 4, kJoinBytes));
+    static constexpr int kStat = kQ + kQBytes;             // float2[G][kRows]: maximum, sum
+    static constexpr int kScale = kStat + G * kRows * 8;   // float[kQRows]
+    static constexpr int kAddr = kScale + kQRows * 4;      // pointers [G][P + 1][2][TOK]
+    static constexpr int kBytes = kAddr + G * (P + 1) * 2 * TOK * 8;
 };
 
-// Copy tile `it` into a ring stage.
-template <int DP, bool FP8>
-__device__ __forceinline__ void load_tile(const AttnArgs &a, const Cursor &it, uint32_t k_smem,
-                                          uint32_t v_smem, int k_pitch, int v_pitch)
-{
-    constexpr int kElem = FP8 ? 1 : 2;
-    constexpr int kCols = DP * kElem / 16;       // 16-byte units of a padded row
-    constexpr int kStep = kThreads / kCols;      // rows per pass
-    const int col = threadIdx.x % kCols;
-    if (col * 16 >= a.D * kElem)
-        return;
-    const int32_t *table = a.table + it.b * a.table_stride;
-    const int whole = it.len - (a.T - 1);        // positions every row sees
-#pragma unroll
-    for (int i = 0; i < kTile / kStep; ++i) {
-        const int r = (int)threadIdx.x / kCols + i * kStep;
-        const int pos = it.t * kTile + r;
-        bool valid = pos < it.len;
-        const int page = valid ? a.page_of(pos) : 0;
-        const int id = valid ? __ldg(table + page) : 0;
-        if ((unsigned)id >= (unsigned)a.pages) {
-            valid = false;
-            set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
-        }
-        const int64_t slot = pos - (int64_t)page * a.page_size;
-        const unsigned char *k = a.k, *v = a.v;
-        if (valid) {
-            k += id * a.kp + slot * a.kt + it.h * a.kh + col * 16;
-            v += id * a.vp + slot * a.vt + it.h * a.vh + col * 16;
-        }
-        cp_async16(k_smem + r * k_pitch + col * 16, k, valid);
-        cp_async16(v_smem + r * v_pitch + col * 16, v, valid && pos < whole);
-    }
-}
-
-// One cached value of V at (position, column), for the positions only some
-// rows see.
+// The output column of accumulator e (of a row) of column tile n.
 template <bool FP8>
-__device__ __forceinline__ float value_at(const AttnArgs &a, int b, int h, int pos, int d)
+__device__ __forceinline__ int out_col(int n, int c, int e)
 {
-    const int page = a.page_of(pos);
-    const int id = a.table[b * a.table_stride + page];
-    if ((unsigned)id >= (unsigned)a.pages)
-        return 0.f;
-    const unsigned char *p =
-        a.v + id * a.vp + (pos - (int64_t)page * a.page_size) * a.vt + h * a.vh;
-    if constexpr (FP8)
-        return unpack1<true>((uint16_t)(e4m3x2_f16x2(p[d]) & 0xffffu));
-    else
-        return unpack1<false>(reinterpret_cast<const uint16_t *>(p)[d]);
+    return FP8 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
 }
 
-// The block's first unit: the sequence that holds unit u0 and u0's place in
-// it, and the number of units in all.  Every thread calls it.
-__device__ __forceinline__ int64_t locate(const AttnArgs &a, int *s_b, int64_t *s_off,
-                                          int64_t *s_warp, int64_t *u0, int64_t *u1)
-{
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t total = 0;
-    for (int b = threadIdx.x; b < a.B; b += kThreads) {
-        if (a.lengths[b] > a.max_len)
-            set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
-        total += seq_tiles(a, b);
+// Where a token's row starts, found by one thread per token a chunk before the
+// copies need it: the page id is read from the table one chunk earlier still,
+// so no copy waits for the table.
+struct RowAddress {
+    uint32_t k, v;  // byte offsets within the page
+    int id;         // page id, not yet checked
+    bool has;       // a cached token
+
+    template <int TILE>
+    __device__ __forceinline__ void fetch(const AttnArgs &a, const Cursor<TILE> &it, int r)
+    {
+        const int pos = it.t * TILE + r;
+        has = it.b < a.B && pos < it.len;
+        if (!has)
+            return;
+        const int page = a.page_of(pos);
+        id = __ldg(a.table + it.b * a.table_stride + page);
+        const uint32_t slot = pos - page * a.page_size;
+        k = slot * a.kt + it.h * a.kh;
+        v = slot * a.vt + it.h * a.vh;
     }
+    // The row's addresses.  A page outside the pool is reported, and read as
+    // page 0; past the length nothing is read through the address.
+    __device__ __forceinline__ void resolve(const AttnArgs &a, const unsigned char **rows,
+                                            int tok) const
+    {
+        const unsigned char *pk = a.k, *pv = a.v;
+        if (has) {
+            int page = id;
+            if ((unsigned)page >= (unsigned)a.pages) {
+                set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
+                page = 0;
+            }
+            pk += page * a.kp + k;
+            pv += page * a.vp + v;
+        }
+        rows[0] = pk;
+        rows[tok] = pv;
+    }
+};
+
+// Copy a chunk's rows (keys or values) into a ring entry, `live` of them; the
+// others become zeros.  at: the thread's place among the group's N threads.
+template <int DP, bool FP8, int TOK, int N>
+__device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *const *rows, int live,
+                                          int at, uint32_t dst, int pitch)
+{
+    constexpr int kCols = DP * (FP8 ? 1 : 2) / 16;  // 16-byte units of a padded row
+    constexpr int kStep = N / kCols;                // rows per pass
+    const int col = at % kCols, r0 = at / kCols;
+    if (col * 16 >= row_bytes || r0 >= TOK)
+        return;
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        total += __shfl_xor_sync(kFull, total, off);
-    if (lane == 0)
-        s_warp[warp] = total;
-    __syncthreads();
-    total = 0;
+    for (int i = 0; i < (kStep < TOK ? TOK / kStep : 1); ++i) {
+        const int r = r0 + i * kStep;
+        const int unit = FP8 ? col : col ^ (r & 7);
+        cp_async16(dst + r * pitch + unit * 16, rows[r] + col * 16, r < live);
+    }
+}
+
+// Barrier of one group's N threads.
+template <int N>
+__device__ __forceinline__ void group_sync(int group)
+{
+    if constexpr (N == 32)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(N) : "memory");
+}
+
+// A block's share of its lane: units [u0, u1) of `units`, cut into `shares`,
+// and the sequence that holds unit u0 with u0's place in it.
+struct Share {
+    int64_t u0, u1, units;
+    int shares, b;
+    int64_t off;
+};
+
+// floor(i n / d) for i <= d < 2^10.
+__device__ __forceinline__ int64_t cut(int64_t n, int i, int d)
+{
+    if (n >> 22 == 0)
+        return (uint32_t)n * (uint32_t)i / (uint32_t)d;
+    return n * i / d;
+}
+
+// The share that holds unit u.
+__device__ __forceinline__ int holder(int64_t u, int64_t units, int shares)
+{
+    const int64_t x = (u + 1) * shares - 1;
+    return x >> 32 == 0 && units >> 32 == 0 ? (int)((uint32_t)x / (uint32_t)units)
+                                            : (int)(x / units);
+}
+
+// Every thread calls it; scratch: 16 + 8 THREADS / 32 bytes.
+template <int THREADS, int TILE>
+__device__ __forceinline__ Share locate(const AttnArgs &a, int64_t *scratch)
+{
+    constexpr int kW = THREADS / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sets = a.heads / a.lanes;
+    int64_t *s_off = scratch, *s_b = scratch + 1, *s_warp = scratch + 2;
+    Share s;
+    int64_t total = 0;
+    if (a.B > THREADS) {  // the units of all sequences, before the scan by parts
+        for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+            const int b = b0 + (int)threadIdx.x;
+            // at most 2^26 tiles per sequence
+            total += __reduce_add_sync(kFull, b < a.B ? (unsigned)seq_tiles<TILE>(a, b) : 0u);
+        }
+        if (lane == 0)
+            s_warp[warp] = total;
+        __syncthreads();
+        total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w)
-        total += s_warp[w];
-    const int64_t units = total * a.heads;
-    const int64_t blocks = used_blocks(a.blocks, units);
-    *u0 = blockIdx.x * units / (blocks > 0 ? blocks : 1);
-    *u1 = blockIdx.x < blocks ? (blockIdx.x + 1ll) * units / blocks : *u0;
+        for (int w = 0; w < kW; ++w)
+            total += s_warp[w];
+        __syncthreads();
+    }
+    s.shares = 0;
     int64_t carry = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + threadIdx.x;
-        const int64_t mine = b < a.B ? seq_tiles(a, b) : 0;
-        int64_t scan = mine;
+    for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+        const int b = b0 + (int)threadIdx.x;
+        const unsigned mine = b < a.B ? (unsigned)seq_tiles<TILE>(a, b) : 0u;
+        unsigned scan = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t o = __shfl_up_sync(kFull, scan, off);
+            const unsigned o = __shfl_up_sync(kFull, scan, off);
             if (lane >= off)
                 scan += o;
         }
-        __syncthreads();
         if (lane == 31)
             s_warp[warp] = scan;
         __syncthreads();
-        for (int w = 0; w < warp; ++w)
-            scan += s_warp[w];
-        const int64_t end = (carry + scan) * a.heads, begin = end - mine * a.heads;
-        if (begin <= *u0 && *u0 < end) {
-            *s_b = b;
-            *s_off = *u0 - begin;
-        }
-        for (int w = 0; w < kWarps; ++w)
+        int64_t end = carry + scan;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            if (w < warp)
+                end += s_warp[w];
             carry += s_warp[w];
+        }
+        if (s.shares == 0) {
+            s.units = (a.B > THREADS ? total : carry) * sets;
+            s.shares = used_shares(a, s.units);
+            const int share = (int)blockIdx.x / a.lanes;
+            s.u0 = s.u1 = 0;
+            if (share < s.shares) {
+                s.u0 = cut(s.units, share, s.shares);
+                s.u1 = cut(s.units, share + 1, s.shares);
+            }
+        }
+        end *= sets;
+        const int64_t begin = end - (int64_t)mine * sets;
+        if (begin <= s.u0 && s.u0 < end) {
+            *s_b = b;
+            *s_off = s.u0 - begin;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    return units;
+    s.b = (int)*s_b;
+    s.off = *s_off;
+    return s;
 }
 
-template <int DP, bool FP8, int MT, int STAGES>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_constant__ AttnArgs a)
+// Sequences without tokens: zeros, written by whichever block their index names.
+template <int THREADS>
+__device__ __forceinline__ void write_empty(const AttnArgs &a)
 {
-    using S = Shape<DP, FP8, MT, STAGES>;
-    constexpr int kCols = DP / 4;        // output columns per warp
-    constexpr int kNT = kCols / 8;       // MMA column tiles per warp
-    constexpr int kJ = kNT < 4 ? kNT : 4;  // FP8: column tiles that share a V load
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (threadIdx.x == 0 && a.lengths[b] > a.max_len)
+            set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
+        if (seq_len(a, b) != 0)
+            continue;
+        const int64_t n = (int64_t)a.T * a.Hq;
+        for (int64_t i = threadIdx.x; i < n * a.D / 8; i += THREADS)
+            reinterpret_cast<uint4 *>(a.out + b * n * a.D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse)
+            for (int64_t i = threadIdx.x; i < n; i += THREADS)
+                a.lse[b * n + i] = kNegInf;
+    }
+}
+
+// Add n parts (slots[i] of the workspace) in order.  With `last` the result
+// is the (sequence, head)'s output, else it replaces the first part.
+// scratch: 2 (kJoin + 1) rows floats.  Every thread calls it.
+template <int THREADS>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, int second,
+                                           int stride, bool last, int b, int h, float *scratch)
+{
+    // part i: slot `first` for i = 0, then second, second + stride, ..
+    auto part = [&](int i) {
+        return a.parts + (int64_t)(i == 0 ? first : second + (i - 1) * stride) * a.part_floats;
+    };
+    const int stats = a.rows * a.D;
+    float *weight = scratch, *sums = scratch + kJoin * a.rows;  // [n][rows] each
+    float2 *total = reinterpret_cast<float2 *>(scratch + 2 * kJoin * a.rows);
+    for (int i0 = threadIdx.x; i0 < n * a.rows; i0 += THREADS) {
+        const int i = i0 / a.rows, r = i0 - i * a.rows;
+        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(i) + stats) + r);
+        weight[i0] = ml.x;
+        sums[i0] = ml.y;
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < a.rows; r += THREADS) {
+        float m = kNegInf;
+        for (int i = 0; i < n; ++i)
+            m = fmaxf(m, weight[i * a.rows + r]);
+        const float ref = m == kNegInf ? 0.f : m;
+        float sum = 0.f;
+        for (int i = 0; i < n; ++i) {
+            const float w = ex2(weight[i * a.rows + r] - ref);
+            weight[i * a.rows + r] = w;
+            sum += sums[i * a.rows + r] * w;
+        }
+        total[r] = make_float2(m, sum);
+    }
+    __syncthreads();
+    const int cols = a.D / 4;
+    for (int i0 = threadIdx.x; i0 < a.rows * cols; i0 += THREADS) {
+        const int r = i0 / cols, d = 4 * (i0 - r * cols);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float w = weight[i * a.rows + r];
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(i) + r * a.D + d));
+            acc.x = fmaf(w, x.x, acc.x);
+            acc.y = fmaf(w, x.y, acc.y);
+            acc.z = fmaf(w, x.z, acc.z);
+            acc.w = fmaf(w, x.w, acc.w);
+        }
+        const float m = total[r].x, sum = total[r].y;
+        if (last) {
+            const int t = r / a.G;
+            const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
+            // a row without positions (or of -inf scores only): 0
+            const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+            *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
+                make_uint2(pack2<false>(acc.x * inv, acc.y * inv),
+                           pack2<false>(acc.z * inv, acc.w * inv));
+            if (a.lse && d == 0)
+                a.lse[to] = log_sum(m, sum);
+        } else {
+            *reinterpret_cast<float4 *>(part(0) + r * a.D + d) = acc;
+            if (d == 0)
+                reinterpret_cast<float2 *>(part(0) + stats)[r] = make_float2(m, sum);
+        }
+    }
+    __syncthreads();
+}
+
+template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
+__global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCKS)
+    attention_kernel(const __grid_constant__ AttnArgs a)
+{
+    using S = Shape<DP, FP8, RT, TOK, P, G>;
+    constexpr int kThreads = S::kThreads;
+    constexpr int kGroup = S::kGroup;
+    constexpr int kWarps = kThreads / 32;
+    constexpr int NJ = RT == 0 ? 1 : 2;  // row halves kept per MMA (rows g, g + 8)
+    constexpr int kNT = DP / 8;          // MMA column tiles of the output
+    constexpr int kSN = TOK / 8;         // MMA column tiles of the scores
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_b;
-    __shared__ int64_t s_off, s_warp[kWarps];
+    __shared__ int64_t s_scan[2 + kWarps];
+    __shared__ int s_last;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = threadIdx.x / kGroup, at = threadIdx.x % kGroup;  // place in the group
+    const int mt = at / 32;                                             // row tile
     const int g = lane >> 2, c = lane & 3;
     const uint32_t base = smem_u32(smem);
-    float *red = reinterpret_cast<float *>(smem + S::kRed);
-    float *sums = reinterpret_cast<float *>(smem + S::kSum);
+    float2 *stat = reinterpret_cast<float2 *>(smem + S::kStat);
     float *row_scale = reinterpret_cast<float *>(smem + S::kScale);
+    float *merged = reinterpret_cast<float *>(smem + S::kQ);
 
-    int64_t u0, u1;
-    locate(a, &s_b, &s_off, s_warp, &u0, &u1);
-    if (u0 >= u1)
+    const Share share = locate<kThreads, S::kTile>(a, s_scan);
+    if (share.u0 >= share.u1) {
+        write_empty<kThreads>(a);
         return;
-    Cursor cur;
-    cur.b = s_b;
+    }
+    Cursor<S::kTile> cur;
+    cur.b = share.b;
     cur.len = seq_len(a, cur.b);
-    cur.tiles = (cur.len + kTile - 1) / kTile;
-    cur.h = (int)(s_off / cur.tiles);
-    cur.t = (int)(s_off - (int64_t)cur.h * cur.tiles);
-    const int64_t n_units = u1 - u0;
+    cur.tiles = (cur.len + S::kTile - 1) / S::kTile;
+    const int set = a.heads == a.lanes ? 0 : (int)(share.off / cur.tiles);
+    cur.h = set * a.lanes + blockIdx.x % a.lanes;
+    cur.t = (int)(share.off - (int64_t)set * cur.tiles);
+    const int64_t n_units = share.u1 - share.u0;
 
     // Padding columns of K meet zeros of Q: they must hold no NaN.
-    if (a.D < DP)
+    if (a.D < DP) {
         for (int i = threadIdx.x * 16; i < S::kQ; i += kThreads * 16)
             *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+        __syncthreads();
+    }
 
-    Cursor ahead = cur;
-    int64_t loaded = 0;
-    auto load_next = [&]() {
-        if (loaded < n_units) {
-            const uint32_t st = base + (uint32_t)(loaded % STAGES) * S::kStage;
-            load_tile<DP, FP8>(a, ahead, st, st + kTile * S::kKPitch, S::kKPitch, S::kVPitch);
+    // Row addresses are known P + 1 chunks ahead of the chunk in work, page
+    // ids one more.
+    const unsigned char **addr = reinterpret_cast<const unsigned char **>(smem + S::kAddr) +
+                                 group * (P + 1) * 2 * TOK;
+    const uint32_t ring = base + group * S::kRing;
+    const int row_bytes = a.D * S::kElem;
+    RowAddress row;
+    Cursor<S::kTile> ahead = cur;  // of the row addresses
+    Cursor<S::kTile> load = cur;   // of the copies
+    const bool finds = at < TOK;
+    if (finds) {
+        RowAddress first[P + 1];
+#pragma unroll
+        for (int i = 0; i < P + 1; ++i) {
+            first[i].fetch(a, ahead, TOK * group + at);
             ahead.next(a);
         }
-        ++loaded;
+        row.fetch(a, ahead, TOK * group + at);
+        ahead.next(a);
+#pragma unroll
+        for (int i = 0; i < P + 1; ++i)
+            first[i].resolve(a, addr + i * 2 * TOK + at, TOK);
+    }
+    group_sync<kGroup>(group);
+    int64_t to_load = n_units;
+    int load_slot = 0, load_entry = 0;  // of addr, of the ring
+    auto load_keys = [&]() {
+        if (to_load > 0)
+            load_rows<DP, FP8, TOK, kGroup>(row_bytes, addr + load_slot * 2 * TOK,
+                                            load.len - load.t * S::kTile - TOK * group, at,
+                                            ring + load_entry * S::kEntry, S::kKPitch);
         cp_async_commit();
+        load_entry = load_entry + 1 == S::kEntries ? 0 : load_entry + 1;
+    };
+    auto load_values = [&]() {
+        if (to_load > 0)
+            load_rows<DP, FP8, TOK, kGroup>(row_bytes, addr + load_slot * 2 * TOK + TOK,
+                                            load.len - load.t * S::kTile - TOK * group, at,
+                                            ring + load_entry * S::kEntry, S::kVPitch);
+        cp_async_commit();
+        load_entry = load_entry + 1 == S::kEntries ? 0 : load_entry + 1;
+        load_slot = load_slot + 1 == P + 1 ? 0 : load_slot + 1;
+        --to_load;
+        load.next(a);
     };
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i)
-        load_next();
+    for (int i = 0; i < P; ++i) {
+        load_keys();
+        load_values();
+    }
 
-    float o[MT][kNT][4];
-    float m[MT][2], l[MT][2];
-    int sees[MT][2];
+    float o[kNT][2 * NJ];
+    float m[NJ], l[NJ];
+    int sees[NJ], sees_least = 0;
     bool fresh = true;       // the next tile starts a (sequence, head)
     bool first_part = true;  // still in the block's first (sequence, head)
     int t_first = 0;
-    for (int64_t i = 0; i < n_units; ++i) {
+    int entry = 0;
+    for (int64_t left = n_units; left > 0; --left) {
         if (fresh) {
             fresh = false;
             t_first = cur.t;
             // Q of this (sequence, cached head): row t * G + g
-            for (int r = warp; r < S::kRows; r += kWarps) {
+            for (int r = warp; r < S::kQRows; r += kWarps) {
                 const int t = r / a.G;
                 const uint16_t *q = a.q + cur.b * a.qb + t * a.qt +
                                     (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh;
                 unsigned char *dst = smem + S::kQ + r * S::kQPitch;
                 if constexpr (FP8) {
-                    constexpr int kPer = DP / 32 < 2 ? 2 : DP / 32;  // values per lane
+                    constexpr int kPer = DP / 32;  // values per lane
                     float v[kPer];
                     uint32_t big = 0u;
 #pragma unroll
@@ -409,16 +661,13 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
                     const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
 #pragma unroll
                     for (int e = 0; e < kPer; ++e) {
+                        // place of d in the permuted order: block of 32, lane
+                        // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
                         const int d = lane + 32 * e;
-                        if (d < DP) {
-                            // place of d in the permuted order: block of 32,
-                            // lane quarter (d / 8 % 4), step (d / 4 % 2),
-                            // half (d / 2 % 2)
-                            const int p = (d & ~31) + ((d >> 2) & 1) * 16 + ((d >> 1) & 1) * 8 +
-                                          ((d >> 3) & 3) * 2 + (d & 1);
-                            reinterpret_cast<uint16_t *>(dst)[p] =
-                                (uint16_t)(pack2<true>(v[e] * up, 0.f) & 0xffffu);
-                        }
+                        const int p = (d & ~31) + ((d >> 2) & 1) * 16 + ((d >> 1) & 1) * 8 +
+                                      ((d >> 3) & 3) * 2 + (d & 1);
+                        reinterpret_cast<uint16_t *>(dst)[p] =
+                            (uint16_t)(pack2<true>(v[e] * up, 0.f) & 0xffffu);
                     }
                     if (lane == 0)
                         row_scale[r] = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
@@ -431,312 +680,351 @@ __global__ void __launch_bounds__(kThreads) attention_kernel(const __grid_consta
                 }
             }
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = 16 * mt + 8 * j + g;
-                    sees[mt][j] = r < a.rows ? cur.len - (a.T - 1 - r / a.G) : 0;
-                    m[mt][j] = kNegInf;
-                    l[mt][j] = 0.f;
-                }
-#pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        o[mt][n][e] = 0.f;
+            for (int j = 0; j < NJ; ++j) {
+                const int r = 16 * mt + 8 * j + g;
+                sees[j] = r < a.rows ? cur.len - (a.T - 1 - r / a.G) : 0;
+                m[j] = kNegInf;
+                l[j] = 0.f;
             }
+            sees_least = cur.len - (a.T - 1);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2 * NJ; ++e)
+                    o[n][e] = 0.f;
+            __syncthreads();
         }
-        cp_async_wait<STAGES - 2>();
-        __syncthreads();
-        load_next();  // into the stage the previous tile used
+        const int pos0 = cur.t * S::kTile + TOK * group;
 
-        const uint32_t k_smem = base + (uint32_t)(i % STAGES) * S::kStage;
-        const uint32_t v_smem = k_smem + kTile * S::kKPitch;
-        const int pos0 = cur.t * kTile;
-
-        // 1. scores of this warp's 16 tokens
-        float s[MT][2][4];
+        // keys
+        cp_async_wait<2 * P - 1>();
+        group_sync<kGroup>(group);
+        load_keys();  // into the entry of the previous values
+        const uint32_t k_smem = ring + entry * S::kEntry;
+        entry = entry + 1 == S::kEntries ? 0 : entry + 1;
+        uint32_t pa[TOK / 16][4];  // the weights as the second product's operand
+        float s[kSN][2 * NJ];
+        if (pos0 < cur.len) {
+            // scores
+            float acc[kSN][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < kSN; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    s[mt][n][e] = 0.f;
-        const uint32_t q_row = base + S::kQ + (lane & 15) * S::kQPitch + (lane >> 4) * 16;
-        if constexpr (FP8) {
-            const uint32_t k_row = k_smem + (16 * warp + g) * S::kKPitch + 8 * c;
-#pragma unroll
-            for (int d = 0; d < DP; d += 32) {
-                uint32_t kb[2][4];
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const uint2 x = lds64(k_row + 8 * n * S::kKPitch + d);
-                    kb[n][0] = e4m3x2_f16x2((uint16_t)x.x);
-                    kb[n][1] = e4m3x2_f16x2((uint16_t)(x.x >> 16));
-                    kb[n][2] = e4m3x2_f16x2((uint16_t)x.y);
-                    kb[n][3] = e4m3x2_f16x2((uint16_t)(x.y >> 16));
-                }
-#pragma unroll
-                for (int st = 0; st < 2; ++st)
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        uint32_t qa[4];
-                        ldsm4(qa, q_row + 16 * mt * S::kQPitch + (d + 16 * st) * 2);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n)
-                            mma16<true>(s[mt][n], qa, kb[n][2 * st], kb[n][2 * st + 1]);
-                    }
-            }
-        } else {
-            const uint32_t k_row = k_smem +
-                                   (16 * warp + (lane & 7) + (lane >> 4) * 8) * S::kKPitch +
-                                   ((lane >> 3) & 1) * 16;
-#pragma unroll
-            for (int d = 0; d < DP; d += 16) {
-                uint32_t kb[4];
-                ldsm4(kb, k_row + d * 2);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    uint32_t qa[4];
-                    ldsm4(qa, q_row + 16 * mt * S::kQPitch + d * 2);
-                    mma16<false>(s[mt][0], qa, kb[0], kb[1]);
-                    mma16<false>(s[mt][1], qa, kb[2], kb[3]);
-                }
-            }
-        }
-
-        // 2. scale, mask, row maxima
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 16 * mt + 8 * j + g;
-                const float sc = row_scale[r];
-                float big = kNegInf;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int pos = pos0 + 16 * warp + 8 * n + 2 * c + e;
-                        float &x = s[mt][n][2 * j + e];
-                        x = pos < sees[mt][j] ? x * sc : kNegInf;
-                        big = fmaxf(big, x);
-                    }
-                big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
-                big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-                if (c == 0)
-                    red[warp * S::kRows + r] = big;
-            }
-        __syncthreads();
-
-        // 3. weights
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int r = 16 * mt + 8 * j + g;
-                float big = m[mt][j];
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    big = fmaxf(big, red[w * S::kRows + r]);
-                const float ref = big == kNegInf ? 0.f : big;
-                const float alpha = ex2(m[mt][j] - ref);
-                m[mt][j] = big;
-                float sum = l[mt][j] * alpha;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float p0 = ex2(s[mt][n][2 * j] - ref);
-                    const float p1 = ex2(s[mt][n][2 * j + 1] - ref);
-                    sum += p0 + p1;
-                    *reinterpret_cast<uint32_t *>(smem + S::kP + r * S::kPPitch +
-                                                  (16 * warp + 8 * n + 2 * c) * 2) =
-                        pack2<FP8>(p0, p1);
-                }
-                l[mt][j] = sum;
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                    o[mt][n][2 * j] *= alpha;
-                    o[mt][n][2 * j + 1] *= alpha;
-                }
-            }
-        __syncthreads();
-
-        // 4. values
-        const uint32_t p_row = base + S::kP + (lane & 15) * S::kPPitch + (lane >> 4) * 16;
-#pragma unroll
-        for (int kk = 0; kk < kTile; kk += 16) {
-            uint32_t pa[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                ldsm4(pa[mt], p_row + 16 * mt * S::kPPitch + kk * 2);
+                    acc[n][e] = 0.f;
+            const uint32_t q_row =
+                base + S::kQ + (16 * mt + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
             if constexpr (FP8) {
-                // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
-                // kJ g .. kJ g + kJ - 1 of each 8 kJ-wide block; column tile j
-                // of the block is columns kJ n + j
-                const uint32_t v_row = v_smem + (kk + 2 * c) * S::kVPitch + warp * kCols + kJ * g;
+                const uint32_t k_row = k_smem + g * S::kKPitch + 8 * c;
 #pragma unroll
-                for (int nb = 0; nb < kNT; nb += kJ) {
-                    uint32_t x[4][kJ / 2];
+                for (int d = 0; d < DP; d += 32) {
+                    uint32_t qa[2][4];
+                    ldsm4(qa[0], q_row + d * 2);
+                    ldsm4(qa[1], q_row + d * 2 + 32);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const uint32_t at =
-                            v_row + ((q & 1) + (q >> 1) * 8) * S::kVPitch + nb * 8;
-                        if constexpr (kJ == 4) {
-                            const uint32_t w = lds32(at);
-                            x[q][0] = e4m3x2_f16x2((uint16_t)w);
-                            x[q][1] = e4m3x2_f16x2((uint16_t)(w >> 16));
-                        } else {
-                            x[q][0] = e4m3x2_f16x2(lds16(at));
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < kJ; ++j) {
-                        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                        const uint32_t b0 = __byte_perm(x[0][j / 2], x[1][j / 2], sel);
-                        const uint32_t b1 = __byte_perm(x[2][j / 2], x[3][j / 2], sel);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            mma16<true>(o[mt][nb + j], pa[mt], b0, b1);
+                    for (int n = 0; n < kSN; ++n) {
+                        const uint2 x = lds64(k_row + 8 * n * S::kKPitch + d);
+                        uint32_t kb[4];
+                        e4m3x4_f16x4(x.x, kb[0], kb[1]);
+                        e4m3x4_f16x4(x.y, kb[2], kb[3]);
+                        mma16<true>(acc[n], qa[0], kb[0], kb[1]);
+                        mma16<true>(acc[n], qa[1], kb[2], kb[3]);
                     }
                 }
             } else {
-                const uint32_t v_row = v_smem +
-                                       (kk + (lane & 7) + ((lane >> 3) & 1) * 8) * S::kVPitch +
-                                       (warp * kCols + (lane >> 4) * 8) * 2;
+                const uint32_t k_row = k_smem + ((lane & 7) + (lane >> 4) * 8) * S::kKPitch;
+                const int half = (lane >> 3) & 1;
 #pragma unroll
-                for (int n = 0; n < kNT; n += 2) {
-                    uint32_t vb[4];
-                    ldsm4_trans(vb, v_row + n * 16);
+                for (int d = 0; d < DP; d += 16) {
+                    uint32_t qa[4];
+                    ldsm4(qa, q_row + d * 2);
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16<false>(o[mt][n], pa[mt], vb[0], vb[1]);
-                        mma16<false>(o[mt][n + 1], pa[mt], vb[2], vb[3]);
+                    for (int n = 0; n < kSN; n += 2) {
+                        uint32_t kb[4];
+                        ldsm4(kb, k_row + n * 8 * S::kKPitch +
+                                      (((d / 8 + half) ^ (lane & 7)) << 4));
+                        mma16<false>(acc[n], qa, kb[0], kb[1]);
+                        mma16<false>(acc[n + 1], qa, kb[2], kb[3]);
+                    }
+                }
+            }
+
+            // scale, mask, running maximum, weights
+            bool raised = false;
+            float alpha[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                const float sc = row_scale[16 * mt + 8 * j + g];
+#pragma unroll
+                for (int n = 0; n < kSN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        s[n][2 * j + e] = acc[n][2 * j + e] * sc;
+            }
+            if (pos0 + TOK > sees_least) {  // some position is masked for some row
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                    for (int n = 0; n < kSN; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (pos0 + 8 * n + 2 * c + e >= sees[j])
+                                s[n][2 * j + e] = kNegInf;
+            }
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                float big = m[j];
+#pragma unroll
+                for (int n = 0; n < kSN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        big = fmaxf(big, s[n][2 * j + e]);
+                big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
+                big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
+                const float ref = big == kNegInf ? 0.f : big;
+                raised |= big != m[j];
+                alpha[j] = ex2(m[j] - ref);
+                m[j] = big;
+                float sum = l[j] * alpha[j];
+#pragma unroll
+                for (int n = 0; n < kSN; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[n][2 * j + e];
+                        x = ex2(x - ref);
+                        sum += x;
+                    }
+                l[j] = sum;
+            }
+            // most chunks raise no maximum: then the output rows stay as they are
+            if (__any_sync(kFull, raised)) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2 * NJ; ++e)
+                        o[n][e] *= alpha[e >> 1];
+            }
+#pragma unroll
+            for (int k = 0; k < TOK / 16; ++k) {
+                pa[k][0] = pack2<FP8>(s[2 * k][0], s[2 * k][1]);
+                pa[k][1] = NJ == 2 ? pack2<FP8>(s[2 * k][2 * NJ - 2], s[2 * k][2 * NJ - 1]) : 0u;
+                pa[k][2] = pack2<FP8>(s[2 * k + 1][0], s[2 * k + 1][1]);
+                pa[k][3] =
+                    NJ == 2 ? pack2<FP8>(s[2 * k + 1][2 * NJ - 2], s[2 * k + 1][2 * NJ - 1]) : 0u;
+            }
+        }
+
+        // values
+        cp_async_wait<2 * P - 1>();
+        group_sync<kGroup>(group);
+        load_values();  // into the entry of these keys
+        if (finds) {    // the chunk after: its addresses are read after the next barrier
+            row.resolve(a, addr + load_slot * 2 * TOK + at, TOK);
+            row.fetch(a, ahead, TOK * group + at);
+            ahead.next(a);
+        }
+        const uint32_t v_smem = ring + entry * S::kEntry;
+        entry = entry + 1 == S::kEntries ? 0 : entry + 1;
+        if (pos0 < cur.len) {
+            // positions only some rows see: added value by value, then zeroed
+            if (a.T > 1 && pos0 + TOK > sees_least) {
+                const int from = max(max(sees_least, 0) - pos0, 0);
+                const int to = min(cur.len - pos0, TOK);
+                for (int tok = from; tok < to; ++tok) {
+                    const int src = (lane & ~3) + ((tok & 7) >> 1);
+                    float w[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        float pair[kSN];
+#pragma unroll
+                        for (int n = 0; n < kSN; ++n)
+                            pair[n] = tok & 1 ? s[n][2 * j + 1] : s[n][2 * j];
+                        float mine = tok & 8 ? pair[1] : pair[0];
+                        if constexpr (kSN == 4)
+                            mine = tok & 16 ? (tok & 8 ? pair[3] : pair[2]) : mine;
+                        w[j] = __shfl_sync(kFull, mine, src);
+                    }
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int d = out_col<FP8>(n, c, e);
+                            float v;
+                            if constexpr (FP8)
+                                v = unpack1<true>((uint16_t)e4m3x2_f16x2(
+                                    lds8(v_smem + tok * S::kVPitch + d)));
+                            else
+                                v = unpack1<false>(lds16(v_smem + tok * S::kVPitch +
+                                                         (((d / 8) ^ (tok & 7)) << 4) + (d & 7) * 2));
+#pragma unroll
+                            for (int j = 0; j < NJ; ++j)
+                                if (pos0 + tok < sees[j])
+                                    o[n][2 * j + e] = fmaf(w[j], v, o[n][2 * j + e]);
+                        }
+                }
+                group_sync<kGroup>(group);
+                for (int u = at; u < (to - from) * (S::kVPitch / 16); u += kGroup)
+                    sts128(v_smem + from * S::kVPitch + u * 16, make_uint4(0, 0, 0, 0));
+                group_sync<kGroup>(group);
+            }
+#pragma unroll
+            for (int k = 0; k < TOK / 16; ++k) {
+                if constexpr (FP8) {
+                    // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
+                    // 4 g .. 4 g + 3 of each block of 32; column tile j of a
+                    // block is columns 4 n + j
+                    const uint32_t v_row = v_smem + (16 * k + 2 * c) * S::kVPitch + 4 * g;
+#pragma unroll
+                    for (int nb = 0; nb < kNT; nb += 4) {
+                        uint32_t x[4][2];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            e4m3x4_f16x4(
+                                lds32(v_row + ((q & 1) + (q >> 1) * 8) * S::kVPitch + nb * 8),
+                                x[q][0], x[q][1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
+                            mma_rows<true, NJ>(o[nb + j], pa[k],
+                                               __byte_perm(x[0][j / 2], x[1][j / 2], sel),
+                                               __byte_perm(x[2][j / 2], x[3][j / 2], sel));
+                        }
+                    }
+                } else {
+                    const uint32_t v_row = v_smem + (16 * k + (lane & 15)) * S::kVPitch;
+#pragma unroll
+                    for (int n = 0; n < kNT; n += 2) {
+                        uint32_t vb[4];
+                        ldsm4_trans(vb, v_row + (((n + (lane >> 4)) ^ (lane & 7)) << 4));
+                        mma_rows<false, NJ>(o[n], pa[k], vb[0], vb[1]);
+                        mma_rows<false, NJ>(o[n + 1], pa[k], vb[2], vb[3]);
                     }
                 }
             }
         }
-        // the column of o[.][n][e] is col(n, e) (+ 2 j rows)
-        auto col = [&](int n, int e) {
-            if constexpr (FP8)
-                return warp * kCols + n / kJ * kJ * 8 + kJ * (2 * c + e) + n % kJ;
-            else
-                return warp * kCols + 8 * n + 2 * c + e;
-        };
-        // positions only some rows see
-        if (a.T > 1 && pos0 + kTile > cur.len - (a.T - 1)) {
-            const int from = max(pos0, max(cur.len - (a.T - 1), 0));
-            const int to = min(pos0 + kTile, cur.len);
-            for (int pos = from; pos < to; ++pos)
-#pragma unroll
-                for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int d = col(n, e);
-                        if (d >= a.D)
-                            continue;
-                        const float v = value_at<FP8>(a, cur.b, cur.h, pos, d);
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                if (pos < sees[mt][j]) {
-                                    const float p = unpack1<FP8>(*reinterpret_cast<const uint16_t *>(
-                                        smem + S::kP + (16 * mt + 8 * j + g) * S::kPPitch +
-                                        (pos - pos0) * 2));
-                                    o[mt][n][2 * j + e] = fmaf(p, v, o[mt][n][2 * j + e]);
-                                }
-                    }
-        }
 
         const bool ends = cur.t + 1 == cur.tiles;
-        if (ends || i + 1 == n_units) {
-            // this block's part of the (sequence, head) is complete
+        if (ends || left == 1) {
+            // This block's part of the (sequence, head) is complete: join the
+            // groups, one after the other, in Q's place.
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float x = l[mt][j];
-                    x += __shfl_xor_sync(kFull, x, 1);
-                    x += __shfl_xor_sync(kFull, x, 2);
-                    if (c == 0)
-                        sums[warp * S::kRows + 16 * mt + 8 * j + g] = x;
-                }
+            for (int j = 0; j < NJ; ++j) {
+                l[j] += __shfl_xor_sync(kFull, l[j], 1);
+                l[j] += __shfl_xor_sync(kFull, l[j], 2);
+                if (c == 0)
+                    stat[group * S::kRows + 16 * mt + 8 * j + g] = make_float2(m[j], l[j]);
+            }
             __syncthreads();
+            float f[NJ];
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) {
+                float big = kNegInf;
+#pragma unroll
+                for (int w = 0; w < G; ++w)
+                    big = fmaxf(big, stat[w * S::kRows + 16 * mt + 8 * j + g].x);
+                f[j] = ex2(m[j] - (big == kNegInf ? 0.f : big));
+            }
+            for (int w = 0; w < G; ++w) {
+                if (w == group) {
+#pragma unroll
+                    for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2 * NJ; ++e) {
+                            float *dst = merged + (16 * mt + 8 * (e >> 1) + g) * S::kMPitch +
+                                         out_col<FP8>(n, c, e & 1);
+                            const float x = o[n][e] * f[e >> 1];
+                            *dst = w == 0 ? x : *dst + x;
+                        }
+                }
+                __syncthreads();
+            }
             const bool whole = ends && t_first == 0;
             float *part = a.parts + (2 * (int64_t)blockIdx.x + (first_part ? 0 : 1)) * a.part_floats;
+            for (int r = warp; r < a.rows; r += kWarps) {
+                float big = kNegInf, sum = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+                for (int w = 0; w < G; ++w)
+                    big = fmaxf(big, stat[w * S::kRows + r].x);
+                const float ref = big == kNegInf ? 0.f : big;
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int r = 16 * mt + 8 * j + g;
-                    if (r >= a.rows)
-                        continue;
-                    float x = 0.f;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w)
-                        x += sums[w * S::kRows + r];
-                    if (whole) {
-                        const int t = r / a.G;
-                        const int64_t at = ((int64_t)cur.b * a.T + t) * a.Hq + cur.h * a.G +
-                                           (r - t * a.G);
-                        // a row without positions (or of -inf scores only): 0
-                        const float f = x == 0.f ? 0.f : a.v_scale / x;
-#pragma unroll
-                        for (int n = 0; n < kNT; ++n) {
-                            if constexpr (FP8) {
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (col(n, e) < a.D)
-                                        a.out[at * a.D + col(n, e)] =
-                                            (uint16_t)(pack2<false>(o[mt][n][2 * j + e] * f, 0.f));
-                            } else if (col(n, 0) < a.D) {
-                                *reinterpret_cast<uint32_t *>(a.out + at * a.D + col(n, 0)) =
-                                    pack2<false>(o[mt][n][2 * j] * f, o[mt][n][2 * j + 1] * f);
-                            }
-                        }
-                        if (a.lse && warp == 0 && c == 0)
-                            a.lse[at] = log_sum(m[mt][j], x);
-                    } else {
-#pragma unroll
-                        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (col(n, e) < a.D)
-                                    part[r * a.D + col(n, e)] = o[mt][n][2 * j + e];
-                        if (warp == 0 && c == 0) {
-                            part[a.rows * a.D + 2 * r] = m[mt][j];
-                            part[a.rows * a.D + 2 * r + 1] = x;
-                        }
+                for (int w = 0; w < G; ++w)
+                    sum += stat[w * S::kRows + r].y * ex2(stat[w * S::kRows + r].x - ref);
+                const float *src = merged + r * S::kMPitch;
+                if (whole) {
+                    const int t = r / a.G;
+                    const int64_t to =
+                        ((int64_t)cur.b * a.T + t) * a.Hq + cur.h * a.G + (r - t * a.G);
+                    // a row without positions (or of -inf scores only): 0
+                    const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+                    for (int d = 2 * lane; d < a.D; d += 64)
+                        *reinterpret_cast<uint32_t *>(a.out + to * a.D + d) =
+                            pack2<false>(src[d] * inv, src[d + 1] * inv);
+                    if (a.lse && lane == 0)
+                        a.lse[to] = log_sum(big, sum);
+                } else {
+                    for (int d = 4 * lane; d < a.D; d += 128)
+                        *reinterpret_cast<float4 *>(part + r * a.D + d) =
+                            *reinterpret_cast<const float4 *>(src + d);
+                    if (lane == 0)
+                        reinterpret_cast<float2 *>(part + a.rows * a.D)[r] = make_float2(big, sum);
+                }
+            }
+            if (!whole) {
+                // The shares that hold the pair: those of its first and last
+                // unit (s holds unit u when floor(s U / n) <= u < floor((s + 1) U / n)).
+                const int64_t here = share.u1 - left;  // this unit
+                const int64_t first = here - cur.t, last = first + cur.tiles - 1;
+                const int n = share.shares, mine = (int)blockIdx.x / a.lanes;
+                const int s0 = holder(first, share.units, n), s1 = holder(last, share.units, n);
+                const int lane_of = blockIdx.x % a.lanes;
+                // a share's first pair is in its slot 0, a later one in slot 1
+                const int slot0 =
+                    2 * (s0 * a.lanes + lane_of) + (cut(share.units, s0, n) < first ? 1 : 0);
+                auto slot_of = [&](int s) { return s == s0 ? slot0 : 2 * (s * a.lanes + lane_of); };
+                const int count = s1 - s0 + 1, index = mine - s0;
+                const int from = index / kJoin * kJoin;       // first part of this part's group
+                const int size = min(kJoin, count - from);
+                const int groups = (count + kJoin - 1) / kJoin;
+                const int step = 2 * a.lanes;                 // slots from a share to the next
+                unsigned int *tickets = a.tickets;
+                __syncthreads();
+                if (threadIdx.x == 0)
+                    s_last = ticket_inc(tickets + slot_of(s0 + from), size - 1) ==
+                             (unsigned)size - 1;
+                __syncthreads();
+                if (s_last) {
+                    join_parts<kThreads>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1), step,
+                                         groups == 1, cur.b, cur.h, merged);
+                    if (groups > 1) {
+                        if (threadIdx.x == 0)
+                            s_last = ticket_inc(tickets + a.top_tickets + slot0, groups - 1) ==
+                                     (unsigned)groups - 1;
+                        __syncthreads();
+                        if (s_last)
+                            join_parts<kThreads>(a, groups, slot0, slot_of(s0 + kJoin),
+                                                 step * kJoin, true, cur.b, cur.h, merged);
                     }
                 }
+            }
+            __syncthreads();
             first_part = false;
             fresh = true;
         }
         cur.next(a);
     }
+    write_empty<kThreads>(a);
 }
 
-// STAGES tiles in the ring, or one fewer where they and Q exceed a block's
-// shared memory (227 KB less the static part).
-template <int DP, bool FP8, int MT, int STAGES>
+template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
 cudaError_t config(AttnConfig *out)
 {
-    constexpr int kFit = Shape<DP, FP8, MT, STAGES>::kBytes <= 227 * 1024 - 128 ? STAGES : STAGES - 1;
-    static_assert(kFit >= 2, "the ring needs two stages");
-    out->func = reinterpret_cast<const void *>(attention_kernel<DP, FP8, MT, kFit>);
-    out->smem = Shape<DP, FP8, MT, kFit>::kBytes;
+    using S = Shape<DP, FP8, RT, TOK, P, G>;
+    static_assert(BLOCKS * (S::kBytes + 1024 + 256) <= 228 * 1024, "shared memory per SM");
+    out->func = reinterpret_cast<const void *>(attention_kernel<DP, FP8, RT, TOK, P, G, BLOCKS>);
+    out->smem = S::kBytes;
+    out->threads = S::kThreads;
+    out->tile = S::kTile;
     return cudaSuccess;
-}
-
-template <int DP, bool FP8, int STAGES>
-cudaError_t config_rows(int rows, AttnConfig *out)
-{
-    if (rows <= 16)
-        return config<DP, FP8, 1, STAGES>(out);
-    if (rows <= 32)
-        return config<DP, FP8, 2, STAGES>(out);
-    return config<DP, FP8, 4, STAGES>(out);
 }
 
 }  // namespace attn

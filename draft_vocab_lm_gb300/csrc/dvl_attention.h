@@ -7,20 +7,20 @@
 namespace dvl {
 namespace attn {
 
-constexpr int kTile = 64;  // tokens per unit of work
-
 struct AttnArgs {
     const uint16_t *q;        // bf16
     int64_t qb, qt, qh;       // strides in elements: sequence, token, head
     const unsigned char *k, *v;
-    int64_t kp, kt, kh;       // strides in bytes: page, token, head
-    int64_t vp, vt, vh;
+    int64_t kp, vp;           // strides in bytes: page
+    uint32_t kt, kh, vt, vh;  // token, head (within a page)
     const int32_t *table;
     int64_t table_stride;
     const int32_t *lengths;
     uint16_t *out;            // bf16 [B][T][Hq][D]
     float *lse;               // [B][T][Hq] or nullptr
     unsigned char *ws;        // its header holds the status word
+    unsigned int *tickets;    // [2 * blocks] of parts, then as many of groups of parts
+    int top_tickets;          // 2 * blocks
     float *parts;             // [2 * blocks][part_floats]
     int64_t part_floats;      // rows * D sums, then (maximum, sum) per row
     int B, T, Hq, heads, G, D;
@@ -31,7 +31,8 @@ struct AttnArgs {
     int page_shift;
     float qk_scale;           // scale * k_scale * log2(e)
     float v_scale;
-    int blocks;               // of the attention kernel
+    int blocks;               // of the grid
+    int lanes;                // blocks that walk the same tokens, one head each
 
 #ifdef __CUDACC__
     __device__ __forceinline__ int page_of(int pos) const
@@ -42,11 +43,25 @@ struct AttnArgs {
 };
 
 #ifdef __CUDACC__
-// Blocks that hold units: with fewer units than blocks, one unit each, so
-// that every block between a pair's first and last holds a part of it.
-__device__ __forceinline__ int64_t used_blocks(int blocks, int64_t units)
+// Shares that hold units: with fewer units than blocks of a lane, one unit
+// each, so that every share between a pair's first and last holds a part.
+__device__ __forceinline__ int used_shares(const AttnArgs &a, int64_t units)
 {
-    return units < blocks ? units : blocks;
+    const int n = a.blocks / a.lanes;
+    return units < n ? (int)units : n;
+}
+
+// Cached tokens of sequence b, cut to what its table row can name, and the
+// units of one cached head of it.
+__device__ __forceinline__ int seq_len(const AttnArgs &a, int b)
+{
+    const int n = a.lengths[b];
+    return n < 0 ? 0 : n > a.max_len ? a.max_len : n;
+}
+template <int TILE>
+__device__ __forceinline__ int seq_tiles(const AttnArgs &a, int b)
+{
+    return (seq_len(a, b) + TILE - 1) / TILE;
 }
 
 // Natural logarithm of a sum of weights relative to 2^m; -inf for an empty row.
@@ -60,14 +75,16 @@ __device__ __forceinline__ float log_sum(float m, float sum)
 struct AttnConfig {
     const void *func;
     size_t smem;
+    int threads;
+    int tile;  // tokens per unit
 };
 // The kernel for padded head widths of 64, 128 and 256, by cache type.
 cudaError_t config_bf16(int D, int rows, AttnConfig *out);
 cudaError_t config_fp8(int D, int rows, AttnConfig *out);
 
-// Blocks of the attention kernel on the current device.
+// The kernel and its grid on the current device.
 cudaError_t grid_blocks(bool fp8, int D, int rows, AttnConfig *cfg, int *blocks);
-cudaError_t launch_attention(AttnArgs &a, bool fp8, cudaStream_t s);
+cudaError_t launch_attention(AttnArgs &a, const AttnConfig &cfg, cudaStream_t s);
 
 }  // namespace attn
 }  // namespace dvl

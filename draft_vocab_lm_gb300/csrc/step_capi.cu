@@ -35,6 +35,10 @@ dvl_status check_cache(const dvl_kv_cache *c)
     for (int64_t s : strides)
         if (s < 0 || s % unit != 0)
             return DVL_ERR_INVALID_ARG;
+    // one page spans less than 2 GB: offsets within a page are 32-bit
+    for (int i = 0; i < 6; i += 3)
+        if ((double)strides[i + 1] * c->page_size + (double)strides[i + 2] * c->heads > 1e9)
+            return DVL_ERR_INVALID_ARG;
     if (!std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
         return DVL_ERR_INVALID_ARG;
     return DVL_OK;
@@ -54,7 +58,8 @@ int64_t part_floats(int rows, int D) { return ((int64_t)rows * (D + 2) + 3) / 4 
 
 size_t attention_bytes(int blocks, int rows, int D)
 {
-    return kWsSlots + (size_t)2 * blocks * part_floats(rows, D) * sizeof(float);
+    return kWsSlots + (size_t)4 * blocks * sizeof(unsigned int) +
+           (size_t)2 * blocks * part_floats(rows, D) * sizeof(float);
 }
 
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)
@@ -123,7 +128,7 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     if (rows == 0 || B < 0 || (int64_t)B * cache->heads * rows > 0x7fffffffLL)
         return DVL_ERR_INVALID_ARG;
     if (table_width < 1 || table_stride < 0 ||
-        (int64_t)table_width * cache->page_size > 0x7fffffffLL - attn::kTile)
+        (int64_t)table_width * cache->page_size > 0x7fffffffLL - 64)  // a tile more than the last token
         return DVL_ERR_INVALID_ARG;
     if (!q || !aligned(q, 16) || !table || !aligned(table, 4) || !lengths || !aligned(lengths, 4) ||
         !out || !aligned(out, 16) || !aligned(lse, 4))
@@ -150,18 +155,20 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.k = static_cast<const unsigned char *>(cache->k);
     a.v = static_cast<const unsigned char *>(cache->v);
     a.kp = cache->k_page_stride * size;
-    a.kt = cache->k_token_stride * size;
-    a.kh = cache->k_head_stride * size;
+    a.kt = (uint32_t)(cache->k_token_stride * size);
+    a.kh = (uint32_t)(cache->k_head_stride * size);
     a.vp = cache->v_page_stride * size;
-    a.vt = cache->v_token_stride * size;
-    a.vh = cache->v_head_stride * size;
+    a.vt = (uint32_t)(cache->v_token_stride * size);
+    a.vh = (uint32_t)(cache->v_head_stride * size);
     a.table = table;
     a.table_stride = table_stride;
     a.lengths = lengths;
     a.out = static_cast<uint16_t *>(out);
     a.lse = lse;
     a.ws = static_cast<unsigned char *>(ws);
-    a.parts = reinterpret_cast<float *>(a.ws + kWsSlots);
+    a.tickets = reinterpret_cast<unsigned int *>(a.ws + kWsSlots);
+    a.top_tickets = 2 * a.blocks;
+    a.parts = reinterpret_cast<float *>(a.tickets + 4 * a.blocks);
     a.part_floats = part_floats(rows, cache->D);
     a.B = B;
     a.T = T;
@@ -182,7 +189,7 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.page_mul = (uint32_t)((1ull << a.page_shift) / (uint64_t)cache->page_size + 1);
     a.qk_scale = scale * cache->k_scale * 1.4426950408889634f;
     a.v_scale = cache->v_scale;
-    return done(attn::launch_attention(a, fp8, static_cast<cudaStream_t>(stream)));
+    return done(attn::launch_attention(a, cfg, static_cast<cudaStream_t>(stream)));
 }
 
 size_t dvl_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t N)

@@ -216,7 +216,7 @@ def test_attention_status_and_workspace_reuse(dvl):
     c = Case(11, [100, 130, 20], 1, 4, 2, 64, 16)
     cache = dvl.KVCache(c.k, c.v)
     ws = dvl.attention_workspace(cache, 3, 1, 4)
-    ws[512:] = 0x7f  # what earlier calls leave in the parts must not matter
+    ws[512 + 16 * 1024:] = 0x7f  # what earlier calls leave in the parts must not matter
     good = c.call(dvl, ws=ws)
     c.verify(good)
     assert dvl.workspace_status(ws) == 0
