@@ -77,7 +77,7 @@ namespace dvl {
 namespace attn {
 
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr int kJoin = 32;  // parts joined at once; its square bounds the shares
+constexpr int kJoin = 16;  // parts per first-level join
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -265,9 +265,7 @@ struct Shape {
     static constexpr int kEntries = 2 * P + 1;
     static constexpr int kRing = kEntries * kEntry;        // per group
     static constexpr int kQ = G * kRing;                   // Q; the merged rows at a pair's end
-    static constexpr int kJoinBytes = 2 * (kJoin + 1) * kRows * 4;  // weights of a join
-    static constexpr int kQBytes =
-        max_of(kQRows * kQPitch, max_of(kRows * kMPitch * 4, kJoinBytes));
+    static constexpr int kQBytes = max_of(kQRows * kQPitch, kRows * kMPitch * 4);
     static constexpr int kStat = kQ + kQBytes;             // float2[G][kRows]: maximum, sum
     static constexpr int kScale = kStat + G * kRows * 8;   // float[kQRows]
     static constexpr int kAddr = kScale + kQRows * 4;      // pointers [G][P + 1][2][TOK]
@@ -463,57 +461,60 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a)
     }
 }
 
-// Add n parts (slots[i] of the workspace) in order.  With `last` the result
-// is the (sequence, head)'s output, else it replaces the first part.
-// scratch: 2 (kJoin + 1) rows floats.  Every thread calls it.
-template <int THREADS>
+// Add n parts in order: slot `first`, then second, second + stride, ..  Their
+// statistics lie at `stats`.  With `last` the result is the (sequence, head)'s
+// output, else its sums replace the first part's and its statistics go behind
+// that part's own.  Every thread takes its own (row, 4 columns) and runs through
+// the parts with a running maximum, kBatch parts' loads in flight at a time;
+// no shared memory and no barrier.
+template <int DP, int THREADS>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, int second,
-                                           int stride, bool last, int b, int h, float *scratch)
+                                           int stride, int stats, bool last, int b, int h)
 {
-    // part i: slot `first` for i = 0, then second, second + stride, ..
-    auto part = [&](int i) {
-        return a.parts + (int64_t)(i == 0 ? first : second + (i - 1) * stride) * a.part_floats;
-    };
-    const int stats = a.rows * a.D;
-    float *weight = scratch, *sums = scratch + kJoin * a.rows;  // [n][rows] each
-    float2 *total = reinterpret_cast<float2 *>(scratch + 2 * kJoin * a.rows);
-    for (int i0 = threadIdx.x; i0 < n * a.rows; i0 += THREADS) {
-        const int i = i0 / a.rows, r = i0 - i * a.rows;
-        const float2 ml = __ldcg(reinterpret_cast<const float2 *>(part(i) + stats) + r);
-        weight[i0] = ml.x;
-        sums[i0] = ml.y;
-    }
-    __syncthreads();
-    for (int r = threadIdx.x; r < a.rows; r += THREADS) {
-        float m = kNegInf;
-        for (int i = 0; i < n; ++i)
-            m = fmaxf(m, weight[i * a.rows + r]);
-        const float ref = m == kNegInf ? 0.f : m;
-        float sum = 0.f;
-        for (int i = 0; i < n; ++i) {
-            const float w = ex2(weight[i * a.rows + r] - ref);
-            weight[i * a.rows + r] = w;
-            sum += sums[i * a.rows + r] * w;
-        }
-        total[r] = make_float2(m, sum);
-    }
-    __syncthreads();
-    const int cols = a.D / 4;
-    for (int i0 = threadIdx.x; i0 < a.rows * cols; i0 += THREADS) {
-        const int r = i0 / cols, d = 4 * (i0 - r * cols);
+    constexpr int kBatch = 8;
+    constexpr int kCols = DP / 4;
+    const int d = 4 * ((int)threadIdx.x % kCols);
+    if (d >= a.D)
+        return;
+    for (int r = (int)threadIdx.x / kCols; r < a.rows; r += THREADS / kCols) {
+        float m = kNegInf, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float w = weight[i * a.rows + r];
-            const float4 x = __ldcg(reinterpret_cast<const float4 *>(part(i) + r * a.D + d));
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
+        float *to_part = a.parts + (int64_t)first * a.part_floats;
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+            float2 ml[kBatch];
+            float4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                ml[i] = make_float2(kNegInf, 0.f);
+                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i0 + i < n) {
+                    const int slot = i0 + i == 0 ? first : second + (i0 + i - 1) * stride;
+                    const float *p = a.parts + (int64_t)slot * a.part_floats;
+                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + stats) + r);
+                    x[i] = __ldcg(reinterpret_cast<const float4 *>(p + r * a.D + d));
+                }
+            }
+            float big = m;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                big = fmaxf(big, ml[i].x);
+            const float ref = big == kNegInf ? 0.f : big;
+            const float alpha = ex2(m - ref);
+            m = big;
+            sum *= alpha;
+            acc.x *= alpha, acc.y *= alpha, acc.z *= alpha, acc.w *= alpha;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const float w = ex2(ml[i].x - ref);
+                sum = fmaf(w, ml[i].y, sum);
+                acc.x = fmaf(w, x[i].x, acc.x);
+                acc.y = fmaf(w, x[i].y, acc.y);
+                acc.z = fmaf(w, x[i].z, acc.z);
+                acc.w = fmaf(w, x[i].w, acc.w);
+            }
         }
-        const float m = total[r].x, sum = total[r].y;
         if (last) {
-            const int t = r / a.G;
+            const int t = a.token_of(r);
             const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
             // a row without positions (or of -inf scores only): 0
             const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
@@ -523,12 +524,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, 
             if (a.lse && d == 0)
                 a.lse[to] = log_sum(m, sum);
         } else {
-            *reinterpret_cast<float4 *>(part(0) + r * a.D + d) = acc;
+            // (the part's own statistics may still be read by other threads)
+            *reinterpret_cast<float4 *>(to_part + r * a.D + d) = acc;
             if (d == 0)
-                reinterpret_cast<float2 *>(part(0) + stats)[r] = make_float2(m, sum);
+                reinterpret_cast<float2 *>(to_part + stats + 2 * a.rows)[r] = make_float2(m, sum);
         }
     }
-    __syncthreads();
 }
 
 template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
@@ -639,50 +640,63 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
         if (fresh) {
             fresh = false;
             t_first = cur.t;
-            // Q of this (sequence, cached head): row t * G + g
-            for (int r = warp; r < S::kQRows; r += kWarps) {
-                const int t = r / a.G;
-                const uint16_t *q = a.q + cur.b * a.qb + t * a.qt +
-                                    (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh;
+            // Q of this (sequence, cached head): row t * G + g; a thread takes
+            // 8 values of a row, all of its loads in flight at once
+            constexpr int kUnits = DP / 8;
+            constexpr int kPasses = (S::kQRows * kUnits + kThreads - 1) / kThreads;
+            uint4 qv[kPasses];
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
+                const int d = ((int)threadIdx.x % kUnits) * 8;
+                qv[i] = make_uint4(0, 0, 0, 0);
+                if (r < a.rows && d < a.D) {
+                    const int t = a.token_of(r);
+                    qv[i] = *reinterpret_cast<const uint4 *>(
+                        a.q + cur.b * a.qb + t * a.qt +
+                        (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh + d);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
+                const int d = ((int)threadIdx.x % kUnits) * 8;
                 unsigned char *dst = smem + S::kQ + r * S::kQPitch;
                 if constexpr (FP8) {
-                    constexpr int kPer = DP / 32;  // values per lane
-                    float v[kPer];
+                    const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
                     uint32_t big = 0u;
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        const int d = lane + 32 * e;
-                        v[e] = r < a.rows && d < a.D ? __uint_as_float((uint32_t)q[d] << 16) : 0.f;
-                        big = max(big, __float_as_uint(v[e]) & 0x7fffffffu);
-                    }
-                    big = __reduce_max_sync(kFull, big);
+                    for (int e = 0; e < 4; ++e)
+                        big = max(big, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+#pragma unroll
+                    for (int off = kUnits / 2; off >= 1; off >>= 1)
+                        big = max(big, __shfl_xor_sync(kFull, big, off));
                     int e2 = (int)(big >> 23) - 127;
                     e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
                     const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                    if (r < S::kQRows) {
+                        // place of value d in the permuted order: block of 32,
+                        // lane quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
 #pragma unroll
-                    for (int e = 0; e < kPer; ++e) {
-                        // place of d in the permuted order: block of 32, lane
-                        // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
-                        const int d = lane + 32 * e;
-                        const int p = (d & ~31) + ((d >> 2) & 1) * 16 + ((d >> 1) & 1) * 8 +
-                                      ((d >> 3) & 3) * 2 + (d & 1);
-                        reinterpret_cast<uint16_t *>(dst)[p] =
-                            (uint16_t)(pack2<true>(v[e] * up, 0.f) & 0xffffu);
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint32_t *>(
+                                dst + 2 * ((d & ~31) + (e >> 1) * 16 + (e & 1) * 8 +
+                                           ((d >> 3) & 3) * 2)) =
+                                pack2<true>(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+                        if (d == 0)
+                            row_scale[r] =
+                                a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
                     }
-                    if (lane == 0)
-                        row_scale[r] = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
-                } else {
-                    for (int d = 2 * lane; d < DP; d += 64)
-                        *reinterpret_cast<uint32_t *>(dst + 2 * d) =
-                            r < a.rows && d < a.D ? *reinterpret_cast<const uint32_t *>(q + d) : 0u;
-                    if (lane == 0)
+                } else if (r < S::kQRows) {
+                    *reinterpret_cast<uint4 *>(dst + 2 * d) = qv[i];
+                    if (d == 0)
                         row_scale[r] = a.qk_scale;
                 }
             }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 const int r = 16 * mt + 8 * j + g;
-                sees[j] = r < a.rows ? cur.len - (a.T - 1 - r / a.G) : 0;
+                sees[j] = r < a.rows ? cur.len - (a.T - 1 - a.token_of(r)) : 0;
                 m[j] = kNegInf;
                 l[j] = 0.f;
             }
@@ -926,14 +940,40 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             }
             for (int w = 0; w < G; ++w) {
                 if (w == group) {
+                    // four column tiles at a time, loads before stores
 #pragma unroll
-                    for (int n = 0; n < kNT; ++n)
+                    for (int n0 = 0; n0 < kNT; n0 += 4)
 #pragma unroll
-                        for (int e = 0; e < 2 * NJ; ++e) {
-                            float *dst = merged + (16 * mt + 8 * (e >> 1) + g) * S::kMPitch +
-                                         out_col<FP8>(n, c, e & 1);
-                            const float x = o[n][e] * f[e >> 1];
-                            *dst = w == 0 ? x : *dst + x;
+                        for (int j = 0; j < NJ; ++j) {
+                            float *dst = merged + (16 * mt + 8 * j + g) * S::kMPitch;
+                            if constexpr (FP8) {
+                                // the four tiles' columns interleave: two runs of four
+                                float4 *p[2];
+                                float4 x[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    p[e] = reinterpret_cast<float4 *>(dst + out_col<true>(n0, c, e));
+                                    x[e] = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *p[e];
+                                }
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    *p[e] = make_float4(fmaf(o[n0][2 * j + e], f[j], x[e].x),
+                                                        fmaf(o[n0 + 1][2 * j + e], f[j], x[e].y),
+                                                        fmaf(o[n0 + 2][2 * j + e], f[j], x[e].z),
+                                                        fmaf(o[n0 + 3][2 * j + e], f[j], x[e].w));
+                            } else {
+                                float2 x[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    x[i] = w == 0 ? make_float2(0.f, 0.f)
+                                                  : *reinterpret_cast<const float2 *>(
+                                                        dst + out_col<false>(n0 + i, c, 0));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    *reinterpret_cast<float2 *>(dst + out_col<false>(n0 + i, c, 0)) =
+                                        make_float2(fmaf(o[n0 + i][2 * j], f[j], x[i].x),
+                                                    fmaf(o[n0 + i][2 * j + 1], f[j], x[i].y));
+                            }
                         }
                 }
                 __syncthreads();
@@ -951,7 +991,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     sum += stat[w * S::kRows + r].y * ex2(stat[w * S::kRows + r].x - ref);
                 const float *src = merged + r * S::kMPitch;
                 if (whole) {
-                    const int t = r / a.G;
+                    const int t = a.token_of(r);
                     const int64_t to =
                         ((int64_t)cur.b * a.T + t) * a.Hq + cur.h * a.G + (r - t * a.G);
                     // a row without positions (or of -inf scores only): 0
@@ -993,16 +1033,19 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                              (unsigned)size - 1;
                 __syncthreads();
                 if (s_last) {
-                    join_parts<kThreads>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1), step,
-                                         groups == 1, cur.b, cur.h, merged);
+                    const int stats = a.rows * a.D;
+                    join_parts<DP, kThreads>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1),
+                                             step, stats, groups == 1, cur.b, cur.h);
                     if (groups > 1) {
+                        __syncthreads();
                         if (threadIdx.x == 0)
                             s_last = ticket_inc(tickets + a.top_tickets + slot0, groups - 1) ==
                                      (unsigned)groups - 1;
                         __syncthreads();
                         if (s_last)
-                            join_parts<kThreads>(a, groups, slot0, slot_of(s0 + kJoin),
-                                                 step * kJoin, true, cur.b, cur.h, merged);
+                            join_parts<DP, kThreads>(a, groups, slot0, slot_of(s0 + kJoin),
+                                                     step * kJoin, stats + 2 * a.rows, true, cur.b,
+                                                     cur.h);
                     }
                 }
             }

@@ -9,10 +9,10 @@ namespace attn {
 cudaError_t config_bf16(int D, int rows, AttnConfig *out)
 {
     if (D <= 64)
-        return rows <= 8    ? config<64, false, 0, 32, 1, 4, 4>(out)
+        return rows <= 8    ? config<64, false, 0, 32, 1, 4, 3>(out)
                : rows <= 16 ? config<64, false, 1, 32, 1, 4, 3>(out)
-               : rows <= 32 ? config<64, false, 2, 32, 1, 4, 2>(out)
-                            : config<64, false, 4, 32, 1, 2, 2>(out);
+               : rows <= 32 ? config<64, false, 2, 32, 1, 4, 1>(out)
+                            : config<64, false, 4, 32, 1, 2, 1>(out);
     if (D <= 128)
         return rows <= 8    ? config<128, false, 0, 32, 1, 4, 2>(out)
                : rows <= 16 ? config<128, false, 1, 32, 1, 4, 2>(out)

@@ -22,9 +22,10 @@ struct AttnArgs {
     unsigned int *tickets;    // [2 * blocks] of parts, then as many of groups of parts
     int top_tickets;          // 2 * blocks
     float *parts;             // [2 * blocks][part_floats]
-    int64_t part_floats;      // rows * D sums, then (maximum, sum) per row
+    int64_t part_floats;      // rows * D sums, (maximum, sum) per row, the same of a joined group
     int B, T, Hq, heads, G, D;
     int rows;                 // T * G: query rows per cached head
+    uint32_t token_mul;       // row / G = row * token_mul >> 16, for up to 64 rows
     int pages, page_size;
     int max_len;              // tokens a table row can name
     uint32_t page_mul;        // pos / page_size = pos * page_mul >> page_shift
@@ -39,6 +40,7 @@ struct AttnArgs {
     {
         return (int)((uint64_t)(uint32_t)pos * page_mul >> page_shift);
     }
+    __device__ __forceinline__ int token_of(int row) const { return row * token_mul >> 16; }
 #endif
 };
 

@@ -53,8 +53,9 @@ int query_rows(const dvl_kv_cache *c, int32_t T, int32_t Hq)
     return rows <= DVL_MAX_QUERY_ROWS ? (int)rows : 0;
 }
 
-// Floats of one part: the rows' sums, then maximum and weight sum per row.
-int64_t part_floats(int rows, int D) { return ((int64_t)rows * (D + 2) + 3) / 4 * 4; }
+// Floats of one part: the rows' sums, then maximum and weight sum per row, and
+// room for those of a joined group.
+int64_t part_floats(int rows, int D) { return (int64_t)rows * (D + 4); }
 
 size_t attention_bytes(int blocks, int rows, int D)
 {
@@ -177,6 +178,7 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.G = Hq / cache->heads;
     a.D = cache->D;
     a.rows = rows;
+    a.token_mul = (uint32_t)((65536 + a.G - 1) / a.G);
     a.pages = cache->pages;
     a.page_size = cache->page_size;
     a.max_len = table_width * cache->page_size;
