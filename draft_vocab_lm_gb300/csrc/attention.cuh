@@ -245,6 +245,12 @@ struct Cursor {
 // G: groups, so G TOK tokens per tile.
 constexpr int max_of(int x, int y) { return x > y ? x : y; }
 
+// The most columns (DP halved as often as needed) of `bytes` each that fit.
+constexpr int round_columns(int dp, int bytes, int room)
+{
+    return dp * bytes <= room ? dp : round_columns(dp / 2, bytes, room);
+}
+
 template <int DP, bool FP8, int RT, int TOK, int P, int G>
 struct Shape {
     static constexpr int kElem = FP8 ? 1 : 2;
@@ -260,13 +266,16 @@ struct Shape {
     static constexpr int kQPitch = DP * 2 + 16;
     static constexpr int kRows = RT == 0 ? 8 : 16 * RT;    // query rows kept
     static constexpr int kQRows = RT == 0 ? 16 : 16 * RT;  // rows of the operand
-    static constexpr int kMPitch = DP + 4;                 // floats per merged row
-    static constexpr int kEntry = TOK * kKPitch;           // one ring entry
+    // One ring entry: a chunk's keys or values; also 32 columns of the rows.
+    static constexpr int kEntry = max_of(TOK * kKPitch, kRows * 4 * 32);
     static constexpr int kEntries = 2 * P + 1;
     static constexpr int kRing = kEntries * kEntry;        // per group
-    static constexpr int kQ = G * kRing;                   // Q; the merged rows at a pair's end
-    static constexpr int kQBytes = max_of(kQRows * kQPitch, kRows * kMPitch * 4);
-    static constexpr int kStat = kQ + kQBytes;             // float2[G][kRows]: maximum, sum
+    // At a pair's end every group lays its output rows, kRound columns at a
+    // time, into the ring entry that is free then.
+    static constexpr int kRound = round_columns(DP, kRows * 4, kEntry);
+    static_assert(kRound >= 32 && kEntry % 16 == 0, "rows are permuted within 32 columns");
+    static constexpr int kQ = G * kRing;
+    static constexpr int kStat = kQ + kQRows * kQPitch;    // float2[G][kRows]: maximum, sum
     static constexpr int kScale = kStat + G * kRows * 8;   // float[kQRows]
     static constexpr int kAddr = kScale + kQRows * 4;      // pointers [G][P + 1][2][TOK]
     static constexpr int kBytes = kAddr + G * (P + 1) * 2 * TOK * 8;
@@ -277,6 +286,13 @@ template <bool FP8>
 __device__ __forceinline__ int out_col(int n, int c, int e)
 {
     return FP8 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
+}
+
+// The permutation of a row's columns while the groups' rows are joined.
+template <bool FP8>
+__device__ __forceinline__ int swizzle(int r)
+{
+    return FP8 ? (r & 1) << 2 : (r & 3) << 3;
 }
 
 // Where a token's row starts, found by one thread per token a chunk before the
@@ -461,13 +477,27 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a)
     }
 }
 
+// Four columns of a finished row: the sums over their weights' sum.
+__device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, int d,
+                                        const float4 &acc, float m, float sum)
+{
+    const int t = a.token_of(r);
+    const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
+    // a row without positions (or of -inf scores only): 0
+    const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+    *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
+        make_uint2(pack2<false>(acc.x * inv, acc.y * inv), pack2<false>(acc.z * inv, acc.w * inv));
+    if (a.lse && d == 0)
+        a.lse[to] = log_sum(m, sum);
+}
+
 // Add n parts in order: slot `first`, then second, second + stride, ..  Their
 // statistics lie at `stats`.  With `last` the result is the (sequence, head)'s
 // output, else its sums replace the first part's and its statistics go behind
-// that part's own.  Every thread takes its own (row, 4 columns) and runs through
-// the parts with a running maximum, kBatch parts' loads in flight at a time;
-// no shared memory and no barrier.
-template <int DP, int THREADS>
+// that part's own.  Every thread takes 4 columns of R rows at a time and runs
+// through the parts with a running maximum, kBatch parts' loads in flight; no
+// shared memory and no barrier.
+template <int DP, int THREADS, int R>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, int second,
                                            int stride, int stats, bool last, int b, int h)
 {
@@ -476,58 +506,71 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, 
     const int d = 4 * ((int)threadIdx.x % kCols);
     if (d >= a.D)
         return;
-    for (int r = (int)threadIdx.x / kCols; r < a.rows; r += THREADS / kCols) {
-        float m = kNegInf, sum = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float *to_part = a.parts + (int64_t)first * a.part_floats;
+    constexpr int kStep = THREADS / kCols;  // rows per pass
+    float *to_part = a.parts + (int64_t)first * a.part_floats;
+    for (int r0 = (int)threadIdx.x / kCols; r0 < a.rows; r0 += R * kStep) {
+        float m[R], sum[R];
+        float4 acc[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            m[k] = kNegInf;
+            sum[k] = 0.f;
+            acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         for (int i0 = 0; i0 < n; i0 += kBatch) {
-            float2 ml[kBatch];
-            float4 x[kBatch];
+            float2 ml[R][kBatch];
+            float4 x[R][kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                ml[i] = make_float2(kNegInf, 0.f);
-                x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i0 + i < n) {
-                    const int slot = i0 + i == 0 ? first : second + (i0 + i - 1) * stride;
-                    const float *p = a.parts + (int64_t)slot * a.part_floats;
-                    ml[i] = __ldcg(reinterpret_cast<const float2 *>(p + stats) + r);
-                    x[i] = __ldcg(reinterpret_cast<const float4 *>(p + r * a.D + d));
+                const int slot = i0 + i == 0 ? first : second + (i0 + i - 1) * stride;
+                const float *p = a.parts + (int64_t)slot * a.part_floats;
+#pragma unroll
+                for (int k = 0; k < R; ++k) {
+                    const int r = r0 + k * kStep;
+                    ml[k][i] = make_float2(kNegInf, 0.f);
+                    x[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i0 + i < n && r < a.rows) {
+                        ml[k][i] = __ldcg(reinterpret_cast<const float2 *>(p + stats) + r);
+                        x[k][i] = __ldcg(reinterpret_cast<const float4 *>(p + r * a.D + d));
+                    }
                 }
             }
-            float big = m;
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                big = fmaxf(big, ml[i].x);
-            const float ref = big == kNegInf ? 0.f : big;
-            const float alpha = ex2(m - ref);
-            m = big;
-            sum *= alpha;
-            acc.x *= alpha, acc.y *= alpha, acc.z *= alpha, acc.w *= alpha;
+            for (int k = 0; k < R; ++k) {
+                float big = m[k];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const float w = ex2(ml[i].x - ref);
-                sum = fmaf(w, ml[i].y, sum);
-                acc.x = fmaf(w, x[i].x, acc.x);
-                acc.y = fmaf(w, x[i].y, acc.y);
-                acc.z = fmaf(w, x[i].z, acc.z);
-                acc.w = fmaf(w, x[i].w, acc.w);
+                for (int i = 0; i < kBatch; ++i)
+                    big = fmaxf(big, ml[k][i].x);
+                const float ref = big == kNegInf ? 0.f : big;
+                const float alpha = ex2(m[k] - ref);
+                m[k] = big;
+                sum[k] *= alpha;
+                acc[k].x *= alpha, acc[k].y *= alpha, acc[k].z *= alpha, acc[k].w *= alpha;
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float w = ex2(ml[k][i].x - ref);
+                    sum[k] = fmaf(w, ml[k][i].y, sum[k]);
+                    acc[k].x = fmaf(w, x[k][i].x, acc[k].x);
+                    acc[k].y = fmaf(w, x[k][i].y, acc[k].y);
+                    acc[k].z = fmaf(w, x[k][i].z, acc[k].z);
+                    acc[k].w = fmaf(w, x[k][i].w, acc[k].w);
+                }
             }
         }
-        if (last) {
-            const int t = a.token_of(r);
-            const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
-            // a row without positions (or of -inf scores only): 0
-            const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
-            *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
-                make_uint2(pack2<false>(acc.x * inv, acc.y * inv),
-                           pack2<false>(acc.z * inv, acc.w * inv));
-            if (a.lse && d == 0)
-                a.lse[to] = log_sum(m, sum);
-        } else {
-            // (the part's own statistics may still be read by other threads)
-            *reinterpret_cast<float4 *>(to_part + r * a.D + d) = acc;
-            if (d == 0)
-                reinterpret_cast<float2 *>(to_part + stats + 2 * a.rows)[r] = make_float2(m, sum);
+#pragma unroll
+        for (int k = 0; k < R; ++k) {
+            const int r = r0 + k * kStep;
+            if (r >= a.rows)
+                continue;
+            if (last) {
+                put_row(a, b, h, r, d, acc[k], m[k], sum[k]);
+            } else {
+                // (the part's own statistics may still be read by other threads)
+                *reinterpret_cast<float4 *>(to_part + r * a.D + d) = acc[k];
+                if (d == 0)
+                    reinterpret_cast<float2 *>(to_part + stats + 2 * a.rows)[r] =
+                        make_float2(m[k], sum[k]);
+            }
         }
     }
 }
@@ -555,7 +598,6 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     const uint32_t base = smem_u32(smem);
     float2 *stat = reinterpret_cast<float2 *>(smem + S::kStat);
     float *row_scale = reinterpret_cast<float *>(smem + S::kScale);
-    float *merged = reinterpret_cast<float *>(smem + S::kQ);
 
     const Share share = locate<kThreads, S::kTile>(a, s_scan);
     if (share.u0 >= share.u1) {
@@ -570,6 +612,28 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     cur.h = set * a.lanes + blockIdx.x % a.lanes;
     cur.t = (int)(share.off - (int64_t)set * cur.tiles);
     const int64_t n_units = share.u1 - share.u0;
+
+    // Q of a (sequence, cached head): row t * G + g; a thread takes 8 values of
+    // a row, all of its loads in flight at once -- the block's first ones
+    // before the ring's copies fill the memory system's queues.
+    constexpr int kUnits = DP / 8;
+    constexpr int kPasses = (S::kQRows * kUnits + kThreads - 1) / kThreads;
+    uint4 qv[kPasses];
+    auto load_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
+            const int d = ((int)threadIdx.x % kUnits) * 8;
+            qv[i] = make_uint4(0, 0, 0, 0);
+            if (r < a.rows && d < a.D) {
+                const int t = a.token_of(r);
+                qv[i] = *reinterpret_cast<const uint4 *>(
+                    a.q + cur.b * a.qb + t * a.qt +
+                    (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh + d);
+            }
+        }
+    };
+    load_q();
 
     // Padding columns of K meet zeros of Q: they must hold no NaN.
     if (a.D < DP) {
@@ -632,6 +696,19 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     float o[kNT][2 * NJ];
     float m[NJ], l[NJ];
     int sees[NJ], sees_least = 0;
+    auto reset = [&]() {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            m[j] = kNegInf;
+            l[j] = 0.f;
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2 * NJ; ++e)
+                o[n][e] = 0.f;
+    };
+    reset();
     bool fresh = true;       // the next tile starts a (sequence, head)
     bool first_part = true;  // still in the block's first (sequence, head)
     int t_first = 0;
@@ -640,23 +717,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
         if (fresh) {
             fresh = false;
             t_first = cur.t;
-            // Q of this (sequence, cached head): row t * G + g; a thread takes
-            // 8 values of a row, all of its loads in flight at once
-            constexpr int kUnits = DP / 8;
-            constexpr int kPasses = (S::kQRows * kUnits + kThreads - 1) / kThreads;
-            uint4 qv[kPasses];
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
-                const int d = ((int)threadIdx.x % kUnits) * 8;
-                qv[i] = make_uint4(0, 0, 0, 0);
-                if (r < a.rows && d < a.D) {
-                    const int t = a.token_of(r);
-                    qv[i] = *reinterpret_cast<const uint4 *>(
-                        a.q + cur.b * a.qb + t * a.qt +
-                        (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh + d);
-                }
-            }
+            if (!first_part)
+                load_q();
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
                 const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
@@ -697,15 +759,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             for (int j = 0; j < NJ; ++j) {
                 const int r = 16 * mt + 8 * j + g;
                 sees[j] = r < a.rows ? cur.len - (a.T - 1 - a.token_of(r)) : 0;
-                m[j] = kNegInf;
-                l[j] = 0.f;
             }
             sees_least = cur.len - (a.T - 1);
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2 * NJ; ++e)
-                    o[n][e] = 0.f;
             __syncthreads();
         }
         const int pos0 = cur.t * S::kTile + TOK * group;
@@ -890,19 +945,21 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     const uint32_t v_row = v_smem + (16 * k + 2 * c) * S::kVPitch + 4 * g;
 #pragma unroll
                     for (int nb = 0; nb < kNT; nb += 4) {
-                        uint32_t x[4][2];
+                        // bytes of two tokens interleaved before they are widened
+                        uint32_t w[4], x[2][4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            e4m3x4_f16x4(
-                                lds32(v_row + ((q & 1) + (q >> 1) * 8) * S::kVPitch + nb * 8),
-                                x[q][0], x[q][1]);
+                            w[q] = lds32(v_row + ((q & 1) + (q >> 1) * 8) * S::kVPitch + nb * 8);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                            mma_rows<true, NJ>(o[nb + j], pa[k],
-                                               __byte_perm(x[0][j / 2], x[1][j / 2], sel),
-                                               __byte_perm(x[2][j / 2], x[3][j / 2], sel));
+                        for (int q = 0; q < 2; ++q) {
+                            e4m3x4_f16x4(__byte_perm(w[2 * q], w[2 * q + 1], 0x5140), x[q][0],
+                                         x[q][1]);
+                            e4m3x4_f16x4(__byte_perm(w[2 * q], w[2 * q + 1], 0x7362), x[q][2],
+                                         x[q][3]);
                         }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            mma_rows<true, NJ>(o[nb + j], pa[k], x[0][j], x[1][j]);
                     }
                 } else {
                     const uint32_t v_row = v_smem + (16 * k + (lane & 15)) * S::kVPitch;
@@ -920,7 +977,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
         const bool ends = cur.t + 1 == cur.tiles;
         if (ends || left == 1) {
             // This block's part of the (sequence, head) is complete: join the
-            // groups, one after the other, in Q's place.
+            // groups in order, through the ring entry of the values just used.
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 l[j] += __shfl_xor_sync(kFull, l[j], 1);
@@ -938,76 +995,69 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     big = fmaxf(big, stat[w * S::kRows + 16 * mt + 8 * j + g].x);
                 f[j] = ex2(m[j] - (big == kNegInf ? 0.f : big));
             }
-            for (int w = 0; w < G; ++w) {
-                if (w == group) {
-                    // four column tiles at a time, loads before stores
-#pragma unroll
-                    for (int n0 = 0; n0 < kNT; n0 += 4)
-#pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            float *dst = merged + (16 * mt + 8 * j + g) * S::kMPitch;
-                            if constexpr (FP8) {
-                                // the four tiles' columns interleave: two runs of four
-                                float4 *p[2];
-                                float4 x[2];
-#pragma unroll
-                                for (int e = 0; e < 2; ++e) {
-                                    p[e] = reinterpret_cast<float4 *>(dst + out_col<true>(n0, c, e));
-                                    x[e] = w == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *p[e];
-                                }
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    *p[e] = make_float4(fmaf(o[n0][2 * j + e], f[j], x[e].x),
-                                                        fmaf(o[n0 + 1][2 * j + e], f[j], x[e].y),
-                                                        fmaf(o[n0 + 2][2 * j + e], f[j], x[e].z),
-                                                        fmaf(o[n0 + 3][2 * j + e], f[j], x[e].w));
-                            } else {
-                                float2 x[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    x[i] = w == 0 ? make_float2(0.f, 0.f)
-                                                  : *reinterpret_cast<const float2 *>(
-                                                        dst + out_col<false>(n0 + i, c, 0));
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    *reinterpret_cast<float2 *>(dst + out_col<false>(n0 + i, c, 0)) =
-                                        make_float2(fmaf(o[n0 + i][2 * j], f[j], x[i].x),
-                                                    fmaf(o[n0 + i][2 * j + 1], f[j], x[i].y));
-                            }
-                        }
-                }
-                __syncthreads();
-            }
             const bool whole = ends && t_first == 0;
             float *part = a.parts + (2 * (int64_t)blockIdx.x + (first_part ? 0 : 1)) * a.part_floats;
-            for (int r = warp; r < a.rows; r += kWarps) {
-                float big = kNegInf, sum = 0.f;
+            unsigned char *free_entry =
+                smem + (entry == 0 ? S::kEntries - 1 : entry - 1) * S::kEntry;
 #pragma unroll
-                for (int w = 0; w < G; ++w)
-                    big = fmaxf(big, stat[w * S::kRows + r].x);
-                const float ref = big == kNegInf ? 0.f : big;
+            for (int c0 = 0; c0 < DP; c0 += S::kRound) {
+                float *mine = reinterpret_cast<float *>(free_entry + group * S::kRing);
+                // columns are permuted by the row so that a store's lanes hit
+                // distinct banks
 #pragma unroll
-                for (int w = 0; w < G; ++w)
-                    sum += stat[w * S::kRows + r].y * ex2(stat[w * S::kRows + r].x - ref);
-                const float *src = merged + r * S::kMPitch;
-                if (whole) {
-                    const int t = a.token_of(r);
-                    const int64_t to =
-                        ((int64_t)cur.b * a.T + t) * a.Hq + cur.h * a.G + (r - t * a.G);
-                    // a row without positions (or of -inf scores only): 0
-                    const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
-                    for (int d = 2 * lane; d < a.D; d += 64)
-                        *reinterpret_cast<uint32_t *>(a.out + to * a.D + d) =
-                            pack2<false>(src[d] * inv, src[d + 1] * inv);
-                    if (a.lse && lane == 0)
-                        a.lse[to] = log_sum(big, sum);
-                } else {
-                    for (int d = 4 * lane; d < a.D; d += 128)
-                        *reinterpret_cast<float4 *>(part + r * a.D + d) =
-                            *reinterpret_cast<const float4 *>(src + d);
-                    if (lane == 0)
-                        reinterpret_cast<float2 *>(part + a.rows * a.D)[r] = make_float2(big, sum);
+                for (int j = 0; j < NJ; ++j) {
+                    const int r = 16 * mt + 8 * j + g;
+                    float *dst = mine + r * S::kRound;
+#pragma unroll
+                    for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += FP8 ? 4 : 1) {
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                *reinterpret_cast<float4 *>(
+                                    dst + ((out_col<true>(n0, c, e) - c0) ^ swizzle<true>(r))) =
+                                    make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
+                                                o[n0 + 2][2 * j + e] * f[j],
+                                                o[n0 + 3][2 * j + e] * f[j]);
+                        } else {
+                            *reinterpret_cast<float2 *>(
+                                dst + ((out_col<false>(n0, c, 0) - c0) ^ swizzle<false>(r))) =
+                                make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
+                        }
+                    }
                 }
+                __syncthreads();
+                constexpr int kCols = S::kRound / 4;
+                const int d = 4 * ((int)threadIdx.x % kCols);
+                if (c0 + d < a.D) {
+#pragma unroll 2
+                    for (int r = (int)threadIdx.x / kCols; r < a.rows; r += kThreads / kCols) {
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float big = kNegInf, sum = 0.f;
+#pragma unroll
+                        for (int w = 0; w < G; ++w) {
+                            const float4 x = *reinterpret_cast<const float4 *>(
+                                free_entry + w * S::kRing +
+                                (r * S::kRound + (d ^ swizzle<FP8>(r))) * 4);
+                            acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
+                            big = fmaxf(big, stat[w * S::kRows + r].x);
+                        }
+                        const float ref = big == kNegInf ? 0.f : big;
+#pragma unroll
+                        for (int w = 0; w < G; ++w)
+                            sum = fmaf(stat[w * S::kRows + r].y,
+                                       ex2(stat[w * S::kRows + r].x - ref), sum);
+                        if (whole) {
+                            put_row(a, cur.b, cur.h, r, c0 + d, acc, big, sum);
+                        } else {
+                            *reinterpret_cast<float4 *>(part + r * a.D + c0 + d) = acc;
+                            if (c0 + d == 0)
+                                reinterpret_cast<float2 *>(part + a.rows * a.D)[r] =
+                                    make_float2(big, sum);
+                        }
+                    }
+                }
+                if (c0 + S::kRound < DP)
+                    __syncthreads();
             }
             if (!whole) {
                 // The shares that hold the pair: those of its first and last
@@ -1034,7 +1084,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                 __syncthreads();
                 if (s_last) {
                     const int stats = a.rows * a.D;
-                    join_parts<DP, kThreads>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1),
+                    join_parts<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1),
                                              step, stats, groups == 1, cur.b, cur.h);
                     if (groups > 1) {
                         __syncthreads();
@@ -1043,7 +1093,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                                      (unsigned)groups - 1;
                         __syncthreads();
                         if (s_last)
-                            join_parts<DP, kThreads>(a, groups, slot0, slot_of(s0 + kJoin),
+                            join_parts<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(a, groups, slot0, slot_of(s0 + kJoin),
                                                      step * kJoin, stats + 2 * a.rows, true, cur.b,
                                                      cur.h);
                     }
@@ -1052,6 +1102,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             __syncthreads();
             first_part = false;
             fresh = true;
+            reset();
         }
         cur.next(a);
     }

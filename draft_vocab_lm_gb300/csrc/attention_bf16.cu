@@ -18,7 +18,7 @@ cudaError_t config_bf16(int D, int rows, AttnConfig *out)
                : rows <= 16 ? config<128, false, 1, 32, 1, 4, 2>(out)
                : rows <= 32 ? config<128, false, 2, 32, 1, 4, 1>(out)
                             : config<128, false, 4, 32, 1, 2, 1>(out);
-    return rows <= 8    ? config<256, false, 0, 16, 1, 4, 2>(out)
+    return rows <= 8    ? config<256, false, 0, 16, 1, 8, 1>(out)
            : rows <= 16 ? config<256, false, 1, 16, 1, 8, 1>(out)
            : rows <= 32 ? config<256, false, 2, 16, 1, 4, 1>(out)
                         : config<256, false, 4, 16, 1, 2, 1>(out);

@@ -9,7 +9,7 @@ namespace attn {
 cudaError_t config_fp8(int D, int rows, AttnConfig *out)
 {
     if (D <= 64)
-        return rows <= 8    ? config<64, true, 0, 32, 1, 4, 3>(out)
+        return rows <= 8    ? config<64, true, 0, 32, 1, 4, 4>(out)
                : rows <= 16 ? config<64, true, 1, 32, 1, 4, 3>(out)
                : rows <= 32 ? config<64, true, 2, 32, 1, 4, 1>(out)
                             : config<64, true, 4, 32, 1, 2, 1>(out);
