@@ -2,24 +2,27 @@
 // and the k best (beam, row) pairs of a request:
 //   score(j, n) = scores[j] + (x[j][n] - lse_j),  lse_j = m + ln sum e^{x - m}.
 //
-// Bound by HBM: each logit is read once and costs one exponential and a few
-// comparisons.  Two kernels:
-//   1. beam_scan_kernel, one block per chunk of a row, the chunk in
-//      registers: the chunk's maximum and sum of exponentials, and its best
-//      rows as packed (logit, row) keys.  Within one beam the order of the
-//      scores is that of the logits, so no score is needed here.  The k best
-//      of the chunk are found without sorting it: the k-th largest of the
-//      threads' own maxima is a lower bound of the k-th largest key, and at
-//      most k threads hold keys at or above it (keys are distinct), so a few
-//      keys (k * E at the very most) go through shared memory to one warp.
-//   2. beam_pick_kernel, one block per request: per beam the chunks' sums
-//      join into lse and the chunks' lists merge into the beam's best; then
-//      the beams' lists, now as (score, beam, place) keys, merge into the k
-//      best of the request.
-// Lists are 32 keys, one per lane of a warp, in descending order; two merge
-// by the elementwise maximum of one and the other reversed (which holds the
-// 32 largest of both as a bitonic sequence) and a five-step bitonic merge.
-// Empty places are key 0.  Nothing depends on the order blocks run in.
+// Bound by HBM: each logit is read once and costs one exponential and a
+// maximum.  One launch:
+//   - A block takes one segment of a row, in chunks that sit in registers.
+//     Every thread keeps the maximum and the sum of exponentials of what it
+//     has seen.  Within one beam the order of the scores is that of the
+//     logits, so the segment's best rows are found as packed (logit, row)
+//     keys: of the first chunk, 32 groups of 8 threads compare their maxima,
+//     and the k-th largest of those bounds the k-th largest key from below;
+//     what lies at or above the bound (a few more than k) goes to a buffer in
+//     shared memory, as does what exceeds it in later chunks.  At the end the
+//     buffer's keys count their betters, and the k best are written out.
+//   - The last block of a request (a wrapping ticket) joins the segments' sums
+//     into lse, turns keys into scores, and picks: a segment list whose head
+//     has r better heads can give its first k - r keys only.
+// Ties are exact: bounds carry the place of their logit, rows are read in
+// order, and later rows have to exceed a bound, not to reach it, so rows of
+// equal logits (a constant row, a mask of the type's lowest value) pass in
+// limited number.  A chunk that overflows the buffer all the same (rising
+// logits) is taken again in slices that fit, with the buffer cut back to its
+// k best after each.
+// Nothing depends on the order blocks run in.
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"
@@ -28,60 +31,19 @@
 namespace dvl {
 namespace {
 
-static_assert(kBeamKeys == 32 && DVL_MAX_BEAMS <= 32, "one key per lane");
+static_assert(DVL_MAX_BEAMS <= 32 && kBeamKeys >= DVL_MAX_BEAMS, "one warp's lanes cover k");
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPickThreads = 1024;
-constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kBuffer = 8 * kThreads + kBeamKeys;  // a slice of 8 logits per thread, and the best so far
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 
-// One compare-exchange step across the warp: this lane keeps the larger key
-// of the pair when `high`.
-__device__ __forceinline__ uint64_t exchange(uint64_t v, int stride, bool high)
+__device__ __forceinline__ float exp_diff(float d)  // e^d
 {
-    const uint64_t o = __shfl_xor_sync(kFull, v, stride);
-    return (o > v) == high ? o : v;
-}
-
-// Descending order across the lanes of a bitonic sequence.
-__device__ __forceinline__ uint64_t warp_bitonic_merge(uint64_t v, int lane)
-{
-#pragma unroll
-    for (int stride = 16; stride >= 1; stride >>= 1)
-        v = exchange(v, stride, (lane & stride) == 0);
-    return v;
-}
-
-__device__ __forceinline__ uint64_t warp_sort(uint64_t v, int lane)
-{
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int stride = size / 2; stride >= 1; stride >>= 1)
-            v = exchange(v, stride, ((lane & size) == 0) == ((lane & stride) == 0));
-    return v;
-}
-
-// The 32 largest of two descending lists.
-__device__ __forceinline__ uint64_t warp_merge_lists(uint64_t a, uint64_t b, int lane)
-{
-    const uint64_t r = __shfl_xor_sync(kFull, b, 31);
-    return warp_bitonic_merge(a > r ? a : r, lane);
-}
-
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1)
-        x += __shfl_xor_sync(kFull, x, off);
-    return x;
-}
-
-__device__ __forceinline__ float exp_diff(float d)  // e^d, d <= 0
-{
-    return exp2f(d * kLog2e);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * kLog2e));
+    return y;
 }
 
 // One 16-byte vector of logits as fp32.
@@ -98,226 +60,390 @@ __device__ __forceinline__ void widen(const uint4 &q, float (&v)[8])
 __device__ __forceinline__ float widen1(float x) { return x; }
 __device__ __forceinline__ float widen1(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
 
-// T: float, or uint16_t holding bf16.  E: logits per thread.  A row may start
-// anywhere: the chunks are cut at 16-byte boundaries, row index n is place
-// n + lead of the aligned sequence, and the vectors that reach over an end of
-// the row are read element by element.
+template <int N>
+__device__ __forceinline__ float max_of(const float (&v)[N])
+{
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i)
+        m = fmaxf(m, v[i]);
+    return m;
+}
+
+struct Shared {
+    uint64_t buffer[kBuffer];
+    uint64_t groups[32];
+    uint64_t best[kBeamKeys];
+    float2 sums[kWarps];
+    int n;           // keys in the buffer (may exceed its size: then it overflowed)
+    unsigned ticket;
+};
+
+// The second half's view of the same shared memory.
+constexpr int kPairs = DVL_MAX_BEAMS * (DVL_MAX_BEAMS + 1) / 2;  // keys r lists of k can give
+struct PickShared {
+    uint64_t hi[kBeamLists], lo[kBeamLists];      // heads: (score, beam), (logit, row)
+    uint64_t c_hi[kPairs], c_lo[kPairs];  // candidates
+    float lse[DVL_MAX_BEAMS];
+    int list[DVL_MAX_BEAMS];
+    int n;
+};
+
+// Cut the buffer's n keys back to the k best, in order, and return the k-th
+// (0 when there are fewer).  Every thread calls it.
+__device__ __forceinline__ uint64_t prune(Shared &s, int n, int k)
+{
+    if (threadIdx.x < kBeamKeys)
+        s.best[threadIdx.x] = 0ull;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t key = s.buffer[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            rank += s.buffer[j] > key;
+        if (rank < k)
+            s.best[rank] = key;
+    }
+    __syncthreads();
+    if (threadIdx.x < k)
+        s.buffer[threadIdx.x] = s.best[threadIdx.x];
+    if (threadIdx.x == 0)
+        s.n = n < k ? n : k;
+    const uint64_t last = s.best[k - 1];
+    __syncthreads();
+    return last;
+}
+
+// (score, beam) as a key whose order is the result's: higher score, lower beam.
+__device__ __forceinline__ uint64_t score_key(float score, int beam)
+{
+    return score > kNegInf ? make_key(score, beam) : 0ull;  // -inf and NaN: no candidate
+}
+__device__ __forceinline__ bool better(uint64_t hi, uint64_t lo, uint64_t hi2, uint64_t lo2)
+{
+    return hi > hi2 || (hi == hi2 && lo > lo2);
+}
+
+// The k best of a request, from its segments' lists.  One block.
+__device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickShared &s)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row0 = request * a.beams;
+    const int heads = a.beams * a.segments;
+    const uint64_t *keys = a.keys + row0 * a.segments * kBeamKeys;
+    for (int beam = warp; beam < a.beams; beam += kWarps) {
+        const float2 *ms = a.sums + (row0 + beam) * a.segments;
+        float m = kNegInf, sum = 0.f;
+        for (int c = lane; c < a.segments; c += 32)
+            m = fmaxf(m, __ldcg(&ms[c].x));
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+        // a row of -inf only: m - m is NaN, and so are its scores
+        for (int c = lane; c < a.segments; c += 32) {
+            const float2 x = __ldcg(&ms[c]);
+            sum += x.y * exp_diff(x.x - m);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            sum += __shfl_xor_sync(kFull, sum, off);
+        if (lane == 0)
+            s.lse[beam] = m + logf(sum);
+    }
+    if (threadIdx.x < DVL_MAX_BEAMS)
+        s.list[threadIdx.x] = -1;
+    if (threadIdx.x == 0)
+        s.n = 0;
+    __syncthreads();
+    auto score_of = [&](uint64_t key, int beam) {
+        return score_key(a.scores[row0 + beam] + (key_logit(key) - s.lse[beam]), beam);
+    };
+    for (int i = threadIdx.x; i < heads; i += kThreads) {
+        const uint64_t key = __ldcg(keys + (int64_t)i * kBeamKeys);
+        s.lo[i] = key;
+        s.hi[i] = key ? score_of(key, i / a.segments) : 0ull;
+    }
+    __syncthreads();
+    // the lists in the order of their heads, k at most
+    for (int i = threadIdx.x; i < heads; i += kThreads) {
+        const uint64_t hi = s.hi[i], lo = s.lo[i];
+        if (hi == 0ull)
+            continue;
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < heads; ++j)
+            rank += better(s.hi[j], s.lo[j], hi, lo);
+        if (rank < a.k)
+            s.list[rank] = i;
+    }
+    __syncthreads();
+    // what is no better than the k-th head is none of the k best
+    const int last = s.list[a.k - 1];
+    const uint64_t floor_hi = last >= 0 ? s.hi[last] : 1ull, floor_lo = last >= 0 ? s.lo[last] : 0ull;
+    for (int i = threadIdx.x; i < a.k * a.k; i += kThreads) {
+        const int r = i / a.k, j = i - r * a.k, list = s.list[r];
+        if (r + j >= a.k || list < 0)
+            continue;
+        const uint64_t key = __ldcg(keys + (int64_t)list * kBeamKeys + j);
+        const uint64_t hi = key ? score_of(key, list / a.segments) : 0ull;
+        if (hi && !better(floor_hi, floor_lo, hi, key)) {
+            const int at = atomicAdd(&s.n, 1);
+            s.c_hi[at] = hi;
+            s.c_lo[at] = key;
+        }
+    }
+    __syncthreads();
+    const int n = s.n;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t hi = s.c_hi[i], lo = s.c_lo[i];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j)
+            rank += better(s.c_hi[j], s.c_lo[j], hi, lo);
+        if (rank < a.k) {
+            const int64_t o = request * a.k + rank;
+            const int row = key_id(lo);
+            a.out_scores[o] = key_logit(hi);
+            a.parents[o] = key_id(hi);
+            a.tokens[o] = a.d2t ? a.d2t[row] : row;
+        }
+    }
+    for (int i = n + threadIdx.x; i < a.k; i += kThreads) {
+        const int64_t o = request * a.k + i;
+        a.out_scores[o] = kNegInf;
+        a.parents[o] = -1;
+        a.tokens[o] = -1;
+    }
+}
+
+// T: float, or uint16_t holding bf16.  E: logits per thread and chunk.  A row
+// may start anywhere: row index n is place n + lead of a sequence aligned to
+// 16 bytes, segments are cut at such boundaries, and the vectors that reach
+// over an end of the row are read element by element.
 template <typename T, int E>
-__global__ void __launch_bounds__(kThreads) beam_scan_kernel(const BeamArgs a)
+__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a)
 {
     constexpr int V = 16 / sizeof(T);
     constexpr int NV = E / V;
-    constexpr int kMost = 32 * E;  // keys that can reach the threshold
-    __shared__ uint64_t lists[kWarps][32];
-    __shared__ uint64_t passed[kMost];
-    __shared__ uint64_t s_thr;
-    __shared__ float s_sum[kWarps];
-    __shared__ int s_n;
+    static_assert(V * kThreads + kBeamKeys <= kBuffer, "a slice fits the buffer");
+    __shared__ union {
+        Shared scan;
+        PickShared pick;
+    } sm;
+    Shared &s = sm.scan;
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x / a.chunks;
-    const int chunk = (int)(blockIdx.x - row * a.chunks);
-    uint64_t *out = a.keys + (row * a.chunks + chunk) * kBeamKeys;
-    if (!(a.scores[row] > kNegInf)) {  // a dead beam
+    const int64_t row = blockIdx.x / a.segments;
+    const int segment = (int)(blockIdx.x - row * a.segments);
+    const int64_t request = row / a.beams;
+    const int k = a.k;
+    uint64_t *out = a.keys + (int64_t)blockIdx.x * kBeamKeys;
+
+    if (a.scores[row] > kNegInf) {
+        const T *x = static_cast<const T *>(a.logits) + request * a.batch_stride +
+                     (row - request * a.beams) * a.beam_stride;
+        const int lead = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % V);
+        const int begin = segment * a.length - lead;  // of the segment, a multiple of V past the lead
+        const int end = min(begin + a.length, a.N);
+        float m = kNegInf, sum = 0.f;
+        float bound = kNegInf;  // later rows must exceed it
+        if (threadIdx.x == 0)
+            s.n = 0;
+        for (int base = begin; base < end; base += kThreads * E) {
+            const int first = base + (int)threadIdx.x * V;
+            float v[NV][V];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int n = first + j * kThreads * V;
+                if (n >= 0 && n + V <= end) {
+                    widen(ld_stream16(x + n), v[j]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        v[j][e] = n + e >= 0 && n + e < end ? widen1(x[n + e]) : kNegInf;
+                }
+            }
+            float top = max_of(v[0]);
+            int top_j = 0;
+#pragma unroll
+            for (int j = 1; j < NV; ++j) {
+                const float t = max_of(v[j]);
+                if (t > top) {
+                    top = t;
+                    top_j = j;
+                }
+            }
+            // the place up to which logits equal to the bound pass
+            int place = -1;
+            if (base == begin) {
+                uint64_t key = top > kNegInf ? make_key(top, top_j * kThreads + threadIdx.x) : 0ull;
+#pragma unroll
+                for (int off = 1; off < 8; off <<= 1) {
+                    const uint64_t o = __shfl_xor_sync(kFull, key, off);
+                    key = o > key ? o : key;
+                }
+                if ((lane & 7) == 0)
+                    s.groups[threadIdx.x >> 3] = key;
+                __syncthreads();
+                key = s.groups[lane];
+                int rank = 0;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const uint64_t o = s.groups[j];
+                    rank += o > key || (o == key && j < lane);  // (empty groups are equal)
+                }
+                key = __shfl_sync(kFull, key, __ffs(__ballot_sync(kFull, rank == k - 1)) - 1);
+                if (key) {
+                    bound = key_logit(key);
+                    place = key_id(key);
+                }
+            }
+
+            const float m_new = fmaxf(m, top);
+            const float ref = m_new == kNegInf ? 0.f : m_new;
+            sum *= exp_diff(m - ref);
+            m = m_new;
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    sum += exp_diff(v[j][e] - ref);
+
+            // keys past the bound into the buffer; with no bound yet, all of them
+            auto passes = [&](float t, int j) {
+                return t > bound || (t == bound && j * kThreads + (int)threadIdx.x <= place);
+            };
+            if (top >= bound) {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (max_of(v[j]) >= bound)
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            if (passes(v[j][e], j)) {
+                                const int at = atomicAdd(&s.n, 1);
+                                if (at < kBuffer)
+                                    s.buffer[at] = make_key(v[j][e], first + j * kThreads * V + e);
+                            }
+            }
+            __syncthreads();
+            const int count = s.n;
+            __syncthreads();
+            if (count > kBuffer) {
+                // Take the chunk again slice by slice.  Of what the buffer
+                // holds, the keys of earlier chunks stay.
+                if (threadIdx.x == 0) {
+                    int kept = 0;
+                    for (int i = 0; i < kBuffer; ++i)
+                        if (key_id(s.buffer[i]) < base)
+                            s.buffer[kept++] = s.buffer[i];
+                    s.n = kept;
+                }
+                __syncthreads();
+                const int kept = s.n;
+                __syncthreads();
+                uint64_t kth = prune(s, kept, k);
+                float least = kth ? key_logit(kth) : kNegInf;
+#pragma unroll
+                for (int j = 0; j < NV; ++j) {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (v[j][e] > least)
+                            s.buffer[atomicAdd(&s.n, 1)] =
+                                make_key(v[j][e], first + j * kThreads * V + e);
+                    __syncthreads();
+                    const int n = s.n;
+                    __syncthreads();
+                    kth = prune(s, n, k);
+                    least = kth ? key_logit(kth) : kNegInf;
+                }
+                bound = least;
+            } else if (count > kBuffer / 2) {
+                const uint64_t kth = prune(s, count, k);
+                if (kth)
+                    bound = key_logit(kth);
+            }
+        }
+        // the block's sum relative to its maximum
+        float big = m;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            big = fmaxf(big, __shfl_xor_sync(kFull, big, off));
+        sum *= exp_diff(m - (big == kNegInf ? 0.f : big));
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+            sum += __shfl_xor_sync(kFull, sum, off);
+        if (lane == 0)
+            s.sums[warp] = make_float2(big, sum);
         if (threadIdx.x < kBeamKeys)
             out[threadIdx.x] = 0ull;
-        return;
-    }
-    const int64_t b = row / a.beams;
-    const T *x = static_cast<const T *>(a.logits) + b * a.batch_stride +
-                 (row - b * a.beams) * a.beam_stride;
-    const int lead = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % V);
-    const int first = chunk * (kThreads * E) - lead + (int)threadIdx.x * V;
-
-    float v[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int n = first + j * kThreads * V;
-        if (n >= 0 && n + V <= a.N) {
-            widen(ld_stream16(x + n), v[j]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                v[j][e] = n + e >= 0 && n + e < a.N ? widen1(x[n + e]) : kNegInf;
+        __syncthreads();
+        // the buffer's k best, each key at the place of its rank
+        const int n = s.n;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint64_t key = s.buffer[i];
+            int rank = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j)
+                rank += s.buffer[j] > key;
+            if (rank < k)
+                out[rank] = key;
         }
+        if (threadIdx.x == 0) {
+            big = kNegInf;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                big = fmaxf(big, s.sums[w].x);
+            sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w)
+                sum += s.sums[w].y * exp_diff(s.sums[w].x - (big == kNegInf ? 0.f : big));
+            a.sums[blockIdx.x] = make_float2(big, sum);
+        }
+    } else {  // a dead beam
+        if (threadIdx.x < kBeamKeys)
+            out[threadIdx.x] = 0ull;
+        if (threadIdx.x == 0)
+            a.sums[blockIdx.x] = make_float2(kNegInf, 0.f);
     }
-
-    // the thread's best key: the lowest row among equal logits; -inf and NaN
-    // are no candidates
-    float best = kNegInf;
-    int at = 0;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            if (v[j][e] > best) {
-                best = v[j][e];
-                at = first + j * kThreads * V + e;
-            }
-    const uint64_t mine = best > kNegInf ? make_key(best, at) : 0ull;
-    lists[warp][lane] = warp_sort(mine, lane);
+    __syncthreads();
+    const unsigned blocks = (unsigned)(a.beams * a.segments);
     if (threadIdx.x == 0)
-        s_n = 0;
+        s.ticket = ticket_inc(a.tickets + request, blocks - 1);
     __syncthreads();
-
-    uint64_t top = lists[0][0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w)
-        top = lists[w][0] > top ? lists[w][0] : top;
-    const float m = top ? key_logit(top) : kNegInf;
-    const float m_use = top ? m : 0.f;
-    if (warp == 0) {
-        uint64_t l = lists[0][lane];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w)
-            l = warp_merge_lists(l, lists[w][lane], lane);
-        if (lane == a.k - 1)
-            s_thr = l;
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-            sum += exp_diff(v[j][e] - m_use);
-    sum = warp_sum(sum);
-    if (lane == 0)
-        s_sum[warp] = sum;
+    const bool last = s.ticket == blocks - 1;
     __syncthreads();
-
-    const uint64_t thr = s_thr;
-    if (mine && mine >= thr) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (v[j][e] > kNegInf) {
-                    const uint64_t key = make_key(v[j][e], first + j * kThreads * V + e);
-                    if (key >= thr)
-                        passed[atomicAdd(&s_n, 1)] = key;
-                }
-    }
-    __syncthreads();
-    if (warp == 0) {
-        const int n = s_n;
-        uint64_t l = warp_sort(lane < n ? passed[lane] : 0ull, lane);
-        for (int i = 32; i < n; i += 32)
-            l = warp_merge_lists(l, warp_sort(i + lane < n ? passed[i + lane] : 0ull, lane), lane);
-        out[lane] = l;
-        const float s = warp_sum(lane < kWarps ? s_sum[lane] : 0.f);
-        if (lane == 0)
-            a.sums[row * a.chunks + chunk] = make_float2(m, s);
-    }
+    if (last)
+        pick(a, request, sm.pick);
 }
 
-__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamArgs a)
-{
-    __shared__ uint64_t lists[kPickWarps][32];
-    __shared__ int rows[DVL_MAX_BEAMS][32];
-    __shared__ float s_lse[DVL_MAX_BEAMS];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row0 = (int64_t)blockIdx.x * a.beams;
-    const int per_beam = kPickWarps / a.beams;  // warps per beam, >= 1
-    const int beam = warp / per_beam, sub = warp - beam * per_beam;
-    const bool live = beam < a.beams && a.scores[row0 + beam] > kNegInf;
-
-    uint64_t l = 0ull;
-    if (live) {
-        const uint64_t *src = a.keys + (row0 + beam) * a.chunks * kBeamKeys + lane;
-        for (int c = sub; c < a.chunks; c += per_beam)
-            l = warp_merge_lists(l, src[(int64_t)c * kBeamKeys], lane);
-        if (sub == 0) {
-            const float2 *ms = a.sums + (row0 + beam) * a.chunks;
-            float m = kNegInf, s = 0.f;
-            for (int c = lane; c < a.chunks; c += 32)
-                m = fmaxf(m, ms[c].x);
-#pragma unroll
-            for (int off = 16; off >= 1; off >>= 1)
-                m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-            // a row of -inf only: m - m is NaN, and so are its scores
-            for (int c = lane; c < a.chunks; c += 32)
-                s += ms[c].y * exp_diff(ms[c].x - m);
-            s = warp_sum(s);
-            if (lane == 0)
-                s_lse[beam] = m + logf(s);
-        }
-    }
-    lists[warp][lane] = l;
-    __syncthreads();
-
-    // warp j: beam j's best, as (score, beam, place) keys
-    l = 0ull;
-    if (warp < a.beams) {
-        for (int w = 0; w < per_beam; ++w) {
-            const uint64_t o = lists[warp * per_beam + w][lane];
-            l = w == 0 ? o : warp_merge_lists(l, o, lane);
-        }
-        rows[warp][lane] = key_id(l);
-        if (l) {
-            const float score = a.scores[row0 + warp] + (key_logit(l) - s_lse[warp]);
-            l = score > kNegInf ? make_key(score, warp * 32 + lane) : 0ull;
-        }
-    }
-    __syncthreads();
-    if (warp < a.beams)
-        lists[warp][lane] = l;
-    __syncthreads();
-    if (warp == 0) {
-        for (int w = 1; w < a.beams; ++w)
-            l = warp_merge_lists(l, lists[w][lane], lane);
-        if (lane < a.k) {
-            const int64_t o = (int64_t)blockIdx.x * a.k + lane;
-            if (l) {
-                const int place = key_id(l);
-                const int n = rows[place >> 5][place & 31];
-                a.out_scores[o] = key_logit(l);
-                a.parents[o] = place >> 5;
-                a.tokens[o] = a.d2t ? a.d2t[n] : n;
-            } else {
-                a.out_scores[o] = kNegInf;
-                a.parents[o] = -1;
-                a.tokens[o] = -1;
-            }
-        }
-    }
-}
-
-constexpr int kLong = 32, kShort = 8;  // logits per thread
-
-template <typename T>
-cudaError_t launch_scan(const BeamArgs &a, cudaStream_t s)
-{
-    const int64_t rows = (int64_t)a.batch * a.beams;
-    const unsigned grid = (unsigned)(rows * a.chunks);
-    if (beam_chunk(rows, a.N) == kThreads * kLong)
-        return launch_pdl(beam_scan_kernel<T, kLong>, grid, kThreads, 0, s, a);
-    return launch_pdl(beam_scan_kernel<T, kShort>, grid, kThreads, 0, s, a);
-}
+constexpr int kLong = 32, kShort = 8;  // logits per thread and chunk
 
 }  // namespace
 
-// Long chunks cost fewer lists; short ones spread a small call over more SMs.
-int beam_chunk(int64_t rows, int N)
+// Segments of a row: as many as fill the SMs, of 2,048 logits at least.
+int beam_segments(int64_t rows, int N)
 {
-    return kThreads * (rows * N >= (1 << 20) ? kLong : kShort);
+    const int64_t most = ((int64_t)N + 7 + kThreads * kShort - 1) / (kThreads * kShort);
+    int64_t n = rows > 0 && rows < kBeamLists ? kBeamLists / rows : 1;
+    return (int)(n < most ? n : most);
 }
 
-int beam_chunks(int64_t rows, int N)
+cudaError_t launch_beam_select(BeamArgs &a, int dtype, cudaStream_t s)
 {
-    const int c = beam_chunk(rows, N);
-    return (int)(((int64_t)N + 7 + c - 1) / c);  // up to 7 places before a row's start
-}
-
-cudaError_t launch_beam_select(const BeamArgs &a, int dtype, cudaStream_t s)
-{
-    const cudaError_t e =
-        dtype == DVL_F32 ? launch_scan<float>(a, s) : launch_scan<uint16_t>(a, s);
-    if (e != cudaSuccess)
-        return e;
-    return launch_pdl(beam_pick_kernel, (unsigned)a.batch, kPickThreads, 0, s, a);
+    const int64_t rows = (int64_t)a.batch * a.beams;
+    // up to 7 places before a row's start; lengths are multiples of a vector
+    a.length = (int)((((int64_t)a.N + 7 + a.segments - 1) / a.segments + 7) / 8 * 8);
+    const unsigned grid = (unsigned)(rows * a.segments);
+    // Chunks of 8,192 logits keep the loads of a long segment in flight; a
+    // segment of one short chunk or two runs less code per logit it lacks.
+    const bool lng = a.length > 2 * kThreads * kShort;
+    if (dtype == DVL_F32)
+        return lng ? launch_pdl(beam_select_kernel<float, kLong>, grid, kThreads, 0, s, a)
+                   : launch_pdl(beam_select_kernel<float, kShort>, grid, kThreads, 0, s, a);
+    return lng ? launch_pdl(beam_select_kernel<uint16_t, kLong>, grid, kThreads, 0, s, a)
+               : launch_pdl(beam_select_kernel<uint16_t, kShort>, grid, kThreads, 0, s, a);
 }
 
 }  // namespace dvl

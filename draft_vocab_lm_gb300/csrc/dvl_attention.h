@@ -19,8 +19,8 @@ struct AttnArgs {
     uint16_t *out;            // bf16 [B][T][Hq][D]
     float *lse;               // [B][T][Hq] or nullptr
     unsigned char *ws;        // its header holds the status word
-    unsigned int *tickets;    // [2 * blocks] of parts, then as many of groups of parts
-    int top_tickets;          // 2 * blocks
+    unsigned int *tickets;    // one per part slot; top_tickets on, one per joined pair
+    int top_tickets;
     float *parts;             // [2 * blocks][part_floats]
     int64_t part_floats;      // rows * D sums, (maximum, sum) per row, the same of a joined group
     int B, T, Hq, heads, G, D;

@@ -10,9 +10,10 @@ namespace dvl {
 // Residual addition and norm; the arguments are dvl_norm's, checked.
 cudaError_t launch_add_rmsnorm(const dvl_norm &a, cudaStream_t s);
 
-// Beam selection.  A row of logits is scanned in chunks, each leaving the
-// kBeamKeys best of it and its part of the row's sum of exponentials.
-constexpr int kBeamKeys = 32;  // keys per chunk list (>= DVL_MAX_BEAMS)
+// Beam selection.  A row of logits is cut into segments, each leaving its best
+// keys and its part of the row's sum of exponentials.
+constexpr int kBeamKeys = 32;    // keys per segment list (>= DVL_MAX_BEAMS)
+constexpr int kBeamLists = 608;  // blocks the segments are cut for: four per SM
 struct BeamArgs {
     const void *logits;
     int64_t batch_stride, beam_stride;  // elements
@@ -21,13 +22,13 @@ struct BeamArgs {
     float *out_scores;                  // [batch][k]
     int32_t *parents, *tokens;          // [batch][k]
     int batch, beams, N, k;
-    int chunks;                         // per row
-    uint64_t *keys;                     // [batch * beams][chunks][kBeamKeys]
-    float2 *sums;                       // [batch * beams][chunks]: maximum, sum
+    int segments, length;               // per row; logits of one
+    unsigned int *tickets;              // [batch]
+    uint64_t *keys;                     // [batch * beams][segments][kBeamKeys]
+    float2 *sums;                       // [batch * beams][segments]: maximum, sum
 };
-int beam_chunk(int64_t rows, int N);    // logits per chunk
-int beam_chunks(int64_t rows, int N);   // chunks per row
-cudaError_t launch_beam_select(const BeamArgs &a, int dtype, cudaStream_t s);
+int beam_segments(int64_t rows, int N);
+cudaError_t launch_beam_select(BeamArgs &a, int dtype, cudaStream_t s);
 
 // Reordering: every copied row is cut into pieces of at most kPiece bytes,
 // one thread block each.

@@ -57,17 +57,29 @@ int query_rows(const dvl_kv_cache *c, int32_t T, int32_t Hq)
 // room for those of a joined group.
 int64_t part_floats(int rows, int D) { return (int64_t)rows * (D + 4); }
 
+// Both workspaces begin with the header and a fixed number of tickets, so that
+// calls of different sizes can share one: no call's data lies where another
+// expects its tickets at zero.
+constexpr size_t kTicketBytes = 4 * kMaxCtas * sizeof(unsigned int);
+constexpr int kBeamRequests = 4 * kMaxCtas;  // requests per launch
+
 size_t attention_bytes(int blocks, int rows, int D)
 {
-    return kWsSlots + (size_t)4 * blocks * sizeof(unsigned int) +
-           (size_t)2 * blocks * part_floats(rows, D) * sizeof(float);
+    return kWsSlots + kTicketBytes + (size_t)2 * blocks * part_floats(rows, D) * sizeof(float);
 }
 
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)
 {
     return batch >= 0 && beams >= 1 && beams <= DVL_MAX_BEAMS && N >= 1 &&
-           N <= 0x7fffffff - 65536 &&
-           (int64_t)batch * beams * beam_chunks((int64_t)batch * beams, N) <= 0x7fffffffLL;
+           N <= 0x7fffffff - 65536 && (int64_t)batch * beams <= 0x7fffffffLL;
+}
+
+// Lists of one launch: at least kBeamLists, so that the size grows with the
+// batch although fewer rows are cut into more segments.
+int64_t beam_lists(int32_t batch, int32_t beams)
+{
+    const int64_t rows = (int64_t)(batch < kBeamRequests ? batch : kBeamRequests) * beams;
+    return rows > kBeamLists ? rows : kBeamLists;
 }
 
 }  // namespace
@@ -168,8 +180,8 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.lse = lse;
     a.ws = static_cast<unsigned char *>(ws);
     a.tickets = reinterpret_cast<unsigned int *>(a.ws + kWsSlots);
-    a.top_tickets = 2 * a.blocks;
-    a.parts = reinterpret_cast<float *>(a.tickets + 4 * a.blocks);
+    a.top_tickets = 2 * kMaxCtas;
+    a.parts = reinterpret_cast<float *>(a.ws + kWsSlots + kTicketBytes);
     a.part_floats = part_floats(rows, cache->D);
     a.B = B;
     a.T = T;
@@ -198,9 +210,8 @@ size_t dvl_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t N)
 {
     if (!beam_sizes_ok(batch, beams, N))
         return 0;
-    const int64_t rows = (int64_t)batch * beams;
-    return kWsSlots +
-           (size_t)rows * beam_chunks(rows, N) * (kBeamKeys * sizeof(uint64_t) + sizeof(float2));
+    return kWsSlots + kTicketBytes +
+           (size_t)beam_lists(batch, beams) * (kBeamKeys * sizeof(uint64_t) + sizeof(float2));
 }
 
 dvl_status dvl_beam_select(const void *logits, int32_t dtype, int64_t batch_stride,
@@ -223,24 +234,32 @@ dvl_status dvl_beam_select(const void *logits, int32_t dtype, int64_t batch_stri
         return DVL_ERR_WORKSPACE;
     if (batch == 0)
         return DVL_OK;
-    BeamArgs a;
-    const int64_t rows = (int64_t)batch * beams;
-    a.logits = logits;
-    a.batch_stride = batch_stride;
-    a.beam_stride = beam_stride;
-    a.scores = scores;
-    a.d2t = d2t;
-    a.out_scores = out_scores;
-    a.parents = parents;
-    a.tokens = tokens;
-    a.batch = batch;
-    a.beams = beams;
-    a.N = N;
-    a.k = k;
-    a.chunks = beam_chunks(rows, N);
-    a.keys = reinterpret_cast<uint64_t *>(static_cast<unsigned char *>(ws) + kWsSlots);
-    a.sums = reinterpret_cast<float2 *>(a.keys + rows * a.chunks * kBeamKeys);
-    return done(launch_beam_select(a, dtype, static_cast<cudaStream_t>(stream)));
+    for (int32_t b0 = 0; b0 < batch; b0 += kBeamRequests) {
+        BeamArgs a;
+        a.batch = batch - b0 < kBeamRequests ? batch - b0 : kBeamRequests;
+        a.logits = static_cast<const unsigned char *>(logits) +
+                   (int64_t)b0 * batch_stride * (dtype == DVL_F32 ? 4 : 2);
+        a.batch_stride = batch_stride;
+        a.beam_stride = beam_stride;
+        a.scores = scores + (int64_t)b0 * beams;
+        a.d2t = d2t;
+        a.out_scores = out_scores + (int64_t)b0 * k;
+        a.parents = parents + (int64_t)b0 * k;
+        a.tokens = tokens + (int64_t)b0 * k;
+        a.beams = beams;
+        a.N = N;
+        a.k = k;
+        const int64_t rows = (int64_t)a.batch * beams;
+        a.segments = beam_segments(rows, N);
+        unsigned char *at = static_cast<unsigned char *>(ws) + kWsSlots;
+        a.tickets = reinterpret_cast<unsigned int *>(at);
+        a.keys = reinterpret_cast<uint64_t *>(at + kTicketBytes);
+        a.sums = reinterpret_cast<float2 *>(a.keys + rows * a.segments * kBeamKeys);
+        const cudaError_t e = launch_beam_select(a, dtype, static_cast<cudaStream_t>(stream));
+        if (e != cudaSuccess)
+            return cuda_failed(e);
+    }
+    return DVL_OK;
 }
 
 dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl_beam_pages *pages,

@@ -351,8 +351,9 @@ typedef struct dvl_kv_cache {
 /* Bytes of device workspace a dvl_paged_attention call with this cache, T new
  * tokens and Hq query heads needs on the current device, whatever the batch
  * and its lengths.  0 for arguments outside the limits or without a device.
- * Zero it once (dvl_workspace_init); dvl_workspace_status reads its status
- * word. */
+ * Zero it once (dvl_workspace_init); every call leaves it as it found it.
+ * Attention calls of any sizes that fit may share one, calls of other entry
+ * points may not.  dvl_workspace_status reads its status word. */
 size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32_t Hq);
 
 /* Attention of the T newest tokens of each of B sequences over their cached
@@ -391,7 +392,8 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
 
 /* Bytes of device workspace a dvl_beam_select call needs; 0 for arguments
  * outside the limits.  Zero it once (dvl_workspace_init); every call leaves
- * it as it found it. */
+ * it as it found it.  Selections of any sizes that fit may share one, calls
+ * of other entry points may not. */
 size_t dvl_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t N);
 
 /* Beam search's choice of the next beams.  For request b, beam j and row n of

@@ -235,7 +235,13 @@ def test_attention_status_and_workspace_reuse(dvl):
     c.lengths = torch.tensor([100, 112, -5], dtype=torch.int32, device="cuda")
     c.verify(c.call(dvl, ws=ws))
     assert dvl.workspace_status(ws) == 0
-    # the same workspace serves other batches
+    # the same workspace serves other batches, and other shapes that fit
+    ws = dvl.attention_workspace(dvl.KVCache(torch.zeros(1, 1, 2, 256, dtype=torch.bfloat16, device="cuda"),
+                                             torch.zeros(1, 1, 2, 256, dtype=torch.bfloat16, device="cuda")), 1, 8, 16)
+    for T, Hq, D in [(1, 4, 64), (8, 8, 256), (2, 16, 128), (1, 4, 64), (3, 10, 256), (1, 2, 128)]:
+        for fp8 in (False, True):
+            x = Case(T * D + Hq, [900, 5, 3000, 129], T, Hq, 2, D, 64, fp8)
+            x.verify(x.call(dvl, ws=ws))
     other = Case(12, [5000, 1], 1, 4, 2, 64, 16)
     other.verify(other.call(dvl, ws=ws))
 

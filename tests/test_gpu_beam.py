@@ -110,6 +110,24 @@ def test_beam_all_equal_logits(dvl):
         assert np.allclose(out.cpu().numpy(), -np.log(N), atol=1e-5)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_beam_rows_that_overflow_the_buffer(dvl, bf16):
+    # rising logits pass every bound set so far; falling ones none
+    N = 70000
+    up = torch.linspace(-20, 20, N)
+    saw = torch.arange(N).remainder(9000).float() / 300
+    logits = torch.stack([up, up.flip(0), saw, torch.full((N,), torch.finfo(torch.float32).min)])[None]
+    logits[0, 3, 69990:] = torch.arange(10).float()  # ten rows that a mask of the lowest value leaves
+    scores = torch.tensor([[0.0, -0.5, 3.0, 1.0]])
+    x = logits.bfloat16() if bf16 else logits
+    for k in (4, 32):
+        verify(x.float().numpy(), scores.numpy(), k, dvl.beam_select(x.cuda(), scores.cuda(), k))
+    # each row by itself: every place of the selection is its own
+    for j in range(4):
+        verify(x[:, j:j + 1].float().numpy(), scores[:, j:j + 1].numpy(), 32,
+               dvl.beam_select(x[:, j:j + 1].cuda(), scores[:, j:j + 1].contiguous().cuda(), 32))
+
+
 def test_beam_masked_dead_and_non_finite(dvl):
     logits, scores = make(3, 6, 4, 5000)
     scores[0, 1:] = -INF            # the first step: one live beam

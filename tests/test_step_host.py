@@ -102,7 +102,7 @@ def select(L, **kw):
     dict(dtype=1), dict(dtype=2), dict(logits=None), dict(logits=0x1002), dict(dtype=0, logits=0x1001), dict(bs=-1),
     dict(js=-1), dict(scores=None), dict(scores=0x2002), dict(batch=-1), dict(beams=0), dict(beams=33), dict(N=0),
     dict(N=0x7fffffff), dict(k=0), dict(k=33), dict(d2t=0x2), dict(out=None), dict(parents=None), dict(tokens=0x5001),
-    dict(batch=1 << 30, beams=32),
+    dict(batch=1 << 27, beams=32),
 ])
 def test_beam_checks(L, bad):
     assert select(L, **bad) == 1
@@ -112,8 +112,10 @@ def test_beam_workspace(L):
     assert select(L, ws=None) == 4 and select(L, ws=0x6008) == 4 and select(L, bytes=100) == 4
     assert select(L, batch=0) == 0
     assert L.dvl_beam_workspace_bytes(1, 33, 10) == 0 and L.dvl_beam_workspace_bytes(1, 1, 0) == 0
-    # a short call keeps one list of 32 keys and one sum per 2,048 places
-    assert L.dvl_beam_workspace_bytes(1, 4, 16000) == 512 + 4 * 8 * (32 * 8 + 8)
+    # header, tickets, and one list of 32 keys and one sum per segment: at least 608
+    need = [L.dvl_beam_workspace_bytes(b, 4, 16000) for b in (1, 100, 200, 5000)]
+    assert need[0] == need[1] == 512 + 16384 + 608 * (32 * 8 + 8)
+    assert need[2] == 512 + 16384 + 800 * (32 * 8 + 8) and need[3] == 512 + 16384 + 16384 * (32 * 8 + 8)
 
 
 def reorder(L, cache=None, n=1, parents=0x9000, batch=2, beams=3, k=3, state=None, pages=None):
