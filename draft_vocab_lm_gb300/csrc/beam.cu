@@ -19,9 +19,11 @@
 // Ties are exact: bounds carry the place of their logit, rows are read in
 // order, and later rows have to exceed a bound, not to reach it, so rows of
 // equal logits (a constant row, a mask of the type's lowest value) pass in
-// limited number.  A chunk that overflows the buffer all the same (rising
-// logits) is taken again in slices that fit, with the buffer cut back to its
-// k best after each.
+// limited number.  A segment that overflows the buffer all the same (rising
+// logits) is read again in slices that fit, with the buffer cut back to its
+// k best after each.  After chunk 1, 2, 4, 8 .. the block looks at the buffer:
+// cutting it back gives a higher bound for the chunks to come (a chunk passes
+// about k / c keys after c chunks).  No other barrier stands in the loop.
 // Nothing depends on the order blocks run in.
 #include <cuda_runtime.h>
 
@@ -57,8 +59,30 @@ __device__ __forceinline__ void widen(const uint4 &q, float (&v)[8])
     v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
     v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
 }
-__device__ __forceinline__ float widen1(float x) { return x; }
-__device__ __forceinline__ float widen1(uint16_t x) { return __uint_as_float((uint32_t)x << 16); }
+// The vector at row index n, -inf outside [0, end).
+__device__ __forceinline__ uint4 load_vector(const float *x, int n, int end)
+{
+    if (n >= 0 && n + 4 <= end)
+        return ld_stream16(x + n);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        w[e] = n + e >= 0 && n + e < end ? __float_as_uint(x[n + e]) : 0xff800000u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 load_vector(const uint16_t *x, int n, int end)
+{
+    if (n >= 0 && n + 8 <= end)
+        return ld_stream16(x + n);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = n + 2 * e;
+        w[e] = (i >= 0 && i < end ? x[i] : 0xff80u) |
+               (uint32_t)(i + 1 >= 0 && i + 1 < end ? x[i + 1] : 0xff80u) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 template <int N>
 __device__ __forceinline__ float max_of(const float (&v)[N])
@@ -82,11 +106,13 @@ struct Shared {
 // The second half's view of the same shared memory.
 constexpr int kPairs = DVL_MAX_BEAMS * (DVL_MAX_BEAMS + 1) / 2;  // keys r lists of k can give
 struct PickShared {
-    uint64_t hi[kBeamLists], lo[kBeamLists];      // heads: (score, beam), (logit, row)
+    uint64_t hi[kBeamLists], lo[kBeamLists];  // heads: (score, beam), (logit, row)
+    int16_t list_of[kBeamLists];
     uint64_t c_hi[kPairs], c_lo[kPairs];  // candidates
+    uint64_t groups[32];
     float lse[DVL_MAX_BEAMS];
-    int list[DVL_MAX_BEAMS];
-    int n;
+    int head[DVL_MAX_BEAMS];              // the k best heads, in order
+    int n_heads, n;
 };
 
 // Cut the buffer's n keys back to the k best, in order, and return the k-th
@@ -115,6 +141,30 @@ __device__ __forceinline__ uint64_t prune(Shared &s, int n, int k)
     return last;
 }
 
+// A bound from below of the k-th largest of the block's keys `mine` (0: none):
+// the k-th largest of the maxima of 32 groups of 8 threads; 0 when fewer than
+// k groups have a key.  Every thread calls it.
+__device__ __forceinline__ uint64_t group_bound(uint64_t *groups, uint64_t mine, int k)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) {
+        const uint64_t o = __shfl_xor_sync(kFull, mine, off);
+        mine = o > mine ? o : mine;
+    }
+    if ((lane & 7) == 0)
+        groups[threadIdx.x >> 3] = mine;
+    __syncthreads();
+    mine = groups[lane];
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint64_t o = groups[j];
+        rank += o > mine || (o == mine && j < lane);  // (empty groups are equal)
+    }
+    return __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == k - 1)) - 1);
+}
+
 // (score, beam) as a key whose order is the result's: higher score, lower beam.
 __device__ __forceinline__ uint64_t score_key(float score, int beam)
 {
@@ -132,6 +182,13 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     const int64_t row0 = request * a.beams;
     const int heads = a.beams * a.segments;
     const uint64_t *keys = a.keys + row0 * a.segments * kBeamKeys;
+    constexpr int kHeads = (kBeamLists + kThreads - 1) / kThreads;  // per thread
+    uint64_t head[kHeads];  // in flight while the sums are joined
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int list = i * kThreads + (int)threadIdx.x;
+        head[i] = list < heads ? __ldcg(keys + (int64_t)list * kBeamKeys) : 0ull;
+    }
     for (int beam = warp; beam < a.beams; beam += kWarps) {
         const float2 *ms = a.sums + (row0 + beam) * a.segments;
         float m = kNegInf, sum = 0.f;
@@ -152,39 +209,50 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
             s.lse[beam] = m + logf(sum);
     }
     if (threadIdx.x < DVL_MAX_BEAMS)
-        s.list[threadIdx.x] = -1;
+        s.head[threadIdx.x] = -1;
     if (threadIdx.x == 0)
-        s.n = 0;
+        s.n = s.n_heads = 0;
     __syncthreads();
     auto score_of = [&](uint64_t key, int beam) {
         return score_key(a.scores[row0 + beam] + (key_logit(key) - s.lse[beam]), beam);
     };
-    for (int i = threadIdx.x; i < heads; i += kThreads) {
-        const uint64_t key = __ldcg(keys + (int64_t)i * kBeamKeys);
-        s.lo[i] = key;
-        s.hi[i] = key ? score_of(key, i / a.segments) : 0ull;
+    uint64_t head_hi[kHeads], top = 0ull;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+        const int list = i * kThreads + (int)threadIdx.x;
+        head_hi[i] = head[i] ? score_of(head[i], list / a.segments) : 0ull;
+        top = head_hi[i] > top ? head_hi[i] : top;
     }
+    const uint64_t bound = group_bound(s.groups, top, a.k);
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i)
+        if (head_hi[i] && head_hi[i] >= bound) {
+            const int at = atomicAdd(&s.n_heads, 1);
+            s.hi[at] = head_hi[i];
+            s.lo[at] = head[i];
+            s.list_of[at] = (int16_t)(i * kThreads + threadIdx.x);
+        }
     __syncthreads();
-    // the lists in the order of their heads, k at most
-    for (int i = threadIdx.x; i < heads; i += kThreads) {
+    // the k best of them in order
+    const int n_heads = s.n_heads;
+    for (int i = threadIdx.x; i < n_heads; i += kThreads) {
         const uint64_t hi = s.hi[i], lo = s.lo[i];
-        if (hi == 0ull)
-            continue;
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < heads; ++j)
+        for (int j = 0; j < n_heads; ++j)
             rank += better(s.hi[j], s.lo[j], hi, lo);
         if (rank < a.k)
-            s.list[rank] = i;
+            s.head[rank] = i;
     }
     __syncthreads();
     // what is no better than the k-th head is none of the k best
-    const int last = s.list[a.k - 1];
+    const int last = s.head[a.k - 1];
     const uint64_t floor_hi = last >= 0 ? s.hi[last] : 1ull, floor_lo = last >= 0 ? s.lo[last] : 0ull;
     for (int i = threadIdx.x; i < a.k * a.k; i += kThreads) {
-        const int r = i / a.k, j = i - r * a.k, list = s.list[r];
-        if (r + j >= a.k || list < 0)
+        const int r = i / a.k, j = i - r * a.k, h = s.head[r];
+        if (r + j >= a.k || h < 0)
             continue;
+        const int list = s.list_of[h];
         const uint64_t key = __ldcg(keys + (int64_t)list * kBeamKeys + j);
         const uint64_t hi = key ? score_of(key, list / a.segments) : 0ull;
         if (hi && !better(floor_hi, floor_lo, hi, key)) {
@@ -217,15 +285,16 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     }
 }
 
-// T: float, or uint16_t holding bf16.  E: logits per thread and chunk.  A row
+// T: float, or uint16_t holding bf16.  NV: 16-byte vectors per thread and chunk,
+// one chunk in work and one in flight.  A row
 // may start anywhere: row index n is place n + lead of a sequence aligned to
 // 16 bytes, segments are cut at such boundaries, and the vectors that reach
 // over an end of the row are read element by element.
-template <typename T, int E>
+template <typename T, int NV>
 __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs a)
 {
     constexpr int V = 16 / sizeof(T);
-    constexpr int NV = E / V;
+    constexpr int E = NV * V;  // logits per thread and chunk
     static_assert(V * kThreads + kBeamKeys <= kBuffer, "a slice fits the buffer");
     __shared__ union {
         Shared scan;
@@ -249,21 +318,20 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         const int end = min(begin + a.length, a.N);
         float m = kNegInf, sum = 0.f;
         float bound = kNegInf;  // later rows must exceed it
+        int chunk = 0;
         if (threadIdx.x == 0)
             s.n = 0;
+        uint4 next[NV];  // the chunk after the one in work
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            next[j] = load_vector(x, begin + (j * kThreads + (int)threadIdx.x) * V, end);
         for (int base = begin; base < end; base += kThreads * E) {
             const int first = base + (int)threadIdx.x * V;
             float v[NV][V];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int n = first + j * kThreads * V;
-                if (n >= 0 && n + V <= end) {
-                    widen(ld_stream16(x + n), v[j]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        v[j][e] = n + e >= 0 && n + e < end ? widen1(x[n + e]) : kNegInf;
-                }
+                widen(next[j], v[j]);
+                next[j] = load_vector(x, first + kThreads * E + j * kThreads * V, end);
             }
             float top = max_of(v[0]);
             int top_j = 0;
@@ -278,23 +346,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
             // the place up to which logits equal to the bound pass
             int place = -1;
             if (base == begin) {
-                uint64_t key = top > kNegInf ? make_key(top, top_j * kThreads + threadIdx.x) : 0ull;
-#pragma unroll
-                for (int off = 1; off < 8; off <<= 1) {
-                    const uint64_t o = __shfl_xor_sync(kFull, key, off);
-                    key = o > key ? o : key;
-                }
-                if ((lane & 7) == 0)
-                    s.groups[threadIdx.x >> 3] = key;
-                __syncthreads();
-                key = s.groups[lane];
-                int rank = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint64_t o = s.groups[j];
-                    rank += o > key || (o == key && j < lane);  // (empty groups are equal)
-                }
-                key = __shfl_sync(kFull, key, __ffs(__ballot_sync(kFull, rank == k - 1)) - 1);
+                const uint64_t key = group_bound(
+                    s.groups, top > kNegInf ? make_key(top, top_j * kThreads + threadIdx.x) : 0ull, k);
                 if (key) {
                     bound = key_logit(key);
                     place = key_id(key);
@@ -327,42 +380,39 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                                     s.buffer[at] = make_key(v[j][e], first + j * kThreads * V + e);
                             }
             }
-            __syncthreads();
-            const int count = s.n;
-            __syncthreads();
-            if (count > kBuffer) {
-                // Take the chunk again slice by slice.  Of what the buffer
-                // holds, the keys of earlier chunks stay.
-                if (threadIdx.x == 0) {
-                    int kept = 0;
-                    for (int i = 0; i < kBuffer; ++i)
-                        if (key_id(s.buffer[i]) < base)
-                            s.buffer[kept++] = s.buffer[i];
-                    s.n = kept;
+            ++chunk;
+            if ((chunk & (chunk - 1)) == 0 && base + kThreads * E < end) {
+                __syncthreads();
+                const int count = s.n;
+                __syncthreads();
+                if (count > k && count <= kBuffer) {
+                    const uint64_t kth = prune(s, count, k);
+                    if (kth)
+                        bound = key_logit(kth);
                 }
-                __syncthreads();
-                const int kept = s.n;
-                __syncthreads();
-                uint64_t kth = prune(s, kept, k);
-                float least = kth ? key_logit(kth) : kNegInf;
+            }
+        }
+        __syncthreads();
+        const int count = s.n;
+        __syncthreads();
+        if (count > kBuffer) {
+            prune(s, 0, k);
+            float least = kNegInf;
+            for (int n0 = begin; n0 < end; n0 += kThreads * V) {
+                const int n = n0 + (int)threadIdx.x * V;
+                float v[V];
+                widen(load_vector(x, n, end), v);
 #pragma unroll
-                for (int j = 0; j < NV; ++j) {
-#pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (v[j][e] > least)
-                            s.buffer[atomicAdd(&s.n, 1)] =
-                                make_key(v[j][e], first + j * kThreads * V + e);
-                    __syncthreads();
-                    const int n = s.n;
-                    __syncthreads();
-                    kth = prune(s, n, k);
+                for (int e = 0; e < V; ++e)
+                    if (v[e] > least)
+                        s.buffer[atomicAdd(&s.n, 1)] = make_key(v[e], n + e);
+                __syncthreads();
+                const int held = s.n;
+                __syncthreads();
+                if (held > kBeamKeys || n0 == begin) {
+                    const uint64_t kth = prune(s, held, k);
                     least = kth ? key_logit(kth) : kNegInf;
                 }
-                bound = least;
-            } else if (count > kBuffer / 2) {
-                const uint64_t kth = prune(s, count, k);
-                if (kth)
-                    bound = key_logit(kth);
             }
         }
         // the block's sum relative to its maximum
@@ -418,16 +468,26 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
         pick(a, request, sm.pick);
 }
 
-constexpr int kLong = 32, kShort = 8;  // logits per thread and chunk
+constexpr int kLeast = 8 * kThreads;  // logits of a segment, at least
 
 }  // namespace
 
-// Segments of a row: as many as fill the SMs, of 2,048 logits at least.
+// Segments of a row: as many as fill the SMs, of kLeast logits at least.
 int beam_segments(int64_t rows, int N)
 {
-    const int64_t most = ((int64_t)N + 7 + kThreads * kShort - 1) / (kThreads * kShort);
-    int64_t n = rows > 0 && rows < kBeamLists ? kBeamLists / rows : 1;
+    const int64_t most = ((int64_t)N + 7 + kLeast - 1) / kLeast;
+    const int64_t n = rows > 0 && rows < kBeamLists ? kBeamLists / rows : 1;
     return (int)(n < most ? n : most);
+}
+
+template <typename T>
+static cudaError_t launch(const BeamArgs &a, unsigned grid, cudaStream_t s)
+{
+    // Four vectors per thread keep 64 KB per SM in flight; a segment of the
+    // least length runs through less code in a chunk of its own size.
+    if (a.length > 2 * kLeast)
+        return launch_pdl(beam_select_kernel<T, 4>, grid, kThreads, 0, s, a);
+    return launch_pdl(beam_select_kernel<T, 8 * sizeof(T) / 16>, grid, kThreads, 0, s, a);
 }
 
 cudaError_t launch_beam_select(BeamArgs &a, int dtype, cudaStream_t s)
@@ -436,14 +496,7 @@ cudaError_t launch_beam_select(BeamArgs &a, int dtype, cudaStream_t s)
     // up to 7 places before a row's start; lengths are multiples of a vector
     a.length = (int)((((int64_t)a.N + 7 + a.segments - 1) / a.segments + 7) / 8 * 8);
     const unsigned grid = (unsigned)(rows * a.segments);
-    // Chunks of 8,192 logits keep the loads of a long segment in flight; a
-    // segment of one short chunk or two runs less code per logit it lacks.
-    const bool lng = a.length > 2 * kThreads * kShort;
-    if (dtype == DVL_F32)
-        return lng ? launch_pdl(beam_select_kernel<float, kLong>, grid, kThreads, 0, s, a)
-                   : launch_pdl(beam_select_kernel<float, kShort>, grid, kThreads, 0, s, a);
-    return lng ? launch_pdl(beam_select_kernel<uint16_t, kLong>, grid, kThreads, 0, s, a)
-               : launch_pdl(beam_select_kernel<uint16_t, kShort>, grid, kThreads, 0, s, a);
+    return dtype == DVL_F32 ? launch<float>(a, grid, s) : launch<uint16_t>(a, grid, s);
 }
 
 }  // namespace dvl

@@ -3,7 +3,8 @@
 //
 // Pure data movement, bound by HBM (or by the launch, for a few rows).  One
 // block copies one piece of at most kPiece bytes of one destination row:
-// every thread keeps two 16-byte loads in flight.  The block index walks the
+// every thread keeps four 16-byte loads in flight (two: 29.0 us for 128 rows
+// of 517 KB and their pages, against 22.1 of HBM time).  The block index walks the
 // states, the page table and the lengths (ReorderItem.first_block), then the
 // pages; a page's blocks read how many of its tokens are filled and leave if
 // their piece lies past that.
@@ -16,7 +17,8 @@ namespace dvl {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPiece = kThreads * 32;  // bytes per block
+constexpr int kLoads = 4;                       // per thread
+constexpr int kPiece = kThreads * 16 * kLoads;  // bytes per block
 
 // The source row of new beam r = b * k + i, or -1 for an unused slot.
 __device__ __forceinline__ int64_t source_row(const ReorderArgs &a, int64_t r)
@@ -34,16 +36,19 @@ __device__ __forceinline__ void copy_piece(const ReorderArgs &a, const ReorderIt
     const unsigned char *src = it.src + from * it.src_stride + off;
     unsigned char *dst = it.dst + r * it.dst_stride + off;
     if (it.wide) {
-        const int i0 = threadIdx.x * 16, i1 = i0 + kThreads * 16;
-        uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
-        if (from >= 0 && i0 < n)
-            v0 = *reinterpret_cast<const uint4 *>(src + i0);
-        if (from >= 0 && i1 < n)
-            v1 = *reinterpret_cast<const uint4 *>(src + i1);
-        if (i0 < n)
-            *reinterpret_cast<uint4 *>(dst + i0) = v0;
-        if (i1 < n)
-            *reinterpret_cast<uint4 *>(dst + i1) = v1;
+        uint4 v[kLoads];
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int i = (j * kThreads + (int)threadIdx.x) * 16;
+            v[j] = from >= 0 && i < n ? *reinterpret_cast<const uint4 *>(src + i)
+                                      : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            const int i = (j * kThreads + (int)threadIdx.x) * 16;
+            if (i < n)
+                *reinterpret_cast<uint4 *>(dst + i) = v[j];
+        }
     } else {
         for (int i = threadIdx.x; i < n; i += kThreads)
             dst[i] = from >= 0 ? src[i] : (unsigned char)0;
@@ -90,17 +95,22 @@ __device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk)
     const int64_t ts = values ? c.v_token_stride : c.k_token_stride;
     const int64_t hs = values ? c.v_head_stride : c.k_head_stride;
     unsigned char *base = static_cast<unsigned char *>(values ? c.v : c.k);
+    uint4 v[kLoads];
+    int64_t at[kLoads];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int u = u0 + threadIdx.x + j * kThreads;
+    for (int j = 0; j < kLoads; ++j) {
+        const int u = u0 + (int)threadIdx.x + j * kThreads;
         if (u < total) {
             const int th = u / row16, unit = u - th * row16;
             const int tok = th / c.heads, head = th - tok * c.heads;
-            const int64_t at = (tok * ts + head * hs) * a.elem + unit * 16;
-            *reinterpret_cast<uint4 *>(base + dst_page * ps * a.elem + at) =
-                *reinterpret_cast<const uint4 *>(base + src_page * ps * a.elem + at);
+            at[j] = (tok * ts + head * hs) * a.elem + unit * 16;
+            v[j] = *reinterpret_cast<const uint4 *>(base + src_page * ps * a.elem + at[j]);
         }
     }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+        if (u0 + (int)threadIdx.x + j * kThreads < total)
+            *reinterpret_cast<uint4 *>(base + dst_page * ps * a.elem + at[j]) = v[j];
 }
 
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderArgs a)

@@ -52,10 +52,10 @@ def _rows(t, shape, dtypes, dev: int, name: str):
 
 def _flat(t, shape, dtype, dev: int, name: str) -> int:
     """Data pointer of a contiguous tensor."""
-    if (t.get_device() != dev or t.dtype != dtype or tuple(t.shape) != shape
+    if (t.get_device() != dev or t.dtype != dtype or t.shape != shape
             or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous CUDA {str(dtype)[6:]} tensor of shape "
-                         f"{shape} on the inputs' device")
+                         f"{tuple(shape)} on the inputs' device")
     return t.data_ptr()
 
 
@@ -193,8 +193,8 @@ def paged_attention(cache: KVCache, q, table, lengths, *, scale=None, out=None, 
         out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
-    po = _flat(out, tuple(shape), torch.bfloat16, dev, "out")
-    pe = _flat(lse, tuple(shape[:-1]), torch.float32, dev, "lse") if lse is not None else 0
+    po = _flat(out, shape, torch.bfloat16, dev, "out")
+    pe = _flat(lse, shape[:-1], torch.float32, dev, "lse") if lse is not None else 0
     if ws is None:
         ws = attention_workspace(cache, B, T, Hq, stream=stream)
     _need(ws.get_device() == dev, "ws must be on the cache's device")
@@ -290,15 +290,14 @@ def beam_reorder(parents, states=(), *, states_out=None, cache: KVCache | None =
         states_out = [torch.empty((batch, k) + tuple(s.shape[2:]), dtype=s.dtype, device=s.device)
                       for s in states]
     _need(len(states_out) == n, "states_out must match states")
-    items = (DvlState * n)() if n else None
-    for i, (s, d) in enumerate(zip(states, states_out)):
-        tail = tuple(s.shape[2:])
-        src = _flat(s, (batch, beams) + tail, s.dtype, dev, "a state")
-        dst = _flat(d, (batch, k) + tail, s.dtype, dev, "a state's output")
-        rows = batch * beams
-        size = s.numel() // rows * s.element_size() if rows else 0
-        _need(size > 0 or rows == 0, "a state's rows must not be empty")
-        items[i] = (src, dst, size, size, size)
+    items = []
+    for s, d in zip(states, states_out):
+        tail = s.shape[2:]
+        size = s.element_size() * tail.numel()
+        _need(size > 0, "a state's rows must not be empty")
+        items.append((_flat(s, (batch, beams, *tail), s.dtype, dev, "a state"),
+                      _flat(d, (batch, k, *tail), s.dtype, dev, "a state's output"), size, size, size))
+    items = (DvlState * n)(*items) if n else None
     pages = None
     if cache is not None:
         _need(table is not None and lengths is not None and spare is not None,
