@@ -337,21 +337,29 @@ struct RowAddress {
 };
 
 // Copy a chunk's rows (keys or values) into a ring entry, `live` of them; the
-// others become zeros.  at: the thread's place among the group's N threads.
-template <int DP, bool FP8, int TOK, int N>
+// others become zeros, and so do the padding columns of keys: they meet zeros
+// of Q and must hold no NaN, which whatever the entry held before may be.
+// at: the thread's place among the group's N threads.
+template <int DP, bool FP8, int TOK, int N, bool KEYS>
 __device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *const *rows, int live,
                                           int at, uint32_t dst, int pitch)
 {
     constexpr int kCols = DP * (FP8 ? 1 : 2) / 16;  // 16-byte units of a padded row
     constexpr int kStep = N / kCols;                // rows per pass
     const int col = at % kCols, r0 = at / kCols;
-    if (col * 16 >= row_bytes || r0 >= TOK)
+    int from = col * 16;
+    if (from >= row_bytes) {
+        if (!KEYS)
+            return;
+        from = live = 0;
+    }
+    if (r0 >= TOK)
         return;
 #pragma unroll
     for (int i = 0; i < (kStep < TOK ? TOK / kStep : 1); ++i) {
         const int r = r0 + i * kStep;
         const int unit = FP8 ? col : col ^ (r & 7);
-        cp_async16(dst + r * pitch + unit * 16, rows[r] + col * 16, r < live);
+        cp_async16(dst + r * pitch + unit * 16, rows[r] + from, r < live);
     }
 }
 
@@ -635,13 +643,6 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     };
     load_q();
 
-    // Padding columns of K meet zeros of Q: they must hold no NaN.
-    if (a.D < DP) {
-        for (int i = threadIdx.x * 16; i < S::kQ; i += kThreads * 16)
-            *reinterpret_cast<uint4 *>(smem + i) = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-    }
-
     // Row addresses are known P + 1 chunks ahead of the chunk in work, page
     // ids one more.
     const unsigned char **addr = reinterpret_cast<const unsigned char **>(smem + S::kAddr) +
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     int load_slot = 0, load_entry = 0;  // of addr, of the ring
     auto load_keys = [&]() {
         if (to_load > 0)
-            load_rows<DP, FP8, TOK, kGroup>(row_bytes, addr + load_slot * 2 * TOK,
+            load_rows<DP, FP8, TOK, kGroup, true>(row_bytes, addr + load_slot * 2 * TOK,
                                             load.len - load.t * S::kTile - TOK * group, at,
                                             ring + load_entry * S::kEntry, S::kKPitch);
         cp_async_commit();
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     };
     auto load_values = [&]() {
         if (to_load > 0)
-            load_rows<DP, FP8, TOK, kGroup>(row_bytes, addr + load_slot * 2 * TOK + TOK,
+            load_rows<DP, FP8, TOK, kGroup, false>(row_bytes, addr + load_slot * 2 * TOK + TOK,
                                             load.len - load.t * S::kTile - TOK * group, at,
                                             ring + load_entry * S::kEntry, S::kVPitch);
         cp_async_commit();

@@ -94,9 +94,14 @@ __device__ __forceinline__ float max_of(const float (&v)[N])
     return m;
 }
 
+struct Groups {
+    uint64_t key[32];
+    int rank[32];
+};
+
 struct Shared {
     uint64_t buffer[kBuffer];
-    uint64_t groups[32];
+    Groups groups;
     uint64_t best[kBeamKeys];
     float2 sums[kWarps];
     int n;           // keys in the buffer (may exceed its size: then it overflowed)
@@ -109,8 +114,8 @@ struct PickShared {
     uint64_t hi[kBeamLists], lo[kBeamLists];  // heads: (score, beam), (logit, row)
     int16_t list_of[kBeamLists];
     uint64_t c_hi[kPairs], c_lo[kPairs];  // candidates
-    uint64_t groups[32];
-    float lse[DVL_MAX_BEAMS];
+    Groups groups;
+    float lse[DVL_MAX_BEAMS], base[DVL_MAX_BEAMS];  // per beam, its score
     int head[DVL_MAX_BEAMS];              // the k best heads, in order
     int n_heads, n;
 };
@@ -143,26 +148,31 @@ __device__ __forceinline__ uint64_t prune(Shared &s, int n, int k)
 
 // A bound from below of the k-th largest of the block's keys `mine` (0: none):
 // the k-th largest of the maxima of 32 groups of 8 threads; 0 when fewer than
-// k groups have a key.  Every thread calls it.
-__device__ __forceinline__ uint64_t group_bound(uint64_t *groups, uint64_t mine, int k)
+// k groups have a key.  The warps share the comparisons, a warp taking four
+// groups against all.  Every thread calls it; g.rank is zero before.
+__device__ __forceinline__ uint64_t group_bound(Groups &g, uint64_t mine, int k)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int off = 1; off < 8; off <<= 1) {
         const uint64_t o = __shfl_xor_sync(kFull, mine, off);
         mine = o > mine ? o : mine;
     }
     if ((lane & 7) == 0)
-        groups[threadIdx.x >> 3] = mine;
+        g.key[threadIdx.x >> 3] = mine;
     __syncthreads();
-    mine = groups[lane];
+    mine = g.key[lane];
     int rank = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-        const uint64_t o = groups[j];
+    for (int i = 0; i < 32 / kWarps; ++i) {
+        const int j = warp * (32 / kWarps) + i;
+        const uint64_t o = g.key[j];
         rank += o > mine || (o == mine && j < lane);  // (empty groups are equal)
     }
-    return __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, rank == k - 1)) - 1);
+    if (rank)
+        atomicAdd(&g.rank[lane], rank);
+    __syncthreads();
+    return __shfl_sync(kFull, mine, __ffs(__ballot_sync(kFull, g.rank[lane] == k - 1)) - 1);
 }
 
 // (score, beam) as a key whose order is the result's: higher score, lower beam.
@@ -183,6 +193,7 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     const int heads = a.beams * a.segments;
     const uint64_t *keys = a.keys + row0 * a.segments * kBeamKeys;
     constexpr int kHeads = (kBeamLists + kThreads - 1) / kThreads;  // per thread
+    const float base = threadIdx.x < a.beams ? a.scores[row0 + threadIdx.x] : 0.f;
     uint64_t head[kHeads];  // in flight while the sums are joined
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
@@ -191,14 +202,18 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     }
     for (int beam = warp; beam < a.beams; beam += kWarps) {
         const float2 *ms = a.sums + (row0 + beam) * a.segments;
-        float m = kNegInf, sum = 0.f;
-        for (int c = lane; c < a.segments; c += 32)
+        const float2 mine =
+            lane < a.segments ? __ldcg(ms + lane) : make_float2(kNegInf, 0.f);
+        float m = mine.x, sum = 0.f;
+        for (int c = lane + 32; c < a.segments; c += 32)
             m = fmaxf(m, __ldcg(&ms[c].x));
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1)
             m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
         // a row of -inf only: m - m is NaN, and so are its scores
-        for (int c = lane; c < a.segments; c += 32) {
+        if (lane < a.segments)
+            sum = mine.y * exp_diff(mine.x - m);
+        for (int c = lane + 32; c < a.segments; c += 32) {
             const float2 x = __ldcg(&ms[c]);
             sum += x.y * exp_diff(x.x - m);
         }
@@ -208,13 +223,16 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
         if (lane == 0)
             s.lse[beam] = m + logf(sum);
     }
-    if (threadIdx.x < DVL_MAX_BEAMS)
+    if (threadIdx.x < DVL_MAX_BEAMS) {
         s.head[threadIdx.x] = -1;
+        s.groups.rank[threadIdx.x] = 0;
+        s.base[threadIdx.x] = base;
+    }
     if (threadIdx.x == 0)
         s.n = s.n_heads = 0;
     __syncthreads();
     auto score_of = [&](uint64_t key, int beam) {
-        return score_key(a.scores[row0 + beam] + (key_logit(key) - s.lse[beam]), beam);
+        return score_key(s.base[beam] + (key_logit(key) - s.lse[beam]), beam);
     };
     uint64_t head_hi[kHeads], top = 0ull;
 #pragma unroll
@@ -265,16 +283,17 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     const int n = s.n;
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t hi = s.c_hi[i], lo = s.c_lo[i];
+        const int row = key_id(lo);
+        const int token = a.d2t ? a.d2t[row] : row;  // in flight while the rank is counted
         int rank = 0;
 #pragma unroll 4
         for (int j = 0; j < n; ++j)
             rank += better(s.c_hi[j], s.c_lo[j], hi, lo);
         if (rank < a.k) {
             const int64_t o = request * a.k + rank;
-            const int row = key_id(lo);
             a.out_scores[o] = key_logit(hi);
             a.parents[o] = key_id(hi);
-            a.tokens[o] = a.d2t ? a.d2t[row] : row;
+            a.tokens[o] = token;
         }
     }
     for (int i = n + threadIdx.x; i < a.k; i += kThreads) {
@@ -310,21 +329,25 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     const int k = a.k;
     uint64_t *out = a.keys + (int64_t)blockIdx.x * kBeamKeys;
 
+    const T *x = static_cast<const T *>(a.logits) + request * a.batch_stride +
+                 (row - request * a.beams) * a.beam_stride;
+    const int lead = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % V);
+    const int begin = segment * a.length - lead;  // of the segment, a multiple of V past the lead
+    const int end = min(begin + a.length, a.N);
+    // the chunk after the one in work; the first is in flight before the
+    // beam's score says whether it is needed
+    uint4 next[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        next[j] = load_vector(x, begin + (j * kThreads + (int)threadIdx.x) * V, end);
     if (a.scores[row] > kNegInf) {
-        const T *x = static_cast<const T *>(a.logits) + request * a.batch_stride +
-                     (row - request * a.beams) * a.beam_stride;
-        const int lead = (int)((reinterpret_cast<uintptr_t>(x) / sizeof(T)) % V);
-        const int begin = segment * a.length - lead;  // of the segment, a multiple of V past the lead
-        const int end = min(begin + a.length, a.N);
         float m = kNegInf, sum = 0.f;
         float bound = kNegInf;  // later rows must exceed it
         int chunk = 0;
         if (threadIdx.x == 0)
             s.n = 0;
-        uint4 next[NV];  // the chunk after the one in work
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            next[j] = load_vector(x, begin + (j * kThreads + (int)threadIdx.x) * V, end);
+        if (threadIdx.x < 32)
+            s.groups.rank[threadIdx.x] = 0;
         for (int base = begin; base < end; base += kThreads * E) {
             const int first = base + (int)threadIdx.x * V;
             float v[NV][V];
@@ -385,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                 __syncthreads();
                 const int count = s.n;
                 __syncthreads();
-                if (count > k && count <= kBuffer) {
+                if (count > 2 * k + 16 && count <= kBuffer) {
                     const uint64_t kth = prune(s, count, k);
                     if (kth)
                         bound = key_logit(kth);

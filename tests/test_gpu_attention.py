@@ -130,6 +130,17 @@ def test_attention_many_sequences(dvl):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("D", [16, 80, 208])
+def test_attention_padded_widths_on_blocks_with_many_sequences(dvl, D, fp8):
+    # blocks that finish many (sequence, head) pairs reuse their shared memory
+    rng = np.random.default_rng(D)
+    c = Case(D, [int(n) for n in rng.integers(1, 300, size=150)], 1, 16, 8, D, 16, fp8)
+    c.verify(c.call(dvl))
+    c = Case(D + 1, [int(n) for n in rng.integers(1, 200, size=90)], 3, 24, 4, D, 48, fp8)
+    c.verify(c.call(dvl))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("T", [1, 4])
 def test_attention_masked_slots_may_hold_anything(dvl, T, fp8):
     lengths = [1, 3, 70, 129, 200, 2]
