@@ -480,8 +480,16 @@ def write_ranks_txt(path: str, ids) -> None:
         f.writelines(f"{int(x)}\n" for x in ids)
 
 
-from . import step as _step  # noqa: E402  (uses this module's stream and workspace helpers)
-from .step import (KVCache, add_rmsnorm, attention_workspace, beam_reorder, beam_select,  # noqa: E402
-                   beam_workspace, paged_attention)
+from . import step as _step_module  # noqa: E402  (uses this module's workspace helpers)
+from .step import KVCache, attention_workspace, beam_workspace  # noqa: E402
 
-__all__ += _step.__all__
+__all__ += _step_module.__all__
+
+
+def __getattr__(name):
+    # the drafting step's operators, loaded with their first use
+    value = getattr(_step_module, name) if name in _step_module._OPERATORS else None
+    if value is None:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    globals()[name] = value
+    return value

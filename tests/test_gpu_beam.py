@@ -201,7 +201,7 @@ def test_beam_refusals(dvl):
             args.update(bad)
             dvl.beam_select(**args)
     for k in (0, 33, -1):
-        with pytest.raises((dvl.DvlError, RuntimeError)):
+        with pytest.raises(ValueError):
             dvl.beam_select(x, s, k)
     with pytest.raises(dvl.DvlError) as e:
         dvl.beam_select(x, s, 3, ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
