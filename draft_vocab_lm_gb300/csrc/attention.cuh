@@ -583,6 +583,52 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, 
     }
 }
 
+// A part of a (sequence, head) that this block has written to the workspace.
+struct Part {
+    int64_t first;  // the pair's first unit in its lane
+    int tiles, b, h;
+};
+
+// Count the part in; the last block of a group of parts joins them, the last
+// of the groups those.  Every thread calls it, after the part's last write.
+template <int DP, int THREADS, int R>
+__device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &share, const Part &p,
+                                            int *s_last)
+{
+    // The shares that hold the pair: those of its first and last unit (s
+    // holds unit u when floor(s U / n) <= u < floor((s + 1) U / n)).
+    const int64_t last = p.first + p.tiles - 1;
+    const int n = share.shares, mine = (int)blockIdx.x / a.lanes;
+    const int s0 = holder(p.first, share.units, n), s1 = holder(last, share.units, n);
+    const int lane_of = blockIdx.x % a.lanes;
+    // a share's first pair is in its slot 0, a later one in slot 1
+    const int slot0 = 2 * (s0 * a.lanes + lane_of) + (cut(share.units, s0, n) < p.first ? 1 : 0);
+    auto slot_of = [&](int s) { return s == s0 ? slot0 : 2 * (s * a.lanes + lane_of); };
+    const int count = s1 - s0 + 1, index = mine - s0;
+    const int from = index / kJoin * kJoin;  // first part of this part's group
+    const int size = min(kJoin, count - from);
+    const int groups = (count + kJoin - 1) / kJoin;
+    const int step = 2 * a.lanes;            // slots from a share to the next
+    const int stats = a.rows * a.D;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *s_last = ticket_inc(a.tickets + slot_of(s0 + from), size - 1) == (unsigned)size - 1;
+    __syncthreads();
+    if (!*s_last)
+        return;
+    join_parts<DP, THREADS, R>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1), step, stats,
+                               groups == 1, p.b, p.h);
+    if (groups == 1)
+        return;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        *s_last = ticket_inc(a.tickets + a.top_tickets + slot0, groups - 1) == (unsigned)groups - 1;
+    __syncthreads();
+    if (*s_last)
+        join_parts<DP, THREADS, R>(a, groups, slot0, slot_of(s0 + kJoin), step * kJoin,
+                                   stats + 2 * a.rows, true, p.b, p.h);
+}
+
 template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
 __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCKS)
     attention_kernel(const __grid_constant__ AttnArgs a)
@@ -627,7 +673,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     constexpr int kUnits = DP / 8;
     constexpr int kPasses = (S::kQRows * kUnits + kThreads - 1) / kThreads;
     uint4 qv[kPasses];
-    auto load_q = [&]() {
+    auto load_q = [&](int b, int h) {
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
@@ -636,12 +682,47 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             if (r < a.rows && d < a.D) {
                 const int t = a.token_of(r);
                 qv[i] = *reinterpret_cast<const uint4 *>(
-                    a.q + cur.b * a.qb + t * a.qt +
-                    (int64_t)(cur.h * a.G + (r - t * a.G)) * a.qh + d);
+                    a.q + b * a.qb + t * a.qt + (int64_t)(h * a.G + (r - t * a.G)) * a.qh + d);
             }
         }
     };
-    load_q();
+    auto store_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
+            const int d = ((int)threadIdx.x % kUnits) * 8;
+            unsigned char *dst = smem + S::kQ + r * S::kQPitch;
+            if constexpr (FP8) {
+                const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+                uint32_t big = 0u;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    big = max(big, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+#pragma unroll
+                for (int off = kUnits / 2; off >= 1; off >>= 1)
+                    big = max(big, __shfl_xor_sync(kFull, big, off));
+                int e2 = (int)(big >> 23) - 127;
+                e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                if (r < S::kQRows) {
+                    // place of value d in the permuted order: block of 32, lane
+                    // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint32_t *>(
+                            dst + 2 * ((d & ~31) + (e >> 1) * 16 + (e & 1) * 8 + ((d >> 3) & 3) * 2)) =
+                            pack2<true>(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
+                    if (d == 0)
+                        row_scale[r] = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
+                }
+            } else if (r < S::kQRows) {
+                *reinterpret_cast<uint4 *>(dst + 2 * d) = qv[i];
+                if (d == 0)
+                    row_scale[r] = a.qk_scale;
+            }
+        }
+    };
+    load_q(cur.b, cur.h);
 
     // Row addresses are known P + 1 chunks ahead of the chunk in work, page
     // ids one more.
@@ -709,61 +790,23 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             for (int e = 0; e < 2 * NJ; ++e)
                 o[n][e] = 0.f;
     };
+    // Visible positions per row of the (sequence, head) that starts.
+    auto start_pair = [&](int len) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int r = 16 * mt + 8 * j + g;
+            sees[j] = r < a.rows ? len - (a.T - 1 - a.token_of(r)) : 0;
+        }
+        sees_least = len - (a.T - 1);
+    };
     reset();
-    bool fresh = true;       // the next tile starts a (sequence, head)
+    start_pair(cur.len);
+    store_q();
+    __syncthreads();
     bool first_part = true;  // still in the block's first (sequence, head)
-    int t_first = 0;
+    int t_first = cur.t;
     int entry = 0;
     for (int64_t left = n_units; left > 0; --left) {
-        if (fresh) {
-            fresh = false;
-            t_first = cur.t;
-            if (!first_part)
-                load_q();
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) {
-                const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
-                const int d = ((int)threadIdx.x % kUnits) * 8;
-                unsigned char *dst = smem + S::kQ + r * S::kQPitch;
-                if constexpr (FP8) {
-                    const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
-                    uint32_t big = 0u;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        big = max(big, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
-#pragma unroll
-                    for (int off = kUnits / 2; off >= 1; off >>= 1)
-                        big = max(big, __shfl_xor_sync(kFull, big, off));
-                    int e2 = (int)(big >> 23) - 127;
-                    e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
-                    const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
-                    if (r < S::kQRows) {
-                        // place of value d in the permuted order: block of 32,
-                        // lane quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint32_t *>(
-                                dst + 2 * ((d & ~31) + (e >> 1) * 16 + (e & 1) * 8 +
-                                           ((d >> 3) & 3) * 2)) =
-                                pack2<true>(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
-                        if (d == 0)
-                            row_scale[r] =
-                                a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
-                    }
-                } else if (r < S::kQRows) {
-                    *reinterpret_cast<uint4 *>(dst + 2 * d) = qv[i];
-                    if (d == 0)
-                        row_scale[r] = a.qk_scale;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                const int r = 16 * mt + 8 * j + g;
-                sees[j] = r < a.rows ? cur.len - (a.T - 1 - a.token_of(r)) : 0;
-            }
-            sees_least = cur.len - (a.T - 1);
-            __syncthreads();
-        }
         const int pos0 = cur.t * S::kTile + TOK * group;
 
         // keys
@@ -979,6 +1022,12 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
         if (ends || left == 1) {
             // This block's part of the (sequence, head) is complete: join the
             // groups in order, through the ring entry of the values just used.
+            // The next one's Q is on its way meanwhile.
+            Cursor<S::kTile> after = cur;
+            if (left > 1) {
+                after.next(a);
+                load_q(after.b, after.h);
+            }
 #pragma unroll
             for (int j = 0; j < NJ; ++j) {
                 l[j] += __shfl_xor_sync(kFull, l[j], 1);
@@ -1060,50 +1109,20 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                 if (c0 + S::kRound < DP)
                     __syncthreads();
             }
-            if (!whole) {
-                // The shares that hold the pair: those of its first and last
-                // unit (s holds unit u when floor(s U / n) <= u < floor((s + 1) U / n)).
-                const int64_t here = share.u1 - left;  // this unit
-                const int64_t first = here - cur.t, last = first + cur.tiles - 1;
-                const int n = share.shares, mine = (int)blockIdx.x / a.lanes;
-                const int s0 = holder(first, share.units, n), s1 = holder(last, share.units, n);
-                const int lane_of = blockIdx.x % a.lanes;
-                // a share's first pair is in its slot 0, a later one in slot 1
-                const int slot0 =
-                    2 * (s0 * a.lanes + lane_of) + (cut(share.units, s0, n) < first ? 1 : 0);
-                auto slot_of = [&](int s) { return s == s0 ? slot0 : 2 * (s * a.lanes + lane_of); };
-                const int count = s1 - s0 + 1, index = mine - s0;
-                const int from = index / kJoin * kJoin;       // first part of this part's group
-                const int size = min(kJoin, count - from);
-                const int groups = (count + kJoin - 1) / kJoin;
-                const int step = 2 * a.lanes;                 // slots from a share to the next
-                unsigned int *tickets = a.tickets;
-                __syncthreads();
-                if (threadIdx.x == 0)
-                    s_last = ticket_inc(tickets + slot_of(s0 + from), size - 1) ==
-                             (unsigned)size - 1;
-                __syncthreads();
-                if (s_last) {
-                    const int stats = a.rows * a.D;
-                    join_parts<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1),
-                                             step, stats, groups == 1, cur.b, cur.h);
-                    if (groups > 1) {
-                        __syncthreads();
-                        if (threadIdx.x == 0)
-                            s_last = ticket_inc(tickets + a.top_tickets + slot0, groups - 1) ==
-                                     (unsigned)groups - 1;
-                        __syncthreads();
-                        if (s_last)
-                            join_parts<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(a, groups, slot0, slot_of(s0 + kJoin),
-                                                     step * kJoin, stats + 2 * a.rows, true, cur.b,
-                                                     cur.h);
-                    }
-                }
-            }
+            if (!whole)
+                finish_part<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(
+                    a, share, {share.u1 - left - cur.t, cur.tiles, cur.b, cur.h}, &s_last);
+            if (left == 1)
+                break;
+            // (all scores with the old Q are done since the first barrier)
+            store_q();
+            start_pair(after.len);
             __syncthreads();
             first_part = false;
-            fresh = true;
+            t_first = after.t;
             reset();
+            cur = after;
+            continue;
         }
         cur.next(a);
     }
