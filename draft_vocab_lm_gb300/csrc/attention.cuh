@@ -609,24 +609,30 @@ __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &shar
     const int size = min(kJoin, count - from);
     const int groups = (count + kJoin - 1) / kJoin;
     const int step = 2 * a.lanes;            // slots from a share to the next
-    const int stats = a.rows * a.D;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *s_last = ticket_inc(a.tickets + slot_of(s0 + from), size - 1) == (unsigned)size - 1;
-    __syncthreads();
-    if (!*s_last)
-        return;
-    join_parts<DP, THREADS, R>(a, size, slot_of(s0 + from), slot_of(s0 + from + 1), step, stats,
-                               groups == 1, p.b, p.h);
-    if (groups == 1)
-        return;
-    __syncthreads();
-    if (threadIdx.x == 0)
-        *s_last = ticket_inc(a.tickets + a.top_tickets + slot0, groups - 1) == (unsigned)groups - 1;
-    __syncthreads();
-    if (*s_last)
-        join_parts<DP, THREADS, R>(a, groups, slot0, slot_of(s0 + kJoin), step * kJoin,
-                                   stats + 2 * a.rows, true, p.b, p.h);
+    int stats = a.rows * a.D;
+    int parts = size, slot_a = slot_of(s0 + from), slot_b = slot_of(s0 + from + 1), stride = step;
+    unsigned int *ticket = a.tickets + slot_a;
+    // (one copy of the code for both levels: a short call waits for most of
+    // its instructions as it waits for its data)
+#pragma unroll 1
+    for (int level = 0;; ++level) {
+        __syncthreads();
+        if (threadIdx.x == 0)
+            *s_last = ticket_inc(ticket, parts - 1) == (unsigned)parts - 1;
+        __syncthreads();
+        if (!*s_last)
+            return;
+        const bool last_level = level == 1 || groups == 1;
+        join_parts<DP, THREADS, R>(a, parts, slot_a, slot_b, stride, stats, last_level, p.b, p.h);
+        if (last_level)
+            return;
+        parts = groups;
+        slot_a = slot0;
+        slot_b = slot_of(s0 + kJoin);
+        stride = step * kJoin;
+        stats += 2 * a.rows;
+        ticket = a.tickets + a.top_tickets + slot0;
+    }
 }
 
 template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
