@@ -2,29 +2,41 @@
 // and the k best (beam, row) pairs of a request:
 //   score(j, n) = scores[j] + (x[j][n] - lse_j),  lse_j = m + ln sum e^{x - m}.
 //
-// Bound by HBM: each logit is read once and costs one exponential and a
-// maximum.  One launch:
+// Each logit is read once and costs one exponential and a maximum: HBM bounds
+// many long fp32 rows (512 rows of 248,320: 0.91 of the copy rate), issue slots
+// many bf16 rows (1,024 of them, k = 8: 94 us, 0.81; with one logit per
+// instruction and every key pushed by its own thread 142 us), and a chain of
+// dependent steps few rows: about 5 us until the last segment has left its
+// keys and 2 to 4 us to pick (64 rows of 248,320, k = 16: 20.7 us of which
+// 9.5 are HBM time; 4 rows of 16,000: 6.4 us).  One launch:
 //   - A block takes one segment of a row, in chunks that sit in registers.
 //     Every thread keeps the maximum and the sum of exponentials of what it
-//     has seen.  Within one beam the order of the scores is that of the
-//     logits, so the segment's best rows are found as packed (logit, row)
-//     keys: of the first chunk, 32 groups of 8 threads compare their maxima,
-//     and the k-th largest of those bounds the k-th largest key from below;
-//     what lies at or above the bound (a few more than k) goes to a buffer in
-//     shared memory, as does what exceeds it in later chunks.  At the end the
-//     buffer's keys count their betters, and the k best are written out.
+//     has seen, two logits per instruction.  Within one beam the order of the
+//     scores is that of the logits, so the segment's best rows are found as
+//     packed (logit, row) keys: of the first chunk, 32 groups of 8 threads
+//     compare their maxima, and the k-th largest of those bounds the k-th
+//     largest key from below; vectors with a logit at or above the bound (a few
+//     more than k) are kept aside in shared memory, as are those that exceed it
+//     in later chunks.  At the end their keys count their betters, and the k
+//     best are written out.  (A whole vector is put aside because a warp with
+//     one passing logit in eight runs through all eight tests: on short
+//     segments, which pass few, that costs less than the second look.)
 //   - The last block of a request (a wrapping ticket) joins the segments' sums
 //     into lse, turns keys into scores, and picks: a segment list whose head
 //     has r better heads can give its first k - r keys only.
 // Ties are exact: bounds carry the place of their logit, rows are read in
 // order, and later rows have to exceed a bound, not to reach it, so rows of
 // equal logits (a constant row, a mask of the type's lowest value) pass in
-// limited number.  A segment that overflows the buffer all the same (rising
-// logits) is read again in slices that fit, with the buffer cut back to its
-// k best after each.  After chunk 1, 2, 4, 8 .. the block looks at the buffer:
-// cutting it back gives a higher bound for the chunks to come (a chunk passes
-// about k / c keys after c chunks).  No other barrier stands in the loop.
-// Nothing depends on the order blocks run in.
+// limited number.  A segment that overflows its room all the same (rising
+// logits) is read again in slices that fit, with the keys cut back to the k
+// best after each.  After chunk 1, 2, 4, 8 .. the block looks at what it
+// holds: cutting it back to k gives a higher bound for the chunks to come (a
+// chunk passes about k / c keys after c chunks).  No other barrier stands in
+// the loop.  Nothing depends on the order blocks run in.
+// Segments: four blocks per SM where the rows allow, never more than one
+// round of them (before the paired instructions, 64 rows of 248,320: 9 segments
+// 22.6 us, 7 24.7, 12 29.8; 800
+// rows of 52,755: 1 segment 46, 2 51, 5 67).
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"
@@ -38,6 +50,8 @@ static_assert(DVL_MAX_BEAMS <= 32 && kBeamKeys >= DVL_MAX_BEAMS, "one warp's lan
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBuffer = 8 * kThreads + kBeamKeys;  // a slice of 8 logits per thread, and the best so far
+constexpr int kVectors = 512;                      // vectors kept aside between two looks
+constexpr int kVectorsPerChunk = 4;                // per thread, in long segments
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -46,6 +60,40 @@ __device__ __forceinline__ float exp_diff(float d)  // e^d
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(d * kLog2e));
     return y;
+}
+
+// Two fp32 values in one register pair, and the instructions that work on both.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi)
+{
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(Pair p, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// e^(v - ref) of both values
+__device__ __forceinline__ Pair exp_diff2(Pair v, Pair minus_ref)
+{
+    float lo, hi;
+    unpair(mul2(add2(v, minus_ref), pair(kLog2e, kLog2e)), lo, hi);
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(lo));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(hi));
+    return pair(lo, hi);
 }
 
 // One 16-byte vector of logits as fp32.
@@ -58,6 +106,36 @@ __device__ __forceinline__ void widen(const uint4 &q, float (&v)[8])
 {
     v[0] = bf16_lo(q.x), v[1] = bf16_hi(q.x), v[2] = bf16_lo(q.y), v[3] = bf16_hi(q.y);
     v[4] = bf16_lo(q.z), v[5] = bf16_hi(q.z), v[6] = bf16_lo(q.w), v[7] = bf16_hi(q.w);
+}
+// Its values two by two (the type selects the width), and their maximum.
+__device__ __forceinline__ void pairs(const uint4 &q, Pair (&p)[2])
+{
+    p[0] = pair(__uint_as_float(q.x), __uint_as_float(q.y));
+    p[1] = pair(__uint_as_float(q.z), __uint_as_float(q.w));
+}
+__device__ __forceinline__ void pairs(const uint4 &q, Pair (&p)[4])
+{
+    p[0] = pair(bf16_lo(q.x), bf16_hi(q.x)), p[1] = pair(bf16_lo(q.y), bf16_hi(q.y));
+    p[2] = pair(bf16_lo(q.z), bf16_hi(q.z)), p[3] = pair(bf16_lo(q.w), bf16_hi(q.w));
+}
+__device__ __forceinline__ float max_of(const float *, const uint4 &q)
+{
+    float m = __uint_as_float(q.x);
+    asm("max.f32 %0, %0, %1, %2;"
+        : "+f"(m)
+        : "f"(__uint_as_float(q.y)), "f"(__uint_as_float(q.z)));
+    return fmaxf(m, __uint_as_float(q.w));
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float max_of(const uint16_t *, const uint4 &q)
+{
+    const uint32_t m = max_bf16x2(max_bf16x2(q.x, q.y), max_bf16x2(q.z, q.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
 }
 // The vector at row index n, -inf outside [0, end).
 __device__ __forceinline__ uint4 load_vector(const float *x, int n, int end)
@@ -84,16 +162,6 @@ __device__ __forceinline__ uint4 load_vector(const uint16_t *x, int n, int end)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <int N>
-__device__ __forceinline__ float max_of(const float (&v)[N])
-{
-    float m = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i)
-        m = fmaxf(m, v[i]);
-    return m;
-}
-
 struct Groups {
     uint64_t key[32];
     int rank[32];
@@ -101,10 +169,13 @@ struct Groups {
 
 struct Shared {
     uint64_t buffer[kBuffer];
+    uint4 vector[kVectors];
+    int row[kVectors];  // of a vector's first logit
     Groups groups;
     uint64_t best[kBeamKeys];
     float2 sums[kWarps];
     int n;           // keys in the buffer (may exceed its size: then it overflowed)
+    int vectors;     // likewise
     unsigned ticket;
 };
 
@@ -120,6 +191,26 @@ struct PickShared {
     int n_heads, n;
 };
 
+// The k best of the buffer's n keys, each to the place of its rank in `out`.
+// Up to eight threads share a key's comparisons.  Every thread calls it.
+__device__ __forceinline__ void rank_keys(const Shared &s, int n, int k, uint64_t *out)
+{
+    const int shift = n <= kThreads / 8 ? 3 : n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0;
+    const int share = threadIdx.x & ((1 << shift) - 1);
+    for (int first = 0; first < n; first += kThreads >> shift) {
+        const int i = first + (threadIdx.x >> shift);
+        const uint64_t key = i < n ? s.buffer[i] : 0ull;
+        int rank = 0;
+#pragma unroll 4
+        for (int j = share; j < n; j += 1 << shift)
+            rank += s.buffer[j] > key;
+        for (int off = 1 << shift >> 1; off >= 1; off >>= 1)
+            rank += __shfl_xor_sync(kFull, rank, off);
+        if (i < n && rank < k && share == 0)
+            out[rank] = key;
+    }
+}
+
 // Cut the buffer's n keys back to the k best, in order, and return the k-th
 // (0 when there are fewer).  Every thread calls it.
 __device__ __forceinline__ uint64_t prune(Shared &s, int n, int k)
@@ -127,15 +218,7 @@ __device__ __forceinline__ uint64_t prune(Shared &s, int n, int k)
     if (threadIdx.x < kBeamKeys)
         s.best[threadIdx.x] = 0ull;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint64_t key = s.buffer[i];
-        int rank = 0;
-#pragma unroll 4
-        for (int j = 0; j < n; ++j)
-            rank += s.buffer[j] > key;
-        if (rank < k)
-            s.best[rank] = key;
-    }
+    rank_keys(s, n, k, s.best);
     __syncthreads();
     if (threadIdx.x < k)
         s.buffer[threadIdx.x] = s.best[threadIdx.x];
@@ -304,6 +387,32 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     }
 }
 
+// The keys of one vector past a bound (ties: or at it) into the buffer.
+template <typename T>
+__device__ __forceinline__ void put_keys(Shared &s, const uint4 &q, int row, float bound, bool ties)
+{
+    constexpr int V = 16 / sizeof(T);
+    float v[V];
+    widen(q, v);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+        if (v[e] > bound || (v[e] == bound && ties)) {
+            const int at = atomicAdd(&s.n, 1);
+            if (at < kBuffer)
+                s.buffer[at] = make_key(v[e], row + e);
+        }
+}
+// Those of the n vectors kept aside, past the bound they were kept for; `begin`
+// is the row index of place 0.
+template <typename T>
+__device__ __forceinline__ void take_keys(Shared &s, int n, float bound, int place, int begin)
+{
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int row = s.row[i];
+        put_keys<T>(s, s.vector[i], row, bound, (row - begin) / (16 / (int)sizeof(T)) <= place);
+    }
+}
+
 // T: float, or uint16_t holding bf16.  NV: 16-byte vectors per thread and chunk,
 // one chunk in work and one in flight.  A row
 // may start anywhere: row index n is place n + lead of a sequence aligned to
@@ -314,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 {
     constexpr int V = 16 / sizeof(T);
     constexpr int E = NV * V;  // logits per thread and chunk
+    constexpr bool kAside = NV == kVectorsPerChunk;
     static_assert(V * kThreads + kBeamKeys <= kBuffer, "a slice fits the buffer");
     __shared__ union {
         Shared scan;
@@ -341,33 +451,41 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
     for (int j = 0; j < NV; ++j)
         next[j] = load_vector(x, begin + (j * kThreads + (int)threadIdx.x) * V, end);
     if (a.scores[row] > kNegInf) {
-        float m = kNegInf, sum = 0.f;
-        float bound = kNegInf;  // later rows must exceed it
+        float m = kNegInf;
+        Pair sum = 0ull;
+        float bound = kNegInf;  // keys must exceed it,
+        int place = -1;         // or reach it up to this place of the first chunk
         int chunk = 0;
         if (threadIdx.x == 0)
-            s.n = 0;
+            s.n = s.vectors = 0;
         if (threadIdx.x < 32)
             s.groups.rank[threadIdx.x] = 0;
         for (int base = begin; base < end; base += kThreads * E) {
             const int first = base + (int)threadIdx.x * V;
-            float v[NV][V];
+            uint4 work[NV];
+            float top_of[NV];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                widen(next[j], v[j]);
-                next[j] = load_vector(x, first + kThreads * E + j * kThreads * V, end);
+                work[j] = next[j];
+                top_of[j] = max_of(x, work[j]);
             }
-            float top = max_of(v[0]);
+            if (kAside && base + 2 * kThreads * E <= end) {  // (base + kThreads * E is above 0)
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    next[j] = ld_stream16(x + first + kThreads * E + j * kThreads * V);
+            } else {
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    next[j] = load_vector(x, first + kThreads * E + j * kThreads * V, end);
+            }
+            float top = top_of[0];
             int top_j = 0;
 #pragma unroll
-            for (int j = 1; j < NV; ++j) {
-                const float t = max_of(v[j]);
-                if (t > top) {
-                    top = t;
+            for (int j = 1; j < NV; ++j)
+                if (top_of[j] > top) {
+                    top = top_of[j];
                     top_j = j;
                 }
-            }
-            // the place up to which logits equal to the bound pass
-            int place = -1;
             if (base == begin) {
                 const uint64_t key = group_bound(
                     s.groups, top > kNegInf ? make_key(top, top_j * kThreads + threadIdx.x) : 0ull, k);
@@ -379,46 +497,73 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 
             const float m_new = fmaxf(m, top);
             const float ref = m_new == kNegInf ? 0.f : m_new;
-            sum *= exp_diff(m - ref);
+            const float scale = exp_diff(m - ref);
+            sum = mul2(sum, pair(scale, scale));
             m = m_new;
+            const Pair minus_ref = pair(-ref, -ref);
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
+            for (int j = 0; j < NV; ++j) {
+                Pair v[V / 2];
+                pairs(work[j], v);
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    sum += exp_diff(v[j][e] - ref);
+                for (int e = 0; e < V / 2; ++e)
+                    sum = add2(sum, exp_diff2(v[e], minus_ref));
+            }
 
-            // keys past the bound into the buffer; with no bound yet, all of them
-            auto passes = [&](float t, int j) {
-                return t > bound || (t == bound && j * kThreads + (int)threadIdx.x <= place);
-            };
+            // vectors with keys past the bound; with no bound yet, all of them
+            const int ties = base == begin ? place : -1;
             if (top >= bound) {
 #pragma unroll
-                for (int j = 0; j < NV; ++j)
-                    if (max_of(v[j]) >= bound)
-#pragma unroll
-                        for (int e = 0; e < V; ++e)
-                            if (passes(v[j][e], j)) {
-                                const int at = atomicAdd(&s.n, 1);
-                                if (at < kBuffer)
-                                    s.buffer[at] = make_key(v[j][e], first + j * kThreads * V + e);
+                for (int j = 0; j < NV; ++j) {
+                    const int row0 = first + j * kThreads * V;
+                    const bool tie = j * kThreads + (int)threadIdx.x <= ties;
+                    if (top_of[j] > bound || (top_of[j] == bound && tie)) {
+                        if constexpr (kAside) {
+                            const int at = atomicAdd(&s.vectors, 1);
+                            if (at < kVectors) {
+                                s.vector[at] = work[j];
+                                s.row[at] = row0;
                             }
+                        } else {
+                            put_keys<T>(s, work[j], row0, bound, tie);
+                        }
+                    }
+                }
             }
             ++chunk;
             if ((chunk & (chunk - 1)) == 0 && base + kThreads * E < end) {
                 __syncthreads();
-                const int count = s.n;
+                const int held = s.vectors;
+                int count = s.n;
                 __syncthreads();
-                if (count > 2 * k + 16 && count <= kBuffer) {
-                    const uint64_t kth = prune(s, count, k);
-                    if (kth)
-                        bound = key_logit(kth);
+                if (held + count > 2 * k + 16 && held <= kVectors) {
+                    if constexpr (kAside) {
+                        take_keys<T>(s, held, bound, place, begin);
+                        if (threadIdx.x == 0)
+                            s.vectors = 0;
+                        __syncthreads();
+                        count = s.n;
+                        __syncthreads();
+                    }
+                    if (count <= kBuffer) {
+                        const uint64_t kth = prune(s, count, k);
+                        if (kth) {
+                            bound = key_logit(kth);
+                            place = -1;
+                        }
+                    }
                 }
             }
         }
         __syncthreads();
+        const int held = s.vectors;
+        if (kAside && held <= kVectors) {
+            take_keys<T>(s, held, bound, place, begin);
+            __syncthreads();
+        }
         const int count = s.n;
         __syncthreads();
-        if (count > kBuffer) {
+        if (held > kVectors || count > kBuffer) {
             prune(s, 0, k);
             float least = kNegInf;
             for (int n0 = begin; n0 < end; n0 += kThreads * V) {
@@ -430,10 +575,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
                     if (v[e] > least)
                         s.buffer[atomicAdd(&s.n, 1)] = make_key(v[e], n + e);
                 __syncthreads();
-                const int held = s.n;
+                const int held_now = s.n;
                 __syncthreads();
-                if (held > kBeamKeys || n0 == begin) {
-                    const uint64_t kth = prune(s, held, k);
+                if (held_now > kBeamKeys || n0 == begin) {
+                    const uint64_t kth = prune(s, held_now, k);
                     least = kth ? key_logit(kth) : kNegInf;
                 }
             }
@@ -443,36 +588,28 @@ __global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const BeamArgs
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1)
             big = fmaxf(big, __shfl_xor_sync(kFull, big, off));
-        sum *= exp_diff(m - (big == kNegInf ? 0.f : big));
+        float even, odd;
+        unpair(sum, even, odd);
+        float total = (even + odd) * exp_diff(m - (big == kNegInf ? 0.f : big));
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1)
-            sum += __shfl_xor_sync(kFull, sum, off);
+            total += __shfl_xor_sync(kFull, total, off);
         if (lane == 0)
-            s.sums[warp] = make_float2(big, sum);
+            s.sums[warp] = make_float2(big, total);
         if (threadIdx.x < kBeamKeys)
             out[threadIdx.x] = 0ull;
         __syncthreads();
-        // the buffer's k best, each key at the place of its rank
-        const int n = s.n;
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint64_t key = s.buffer[i];
-            int rank = 0;
-#pragma unroll 4
-            for (int j = 0; j < n; ++j)
-                rank += s.buffer[j] > key;
-            if (rank < k)
-                out[rank] = key;
-        }
+        rank_keys(s, s.n, k, out);
         if (threadIdx.x == 0) {
             big = kNegInf;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
                 big = fmaxf(big, s.sums[w].x);
-            sum = 0.f;
+            total = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                sum += s.sums[w].y * exp_diff(s.sums[w].x - (big == kNegInf ? 0.f : big));
-            a.sums[blockIdx.x] = make_float2(big, sum);
+                total += s.sums[w].y * exp_diff(s.sums[w].x - (big == kNegInf ? 0.f : big));
+            a.sums[blockIdx.x] = make_float2(big, total);
         }
     } else {  // a dead beam
         if (threadIdx.x < kBeamKeys)
@@ -509,7 +646,7 @@ static cudaError_t launch(const BeamArgs &a, unsigned grid, cudaStream_t s)
     // Four vectors per thread keep 64 KB per SM in flight; a segment of the
     // least length runs through less code in a chunk of its own size.
     if (a.length > 2 * kLeast)
-        return launch_pdl(beam_select_kernel<T, 4>, grid, kThreads, 0, s, a);
+        return launch_pdl(beam_select_kernel<T, kVectorsPerChunk>, grid, kThreads, 0, s, a);
     return launch_pdl(beam_select_kernel<T, 8 * sizeof(T) / 16>, grid, kThreads, 0, s, a);
 }
 
