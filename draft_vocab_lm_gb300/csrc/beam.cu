@@ -33,10 +33,9 @@
 // holds: cutting it back to k gives a higher bound for the chunks to come (a
 // chunk passes about k / c keys after c chunks).  No other barrier stands in
 // the loop.  Nothing depends on the order blocks run in.
-// Segments: four blocks per SM where the rows allow, never more than one
-// round of them (before the paired instructions, 64 rows of 248,320: 9 segments
-// 22.6 us, 7 24.7, 12 29.8; 800
-// rows of 52,755: 1 segment 46, 2 51, 5 67).
+// Segments: four blocks per SM where the rows allow, never more than one round
+// of them (before the paired instructions, 64 rows of 248,320: 9 segments 22.6
+// us, 7 24.7, 12 29.8; 800 rows of 52,755: 1 segment 46, 2 51, 5 67).
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"

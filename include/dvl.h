@@ -332,9 +332,11 @@ typedef struct dvl_norm {
  * its element), DVL_ERR_CUDA. */
 dvl_status dvl_add_rmsnorm(const dvl_norm *args, void *stream);
 
-/* A paged key-value cache.  Strides are in elements; the D values of a head
- * are consecutive.  Every (page, token, head) row starts on a 16-byte
- * boundary. */
+/* A paged key-value cache.  Strides are in elements, not negative; the D
+ * values of a head are consecutive.  Every (page, token, head) row starts on a
+ * 16-byte boundary, and a page spans at most 10^9 elements (page_size token
+ * strides plus heads head strides: offsets within a page are 32-bit; pages may
+ * lie any distance apart). */
 typedef struct dvl_kv_cache {
     int32_t dtype;            /* DVL_BF16, or DVL_FP8 (E4M3 codes, one scale each) */
     int32_t pages;            /* pages of the pool                                 */
@@ -373,14 +375,16 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
  *             three, the last is 1; 16-byte aligned rows.
  *   table:    device int32 [B][table_width], row stride table_stride: the
  *             page of each page_size tokens.  Entries past a sequence's
- *             length are not read.  An entry outside [0, pages) reads as
- *             zeros and sets the status bit DVL_ERR_OUT_OF_RANGE.
+ *             length are not read.  An entry outside [0, pages) sets the
+ *             status bit DVL_ERR_OUT_OF_RANGE, and page 0 is read in its
+ *             place: that sequence's result says nothing, other sequences are not touched.
  *   lengths:  device int32 [B].  Below 0 counts as 0; above
  *             table_width * page_size is cut to that, with the same bit.
  *   out:      device bf16 [B][T][Hq][D] contiguous, 16-byte aligned.
  *   lse:      device fp32 [B][T][Hq] contiguous, or NULL.
  *   ws:       dvl_attention_workspace_bytes, from dvl_workspace_init.
- * Errors: DVL_ERR_INVALID_ARG (NULL or misaligned, B or T or Hq < 1, T above
+ * B = 0 enqueues nothing.
+ * Errors: DVL_ERR_INVALID_ARG (NULL or misaligned, B < 0, T or Hq < 1, T above
  * DVL_MAX_QUERY, Hq not a multiple of heads, T * G above DVL_MAX_QUERY_ROWS,
  * D not a multiple of 16 or above DVL_MAX_HEAD_DIM, page_size * table_width
  * above 2^31 - 1, scale not finite), DVL_ERR_WORKSPACE, DVL_ERR_CUDA. */

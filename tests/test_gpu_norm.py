@@ -1,9 +1,9 @@
 """dvl_add_rmsnorm against the 64-bit form.
 
 Bounds: a thread adds at most 24 squares, two five-step butterflies follow, so
-the mean square is off by at most 36 u and its root by half that; the root,
-the division, two products and the addition of the residual round once or
-twice each: y is within 28 u.  bf16 then adds 2^-8.  A code is the nearest
+the mean square is off by at most 36 u and its root by half that; the
+reciprocal root is within 4 u, 1 / K, its product, two products and the
+addition of the residual round once each: y is within 28 u.  bf16 then adds 2^-8.  A code is the nearest
 E4M3 value of y / scale: half a step is at most 2^-4 of the quotient or, below
 the normal range, 2^-10."""
 import numpy as np
