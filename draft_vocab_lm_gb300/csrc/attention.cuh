@@ -255,6 +255,7 @@ template <int DP, bool FP8, int RT, int TOK, int P, int G>
 struct Shape {
     static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kTile = TOK * G;
+    static_assert(kTile <= 128, "lengths are limited so that a tile more fits 32 bits");
     static constexpr int kGroup = RT == 0 ? 32 : 32 * RT;  // threads
     static constexpr int kThreads = kGroup * G;
     // Rows that one access phase touches lie on distinct banks.  bf16: the

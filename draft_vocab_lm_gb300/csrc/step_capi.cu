@@ -141,7 +141,7 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     if (rows == 0 || B < 0 || (int64_t)B * cache->heads * rows > 0x7fffffffLL)
         return DVL_ERR_INVALID_ARG;
     if (table_width < 1 || table_stride < 0 ||
-        (int64_t)table_width * cache->page_size > 0x7fffffffLL - 64)  // a tile more than the last token
+        (int64_t)table_width * cache->page_size > 0x7fffffffLL - 127)  // rounding up to a tile fits
         return DVL_ERR_INVALID_ARG;
     if (!q || !aligned(q, 16) || !table || !aligned(table, 4) || !lengths || !aligned(lengths, 4) ||
         !out || !aligned(out, 16) || !aligned(lse, 4))

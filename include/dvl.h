@@ -387,7 +387,7 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
  * Errors: DVL_ERR_INVALID_ARG (NULL or misaligned, B < 0, T or Hq < 1, T above
  * DVL_MAX_QUERY, Hq not a multiple of heads, T * G above DVL_MAX_QUERY_ROWS,
  * D not a multiple of 16 or above DVL_MAX_HEAD_DIM, page_size * table_width
- * above 2^31 - 1, scale not finite), DVL_ERR_WORKSPACE, DVL_ERR_CUDA. */
+ * above 2^31 - 128, scale not finite), DVL_ERR_WORKSPACE, DVL_ERR_CUDA. */
 dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t q_batch_stride,
                                int64_t q_token_stride, int64_t q_head_stride, int32_t B, int32_t T,
                                int32_t Hq, const int32_t *table, int64_t table_stride,

@@ -78,7 +78,7 @@ def test_cache_checks(L, bad):
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(q=0x3008), dict(qb=252), dict(qt=4), dict(qh=65), dict(B=-1), dict(T=0), dict(T=9), dict(Hq=0),
     dict(Hq=3), dict(Hq=130), dict(T=8, Hq=18), dict(table=None), dict(table=0x4002), dict(ts=-1), dict(width=0),
-    dict(width=1 << 27), dict(lengths=None), dict(lengths=0x5001), dict(scale=float("nan")), dict(scale=float("inf")),
+    dict(width=1 << 27), dict(width=(1 << 27) - 7), dict(lengths=None), dict(lengths=0x5001), dict(scale=float("nan")), dict(scale=float("inf")),
     dict(out=None), dict(out=0x6004), dict(lse=0x6002),
 ])
 def test_attention_checks(L, bad):
