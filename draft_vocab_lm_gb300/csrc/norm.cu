@@ -4,8 +4,8 @@
 //   per group: a = max |y|, scale = a / 448, code = RNE_e4m3(y (448 / a)).
 //
 // Bound by HBM (6 flops per element against 5 to 13 bytes).  A team takes one
-// row: a warp up to 1,024 values (eight rows per block: a block per row of 80
-// took 10.6 us for 9,999 rows, a warp 3), else a block of up to 1,024
+// row: a warp for short rows (eight per block: a block per row of 80 took 10.6
+// us for 9,999 rows, a warp 3), else a block of up to 1,024
 // threads.  A thread owns 8 values per step (one 16-byte load of a bf16
 // tensor), keeps u in registers between the sum and the output, and reads
 // every input once.  Many small teams hide each other's latencies; a loop over
@@ -406,14 +406,18 @@ template <typename R, bool WIDE>
 cudaError_t launch(const NormArgs &p, cudaStream_t s)
 {
     const int steps = (p.a.K + 255) / 256;  // of 256 values
-    if (steps <= 4) {
+    // A warp takes a row of up to 256 values, and one of up to 512 when the
+    // rows are many: 7,737 rows of 504 4.7 us, a block each 8.2; 99 rows 1.8
+    // and 1.6.  With element accesses a warp issues eight times as many, and
+    // the turn comes later: 999 rows of 511 4.3 and 3.2, 7,737 of 331 7.0 and
+    // 8.7.  (A warp per row of 1,001 values: 43.7 us for 7,737 rows, 10.1 for
+    // 99; a block each 19.5 and 3.0.)
+    if (steps == 1 || (steps == 2 && p.a.rows >= (WIDE ? 768 : 4096))) {
         const unsigned grid = (unsigned)((p.a.rows + kRowsPerBlock - 1) / kRowsPerBlock);
         const int threads = 32 * kRowsPerBlock;
         if (steps == 1)
             return launch_pdl(add_rmsnorm_kernel<R, WIDE, 1, false>, grid, threads, 0, s, p);
-        if (steps == 2)
-            return launch_pdl(add_rmsnorm_kernel<R, WIDE, 2, false>, grid, threads, 0, s, p);
-        return launch_pdl(add_rmsnorm_kernel<R, WIDE, 4, false>, grid, threads, 0, s, p);
+        return launch_pdl(add_rmsnorm_kernel<R, WIDE, 2, false>, grid, threads, 0, s, p);
     }
     const int nc = (steps + 31) / 32;
     const int threads = 32 * ((steps + nc - 1) / nc);
