@@ -23,7 +23,8 @@
 //     segments, which pass few, that costs less than the second look.)
 //   - The last block of a request (a wrapping ticket) joins the segments' sums
 //     into lse, turns keys into scores, and picks: a segment list whose head
-//     has r better heads can give its first k - r keys only.
+//     has r better heads can give its first k - r keys only.  Four keys of
+//     every list come with its head, more only where the fourth is good enough.
 // Ties are exact: bounds carry the place of their logit, rows are read in
 // order, and later rows have to exceed a bound, not to reach it, so rows of
 // equal logits (a constant row, a mask of the type's lowest value) pass in
@@ -180,8 +181,10 @@ struct Shared {
 
 // The second half's view of the same shared memory.
 constexpr int kPairs = DVL_MAX_BEAMS * (DVL_MAX_BEAMS + 1) / 2;  // keys r lists of k can give
+constexpr int kFront = 4;  // keys of a list that are read with its head
 struct PickShared {
-    uint64_t hi[kBeamLists], lo[kBeamLists];  // heads: (score, beam), (logit, row)
+    uint64_t hi[kBeamLists];          // of the heads: (score, beam)
+    uint64_t lo[kBeamLists][kFront];  // of the lists' first keys: (logit, row)
     int16_t list_of[kBeamLists];
     uint64_t c_hi[kPairs], c_lo[kPairs];  // candidates
     Groups groups;
@@ -276,11 +279,15 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     const uint64_t *keys = a.keys + row0 * a.segments * kBeamKeys;
     constexpr int kHeads = (kBeamLists + kThreads - 1) / kThreads;  // per thread
     const float base = threadIdx.x < a.beams ? a.scores[row0 + threadIdx.x] : 0.f;
-    uint64_t head[kHeads];  // in flight while the sums are joined
+    ulonglong2 front[kHeads][kFront / 2];  // in flight while the sums are joined
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         const int list = i * kThreads + (int)threadIdx.x;
-        head[i] = list < heads ? __ldcg(keys + (int64_t)list * kBeamKeys) : 0ull;
+#pragma unroll
+        for (int j = 0; j < kFront / 2; ++j)
+            front[i][j] = list < heads ? __ldcg(reinterpret_cast<const ulonglong2 *>(
+                                             keys + (int64_t)list * kBeamKeys) + j)
+                                       : make_ulonglong2(0ull, 0ull);
     }
     for (int beam = warp; beam < a.beams; beam += kWarps) {
         const float2 *ms = a.sums + (row0 + beam) * a.segments;
@@ -320,7 +327,7 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
 #pragma unroll
     for (int i = 0; i < kHeads; ++i) {
         const int list = i * kThreads + (int)threadIdx.x;
-        head_hi[i] = head[i] ? score_of(head[i], list / a.segments) : 0ull;
+        head_hi[i] = front[i][0].x ? score_of(front[i][0].x, list / a.segments) : 0ull;
         top = head_hi[i] > top ? head_hi[i] : top;
     }
     const uint64_t bound = group_bound(s.groups, top, a.k);
@@ -329,33 +336,44 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
         if (head_hi[i] && head_hi[i] >= bound) {
             const int at = atomicAdd(&s.n_heads, 1);
             s.hi[at] = head_hi[i];
-            s.lo[at] = head[i];
+#pragma unroll
+            for (int j = 0; j < kFront / 2; ++j) {
+                s.lo[at][2 * j] = front[i][j].x;
+                s.lo[at][2 * j + 1] = front[i][j].y;
+            }
             s.list_of[at] = (int16_t)(i * kThreads + threadIdx.x);
         }
     __syncthreads();
     // the k best of them in order
     const int n_heads = s.n_heads;
     for (int i = threadIdx.x; i < n_heads; i += kThreads) {
-        const uint64_t hi = s.hi[i], lo = s.lo[i];
+        const uint64_t hi = s.hi[i], lo = s.lo[i][0];
         int rank = 0;
 #pragma unroll 4
         for (int j = 0; j < n_heads; ++j)
-            rank += better(s.hi[j], s.lo[j], hi, lo);
+            rank += better(s.hi[j], s.lo[j][0], hi, lo);
         if (rank < a.k)
             s.head[rank] = i;
     }
     __syncthreads();
     // what is no better than the k-th head is none of the k best
     const int last = s.head[a.k - 1];
-    const uint64_t floor_hi = last >= 0 ? s.hi[last] : 1ull, floor_lo = last >= 0 ? s.lo[last] : 0ull;
+    const uint64_t floor_hi = last >= 0 ? s.hi[last] : 1ull, floor_lo = last >= 0 ? s.lo[last][0] : 0ull;
+    auto enough = [&](uint64_t hi, uint64_t key) {
+        return hi && !better(floor_hi, floor_lo, hi, key);
+    };
     for (int i = threadIdx.x; i < a.k * a.k; i += kThreads) {
         const int r = i / a.k, j = i - r * a.k, h = s.head[r];
         if (r + j >= a.k || h < 0)
             continue;
-        const int list = s.list_of[h];
-        const uint64_t key = __ldcg(keys + (int64_t)list * kBeamKeys + j);
-        const uint64_t hi = key ? score_of(key, list / a.segments) : 0ull;
-        if (hi && !better(floor_hi, floor_lo, hi, key)) {
+        const int list = s.list_of[h], beam = list / a.segments;
+        uint64_t key = s.lo[h][j < kFront ? j : kFront - 1];
+        uint64_t hi = key ? score_of(key, beam) : 0ull;
+        if (j >= kFront && enough(hi, key)) {  // (lists descend)
+            key = __ldcg(keys + (int64_t)list * kBeamKeys + j);
+            hi = key ? score_of(key, beam) : 0ull;
+        }
+        if (enough(hi, key)) {
             const int at = atomicAdd(&s.n, 1);
             s.c_hi[at] = hi;
             s.c_lo[at] = key;
