@@ -8,7 +8,7 @@
 // instruction and every key pushed by its own thread 142 us), and a chain of
 // dependent steps few rows: about 5 us until the last segment has left its
 // keys and 2 to 4 us to pick (64 rows of 248,320, k = 16: 20.7 us of which
-// 9.5 are HBM time; 4 rows of 16,000: 6.4 us).  One launch:
+// 9.5 are HBM time; 4 rows of 16,000: 6.2 us).  One launch:
 //   - A block takes one segment of a row, in chunks that sit in registers.
 //     Every thread keeps the maximum and the sum of exponentials of what it
 //     has seen, two logits per instruction.  Within one beam the order of the

@@ -128,6 +128,35 @@ def test_beam_rows_that_overflow_the_buffer(dvl, bf16):
                dvl.beam_select(x[:, j:j + 1].cuda(), scores[:, j:j + 1].contiguous().cuda(), 32))
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("k", [4, 32])
+def test_beam_long_segments(dvl, k, bf16):
+    # so many rows that each is one segment of several chunks: every way a
+    # segment's room can fill, and ties at every bound
+    N, beams, batch = 40001, 4, 152
+    g = torch.Generator().manual_seed(k)
+    pool = torch.randn(beams, N, generator=g)
+    logits = pool[None].repeat(batch, 1, 1)
+    logits[0] = torch.linspace(-20, 20, N)                                    # rising: everything passes
+    logits[1] = torch.arange(N).remainder(9000).float() / 300                 # a saw
+    logits[2] = 2.5                                                           # all equal
+    logits[3] = -INF
+    logits[3, :, 20000:25000] = torch.randn(beams, 5000, generator=g)         # an island of candidates
+    logits[4] = torch.finfo(torch.float32).min
+    logits[4, 1, 39990:] = torch.arange(11).float()                           # eleven rows left by a mask
+    logits[5] = (torch.arange(N) % 97 == 5).float()                           # two values only
+    logits[6, :, :16384] = pool[:, :16384] - 30                               # the first chunks say nothing
+    logits[7, :, 4096:4160] = 9.0                                             # a plateau past the first bound
+    scores = -5 * torch.rand(batch, beams, generator=g)
+    scores[2], scores[5] = 0.0, 0.0
+    x = logits.bfloat16() if bf16 else logits
+    got = dvl.beam_select(x.cuda(), scores.cuda(), k)
+    for b in list(range(9)) + [batch - 1]:
+        verify(x[b:b + 1].float().numpy(), scores[b:b + 1].numpy(), k, tuple(t[b:b + 1] for t in got))
+    assert list(zip(got[1][2].tolist(), got[2][2].tolist())) == [(0, n) for n in range(k)]
+    assert list(zip(got[1][5].tolist(), got[2][5].tolist())) == [(0, 97 * i + 5) for i in range(k)]
+
+
 def test_beam_masked_dead_and_non_finite(dvl):
     logits, scores = make(3, 6, 4, 5000)
     scores[0, 1:] = -INF            # the first step: one live beam
