@@ -43,20 +43,27 @@
 // Up to 8 query rows (RT = 0) the upper half of every MMA is padding: its
 // softmax is left out and its accumulators are not kept.
 //
-// Weights are rounded to the MMA operand type: 2^-9 relative for bf16, 2^-12
-// for f16, independent per position, so it averages out over the positions
-// that matter; sums and statistics stay fp32.  Scores are kept in units of
-// log2 (the scale carries log2 e), so a weight is one ex2.
+// Weights are rounded to the MMA operand type, at most 2^-8 relative for bf16
+// and 2^-11 for f16, independently per position; sums and statistics stay
+// fp32.  That keeps the second product on the tensor cores and costs little
+// next to the output's own rounding to bf16 (error against 64 bits 1.00 to
+// 1.07 of that with fp32 weights over short to long caches).  f16 weights are
+// multiplied by 2^15 first (the largest is 1): they are normal numbers down to
+// 2^-29 of the largest and lie on a grid of 2^-39 below, so a long tail far
+// under one position keeps its share, which unscaled it lost (40,000 positions
+// 18 nats down: all of it).  Output sums are in that unit until they are
+// divided.  Scores are kept in units of log2 (the scale carries log2 e), so a
+// weight is one ex2.
 //
 // Operands.  bf16 cache: mma m16n8k16 bf16, K and V by ldmatrix (V
 // transposed).  FP8 cache: E4M3 pairs are widened to f16 (exact) in
 // registers, mma m16n8k16 f16; a query row is multiplied by a power of two
 // that puts its largest value in [2^14, 2^15), which keeps every bf16 value
 // down to 2^-29 of the row's largest exact in f16 (smaller ones round to the
-// f16 subnormal grid, 2^-39 of the largest), and the power is taken out of
-// the score's fp32 scale.  The order of the D values inside an MMA is
-// permuted so that a lane's FP8 bytes are consecutive; Q is stored in the
-// same order.
+// f16 subnormal grid, at most 2^-38 of the largest), and the power is taken
+// out of the score's fp32 scale.  The order of the D values inside an MMA is
+// permuted so that a lane's FP8 bytes are consecutive; Q is stored in the same
+// order.
 //
 // Masks.  Row t sees n = length - (T - 1 - t) positions.  Scores at or past
 // n are replaced, not added to, so nothing a masked key holds can show; a
@@ -192,6 +199,13 @@ __device__ __forceinline__ float unpack1(uint16_t x)
     } else {
         return __uint_as_float((uint32_t)x << 16);
     }
+}
+
+// Two weights as operands of the second product: f16 ones in units of 2^-15.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi)
+{
+    return F16 ? pack2<true>(lo * kF16Weight, hi * kF16Weight) : pack2<false>(lo, hi);
 }
 
 // Two E4M3 bytes -> two f16 (exact); four bytes -> two such pairs.
@@ -493,7 +507,7 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, 
     const int t = a.token_of(r);
     const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
     // a row without positions (or of -inf scores only): 0
-    const float inv = sum == 0.f ? 0.f : a.v_scale / sum;
+    const float inv = sum == 0.f ? 0.f : a.v_scale / (sum * a.weight_one);
     *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
         make_uint2(pack2<false>(acc.x * inv, acc.y * inv), pack2<false>(acc.z * inv, acc.w * inv));
     if (a.lse && d == 0)
@@ -926,11 +940,13 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             }
 #pragma unroll
             for (int k = 0; k < TOK / 16; ++k) {
-                pa[k][0] = pack2<FP8>(s[2 * k][0], s[2 * k][1]);
-                pa[k][1] = NJ == 2 ? pack2<FP8>(s[2 * k][2 * NJ - 2], s[2 * k][2 * NJ - 1]) : 0u;
-                pa[k][2] = pack2<FP8>(s[2 * k + 1][0], s[2 * k + 1][1]);
-                pa[k][3] =
-                    NJ == 2 ? pack2<FP8>(s[2 * k + 1][2 * NJ - 2], s[2 * k + 1][2 * NJ - 1]) : 0u;
+                pa[k][0] = pack_weights<FP8>(s[2 * k][0], s[2 * k][1]);
+                pa[k][1] =
+                    NJ == 2 ? pack_weights<FP8>(s[2 * k][2 * NJ - 2], s[2 * k][2 * NJ - 1]) : 0u;
+                pa[k][2] = pack_weights<FP8>(s[2 * k + 1][0], s[2 * k + 1][1]);
+                pa[k][3] = NJ == 2 ? pack_weights<FP8>(s[2 * k + 1][2 * NJ - 2],
+                                                       s[2 * k + 1][2 * NJ - 1])
+                                   : 0u;
             }
         }
 
@@ -962,7 +978,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                         float mine = tok & 8 ? pair[1] : pair[0];
                         if constexpr (kSN == 4)
                             mine = tok & 16 ? (tok & 8 ? pair[3] : pair[2]) : mine;
-                        w[j] = __shfl_sync(kFull, mine, src);
+                        w[j] = __shfl_sync(kFull, FP8 ? mine * kF16Weight : mine, src);
                     }
 #pragma unroll
                     for (int n = 0; n < kNT; ++n)

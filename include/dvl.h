@@ -366,10 +366,12 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
  *   out = v_scale * sum_j exp(s_j - m) v_j / sum_j exp(s_j - m)
  *   lse = m + ln(sum_j exp(s_j - m))
  * n = 0 gives out 0 and lse -inf.  Positions at or above n are not read into
- * the result, whatever the cache holds there.  Products are exact, sums and
- * softmax statistics fp32; the weights exp(s_j - m) are rounded to the
- * matrix instruction's operand type (bf16, or f16 with an FP8 cache) before
- * they meet V.  The result does not depend on timing: the same call on the
+ * the result, whatever the cache holds there.  Sums and softmax statistics are
+ * fp32.  Products are exact, except that with an FP8 cache query values below
+ * 2^-29 of their row's largest are rounded to a grid of 2^-38 of it.  The
+ * weights exp(s_j - m) are rounded before they meet V: to bf16 (2^-8
+ * relative), or with an FP8 cache to f16 (2^-11 relative down to 2^-29, a grid
+ * of 2^-39 below).  The result does not depend on timing: the same call on the
  * same device gives the same bits.
  *   q:        device bf16 [B][T][Hq][D]; strides in elements for the first
  *             three, the last is 1; 16-byte aligned rows.
