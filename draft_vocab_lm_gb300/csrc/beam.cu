@@ -1,6 +1,9 @@
 // Beam selection: log-softmax of every beam's logits, the beam's score added,
 // and the k best (beam, row) pairs of a request:
-//   score(j, n) = scores[j] + (x[j][n] - lse_j),  lse_j = m + ln sum e^{x - m}.
+//   score(j, n) = scores[j] + ((x[j][n] - m_j) - ln sum_n e^{x[j][n] - m_j}),
+// m_j the row's largest logit.  m and the logarithm stay apart: their sum would
+// lose the logarithm in a row of large numbers, wholly in one of the type's
+// lowest value (a mask), whose rows are uniform and score -ln N, not 0.
 //
 // Each logit is read once and costs one exponential and a maximum: HBM bounds
 // many long fp32 rows (512 rows of 248,320: 0.91 of the copy rate), issue slots
@@ -21,9 +24,9 @@
 //     best are written out.  (A whole vector is put aside because a warp with
 //     one passing logit in eight runs through all eight tests: on short
 //     segments, which pass few, that costs less than the second look.)
-//   - The last block of a request (a wrapping ticket) joins the segments' sums
-//     into lse, turns keys into scores, and picks: a segment list whose head
-//     has r better heads can give its first k - r keys only.  Four keys of
+//   - The last block of a request (a wrapping ticket) joins the segments'
+//     maxima and sums, turns keys into scores, and picks: a segment list whose
+//     head has r better heads can give its first k - r keys only.  Four keys of
 //     every list come with its head, more only where the fourth is good enough.
 // Ties are exact: bounds carry the place of their logit, rows are read in
 // order, and later rows have to exceed a bound, not to reach it, so rows of
@@ -188,7 +191,8 @@ struct PickShared {
     int16_t list_of[kBeamLists];
     uint64_t c_hi[kPairs], c_lo[kPairs];  // candidates
     Groups groups;
-    float lse[DVL_MAX_BEAMS], base[DVL_MAX_BEAMS];  // per beam, its score
+    // per beam: the largest logit, the logarithm of the sum, the beam's score
+    float big[DVL_MAX_BEAMS], log_sum[DVL_MAX_BEAMS], base[DVL_MAX_BEAMS];
     int head[DVL_MAX_BEAMS];              // the k best heads, in order
     int n_heads, n;
 };
@@ -309,8 +313,10 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1)
             sum += __shfl_xor_sync(kFull, sum, off);
-        if (lane == 0)
-            s.lse[beam] = m + logf(sum);
+        if (lane == 0) {
+            s.big[beam] = m;
+            s.log_sum[beam] = logf(sum);
+        }
     }
     if (threadIdx.x < DVL_MAX_BEAMS) {
         s.head[threadIdx.x] = -1;
@@ -321,7 +327,7 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
         s.n = s.n_heads = 0;
     __syncthreads();
     auto score_of = [&](uint64_t key, int beam) {
-        return score_key(s.base[beam] + (key_logit(key) - s.lse[beam]), beam);
+        return score_key(s.base[beam] + ((key_logit(key) - s.big[beam]) - s.log_sum[beam]), beam);
     };
     uint64_t head_hi[kHeads], top = 0ull;
 #pragma unroll

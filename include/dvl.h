@@ -404,8 +404,8 @@ size_t dvl_beam_workspace_bytes(int32_t batch, int32_t beams, int32_t N);
 
 /* Beam search's choice of the next beams.  For request b, beam j and row n of
  * the head:
- *   score(j, n) = scores[b][j] + (logits[b][j][n] - lse(b, j)),
- *   lse(b, j) = ln sum_n exp(logits[b][j][n])        (in fp32),
+ *   x = logits[b][j],  m = max_i x[i],
+ *   score(j, n) = scores[b][j] + ((x[n] - m) - ln sum_i exp(x[i] - m))   (in fp32),
  * and the k best candidates of the request, best first.  Equal scores: the
  * lower beam first; within a beam the larger logit, then the lower row.  A
  * score of -inf or NaN is no candidate (a dead beam's -inf score, a banned
