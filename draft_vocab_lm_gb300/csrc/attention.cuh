@@ -85,6 +85,7 @@ namespace attn {
 
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kJoin = 16;  // parts per first-level join
+constexpr float kF16Weight = 32768.f;  // a weight of 1 among f16 operands (FP8 caches)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
@@ -501,13 +502,14 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a)
 }
 
 // Four columns of a finished row: the sums over their weights' sum.
+template <bool FP8>
 __device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, int d,
                                         const float4 &acc, float m, float sum)
 {
     const int t = a.token_of(r);
     const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
     // a row without positions (or of -inf scores only): 0
-    const float inv = sum == 0.f ? 0.f : a.v_scale / (sum * a.weight_one);
+    const float inv = sum == 0.f ? 0.f : a.v_scale / (FP8 ? sum * kF16Weight : sum);
     *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
         make_uint2(pack2<false>(acc.x * inv, acc.y * inv), pack2<false>(acc.z * inv, acc.w * inv));
     if (a.lse && d == 0)
@@ -520,7 +522,7 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, 
 // that part's own.  Every thread takes 4 columns of R rows at a time and runs
 // through the parts with a running maximum, kBatch parts' loads in flight; no
 // shared memory and no barrier.
-template <int DP, int THREADS, int R>
+template <int DP, bool FP8, int THREADS, int R>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, int second,
                                            int stride, int stats, bool last, int b, int h)
 {
@@ -586,7 +588,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, 
             if (r >= a.rows)
                 continue;
             if (last) {
-                put_row(a, b, h, r, d, acc[k], m[k], sum[k]);
+                put_row<FP8>(a, b, h, r, d, acc[k], m[k], sum[k]);
             } else {
                 // (the part's own statistics may still be read by other threads)
                 *reinterpret_cast<float4 *>(to_part + r * a.D + d) = acc[k];
@@ -606,7 +608,7 @@ struct Part {
 
 // Count the part in; the last block of a group of parts joins them, the last
 // of the groups those.  Every thread calls it, after the part's last write.
-template <int DP, int THREADS, int R>
+template <int DP, bool FP8, int THREADS, int R>
 __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &share, const Part &p,
                                             int *s_last)
 {
@@ -638,7 +640,7 @@ __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &shar
         if (!*s_last)
             return;
         const bool last_level = level == 1 || groups == 1;
-        join_parts<DP, THREADS, R>(a, parts, slot_a, slot_b, stride, stats, last_level, p.b, p.h);
+        join_parts<DP, FP8, THREADS, R>(a, parts, slot_a, slot_b, stride, stats, last_level, p.b, p.h);
         if (last_level)
             return;
         parts = groups;
@@ -1120,7 +1122,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                             sum = fmaf(stat[w * S::kRows + r].y,
                                        ex2(stat[w * S::kRows + r].x - ref), sum);
                         if (whole) {
-                            put_row(a, cur.b, cur.h, r, c0 + d, acc, big, sum);
+                            put_row<FP8>(a, cur.b, cur.h, r, c0 + d, acc, big, sum);
                         } else {
                             *reinterpret_cast<float4 *>(part + r * a.D + c0 + d) = acc;
                             if (c0 + d == 0)
@@ -1133,7 +1135,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     __syncthreads();
             }
             if (!whole)
-                finish_part<DP, kThreads, BLOCKS >= 3 ? 1 : 2>(
+                finish_part<DP, FP8, kThreads, BLOCKS >= 3 ? 1 : 2>(
                     a, share, {share.u1 - left - cur.t, cur.tiles, cur.b, cur.h}, &s_last);
             if (left == 1)
                 break;

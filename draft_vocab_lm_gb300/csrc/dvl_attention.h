@@ -7,8 +7,6 @@
 namespace dvl {
 namespace attn {
 
-constexpr float kF16Weight = 32768.f;  // a weight of 1 among f16 operands (FP8 caches)
-
 struct AttnArgs {
     const uint16_t *q;        // bf16
     int64_t qb, qt, qh;       // strides in elements: sequence, token, head
@@ -34,7 +32,6 @@ struct AttnArgs {
     int page_shift;
     float qk_scale;           // scale * k_scale * log2(e)
     float v_scale;
-    float weight_one;         // what a weight of 1 adds to an output sum
     int blocks;               // of the grid
     int lanes;                // blocks that walk the same tokens, one head each
 

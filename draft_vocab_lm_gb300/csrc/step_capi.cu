@@ -203,7 +203,6 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.page_mul = (uint32_t)((1ull << a.page_shift) / (uint64_t)cache->page_size + 1);
     a.qk_scale = scale * cache->k_scale * 1.4426950408889634f;
     a.v_scale = cache->v_scale;
-    a.weight_one = fp8 ? attn::kF16Weight : 1.f;
     return done(attn::launch_attention(a, cfg, static_cast<cudaStream_t>(stream)));
 }
 
