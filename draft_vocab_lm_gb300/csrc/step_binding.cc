@@ -406,7 +406,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
         Workspace ws;
         if (const Tensor *t = a.tensor(8, "ws")) {
             ws.set(*t, dev);
-        } else {
+        } else if (B > 0) {
             ws.owned = new_workspace("attention_workspace",
                                      Py_BuildValue("(OLLL)", a.v[0], (long long)B, (long long)T,
                                                    (long long)Hq),
@@ -414,13 +414,14 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
             ws.set(THPVariable_Unpack(ws.owned), dev);
         }
         const float scale = (float)a.number(4, 1.0 / std::sqrt((double)D));
-        check("dvl_paged_attention",
-              dvl_paged_attention(cache, q.data_ptr(), B > 1 ? q.stride(0) : 0,
-                                  dim == 4 && T > 1 ? q.stride(1) : 0, Hq > 1 ? q.stride(dim - 2) : 0,
-                                  (int32_t)B, (int32_t)T, (int32_t)Hq,
-                                  static_cast<const int32_t *>(table.data_ptr()),
-                                  B > 1 ? table.stride(0) : 0, (int32_t)table.size(1), pl, scale, po, pe,
-                                  ws.p, ws.bytes, stream_of(a.v[9], dev)));
+        if (B > 0)
+            check("dvl_paged_attention",
+                  dvl_paged_attention(cache, q.data_ptr(), B > 1 ? q.stride(0) : 0,
+                                      dim == 4 && T > 1 ? q.stride(1) : 0,
+                                      Hq > 1 ? q.stride(dim - 2) : 0, (int32_t)B, (int32_t)T,
+                                      (int32_t)Hq, static_cast<const int32_t *>(table.data_ptr()),
+                                      B > 1 ? table.stride(0) : 0, (int32_t)table.size(1), pl, scale,
+                                      po, pe, ws.p, ws.bytes, stream_of(a.v[9], dev)));
         PyObject *t = PyTuple_New(2);
         PyTuple_SET_ITEM(t, 0, wrap(out, a.v[5], new_out));
         PyTuple_SET_ITEM(t, 1, want_lse ? wrap(lse, a.v[6], new_lse) : Py_NewRef(Py_None));
