@@ -83,23 +83,29 @@ class KVCache:
         self._dev = k.get_device()
 
 
+def _workspace(n: int, device, stream):
+    """n zeroed bytes on the device."""
+    torch = _t()
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        workspace_init(ws, stream)
+    return ws
+
+
 def attention_workspace(cache: KVCache, B: int, T: int, Hq: int, *, stream=None):
     """A zeroed workspace for paged_attention calls with this cache, T new
     tokens per sequence and Hq query heads (any batch: B is not used)."""
-    n = int(lib().dvl_attention_workspace_bytes(cache._struct, T, Hq))
-    _need(n > 0, "T or Hq outside the library's limits")
-    ws = _t().empty(n, dtype=_t().uint8, device=cache.device)
-    workspace_init(ws, stream)
-    return ws
+    with _t().cuda.device(cache.device):
+        n = int(lib().dvl_attention_workspace_bytes(cache._struct, T, Hq))
+        _need(n > 0, "T or Hq outside the library's limits")
+        return _workspace(n, cache.device, stream)
 
 
 def beam_workspace(batch: int, beams: int, N: int, k: int = 1, *, device=None, stream=None):
     """A zeroed workspace for beam_select calls of this size (any k)."""
     n = int(lib().dvl_beam_workspace_bytes(batch, beams, N))
     _need(n > 0, "batch, beams or N outside the library's limits")
-    ws = _t().empty(n, dtype=_t().uint8, device=device or "cuda")
-    workspace_init(ws, stream)
-    return ws
+    return _workspace(n, device or "cuda", stream)
 
 
 def _beam_workspace_on(batch: int, beams: int, N: int, device: int, *, stream=None):
