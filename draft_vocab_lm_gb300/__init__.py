@@ -48,6 +48,28 @@ def _stream_handle(stream, device) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream):
+    """Uninitialised memory for work on `stream`.  On another stream than the
+    device's current one it is taken from and returns to that stream's own
+    memory, so that no work of the current stream can still hold it or get it
+    too early; the current stream is recorded as a user of it as well."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    device = torch.device(device)
+    current = torch.cuda.current_stream(device)
+    handle = _stream_handle(stream, device)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(handle, device=current.device) if handle
+                  else torch.cuda.default_stream(current.device))
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=current.device)
+    t.record_stream(current)
+    return t
+
+
 _raw_stream_fn = None
 
 

@@ -130,24 +130,6 @@ struct Args {
     bool truth(int i, bool absent) const { return v[i] ? PyObject_IsTrue(v[i]) == 1 : absent; }
 };
 
-// The stream's handle: a torch stream, an integer handle, or the device's
-// current stream.
-void *stream_of(PyObject *stream, int dev)
-{
-    if (!stream)
-        return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-    PyObject *handle = PyObject_GetAttrString(stream, "cuda_stream");
-    if (!handle) {
-        PyErr_Clear();
-        handle = Py_NewRef(stream);
-    }
-    void *p = PyLong_AsVoidPtr(handle);
-    Py_DECREF(handle);
-    if (PyErr_Occurred())
-        throw Raised{};
-    return p;
-}
-
 // ---- tensors ------------------------------------------------------------
 
 int cuda_device(const Tensor &t) { return t.is_cuda() ? (int)t.get_device() : -1; }
@@ -174,6 +156,57 @@ public:
     }
     OnDevice(const OnDevice &) = delete;
     OnDevice &operator=(const OnDevice &) = delete;
+};
+
+// The stream's handle: a torch stream, or an integer handle.
+cudaStream_t handle_of(PyObject *stream)
+{
+    PyObject *handle = PyObject_GetAttrString(stream, "cuda_stream");
+    if (!handle) {
+        PyErr_Clear();
+        handle = Py_NewRef(stream);
+    }
+    void *p = PyLong_AsVoidPtr(handle);
+    Py_DECREF(handle);
+    if (PyErr_Occurred())
+        throw Raised{};
+    return static_cast<cudaStream_t>(p);
+}
+
+// Where a call runs: its tensors' device, and the given stream or the device's
+// current one.  What the call makes for itself on another stream than the
+// current one is that stream's, so that its memory comes from and returns to
+// work in that stream's order; results are known to the current stream too,
+// where the caller's next use of them is, and outlive it.
+class Place {
+    const OnDevice on_;
+    const c10::cuda::CUDAStream current_;
+    const cudaStream_t stream_;
+    const bool foreign_;
+
+public:
+    Place(PyObject *stream, int dev)
+        : on_(dev), current_(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev)),
+          stream_(stream ? handle_of(stream) : current_.stream()),
+          foreign_(stream && stream_ != current_.stream())
+    {
+    }
+    void *stream() const { return stream_; }
+    Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor &like) const
+    {
+        const auto options = at::TensorOptions().dtype(type).device(like.device());
+        if (!foreign_)
+            return at::empty(shape, options);
+        struct Back {
+            const c10::cuda::CUDAStream &to;
+            ~Back() { c10::cuda::setCurrentCUDAStream(to); }
+        } back{current_};
+        c10::cuda::setCurrentCUDAStream(
+            c10::cuda::getStreamFromExternal(stream_, current_.device_index()));
+        Tensor t = at::empty(shape, options);
+        t.record_stream(current_.unwrap());
+        return t;
+    }
 };
 
 std::string shape_text(at::IntArrayRef shape)
@@ -205,11 +238,6 @@ Rows rows_of(const Tensor &t, at::IntArrayRef shape, bool type_ok, int dev, cons
         throw Refused{std::string(name) + " has another type or shape than x's " +
                       shape_text(shape) + ", rows that are not contiguous, or another device"};
     return {t.data_ptr(), t.stride(0)};
-}
-
-Tensor make(at::IntArrayRef shape, at::ScalarType type, const Tensor &like)
-{
-    return at::empty(shape, like.options().dtype(type));
 }
 
 PyObject *wrap(const Tensor *given, PyObject *object, const Tensor &made)
@@ -312,7 +340,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         const Tensor &x = a.required(0, "x"), &weight = a.required(1, "weight");
         const int dev = cuda_device(x);
         need(dev >= 0 && x.dim() == 2 && weight.dim() == 1, "x must be a CUDA [rows][K] tensor, weight [K]");
-        const OnDevice on(dev);
+        const Place on(a.v[10], dev);
         const int64_t shape[2] = {x.size(0), x.size(1)};
         const int64_t K = shape[1];
         dvl_norm p = {};
@@ -337,7 +365,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
             p.residual_stride = r.stride;
             p.residual_dtype = type == kF32 ? DVL_F32 : DVL_BF16;
             if (!residual_out)
-                new_residual = make(shape, type, x);
+                new_residual = on.make(shape, type, x);
             const Tensor &to = residual_out ? *residual_out : new_residual;
             r = rows_of(to, shape, to.scalar_type() == type, dev, "residual_out");
             p.residual_out = r.p;
@@ -348,7 +376,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         const bool bf16 = a.truth(4, true);
         if (bf16) {
             if (!out)
-                new_out = make(shape, kBf16, x);
+                new_out = on.make(shape, kBf16, x);
             const Tensor &to = out ? *out : new_out;
             r = rows_of(to, shape, to.scalar_type() == kBf16, dev, "out");
             p.out = r.p;
@@ -364,9 +392,9 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
             p.group = (int32_t)group;
             const int64_t groups[2] = {shape[0], group ? (K + group - 1) / group : 1};
             if (!codes)
-                new_codes = make(shape, at::kFloat8_e4m3fn, x);
+                new_codes = on.make(shape, at::kFloat8_e4m3fn, x);
             if (!scales)
-                new_scales = make(groups, kF32, x);
+                new_scales = on.make(groups, kF32, x);
             const Tensor &to = codes ? *codes : new_codes;
             r = rows_of(to, shape,
                         to.scalar_type() == at::kFloat8_e4m3fn || to.scalar_type() == at::kByte, dev,
@@ -380,7 +408,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         }
         need(bf16 || fp8, "no output asked for");
         if (shape[0] > 0)
-            check("dvl_add_rmsnorm", dvl_add_rmsnorm(&p, stream_of(a.v[10], dev)));
+            check("dvl_add_rmsnorm", dvl_add_rmsnorm(&p, on.stream()));
         PyObject *t = PyTuple_New(4);
         PyTuple_SET_ITEM(t, 0, bf16 ? wrap(out, a.v[6], new_out) : Py_NewRef(Py_None));
         PyTuple_SET_ITEM(t, 1, residual ? wrap(residual_out, a.v[7], new_residual) : Py_NewRef(Py_None));
@@ -404,7 +432,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
         need(a.v[0] != nullptr, "cache must be a KVCache");
         int dev = -1;
         const dvl_kv_cache *cache = cache_of(a.v[0], &dev);
-        const OnDevice on(dev);
+        const Place on(a.v[9], dev);
         const Tensor &q = a.required(1, "q"), &table = a.required(2, "table"),
                      &lengths = a.required(3, "lengths");
         const int64_t dim = q.dim();
@@ -424,9 +452,9 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
         const at::IntArrayRef rows = shape.slice(0, dim - 1);
         Tensor new_out, new_lse;
         if (!out)
-            new_out = make(shape, kBf16, q);
+            new_out = on.make(shape, kBf16, q);
         if (!lse && want_lse)
-            new_lse = make(rows, kF32, q);
+            new_lse = on.make(rows, kF32, q);
         void *po = flat(out ? *out : new_out, shape, kBf16, dev, "out");
         float *pe = want_lse ? static_cast<float *>(flat(lse ? *lse : new_lse, rows, kF32, dev, "lse"))
                              : nullptr;
@@ -448,7 +476,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *args, Py_ssize_t n, PyObj
                                       Hq > 1 ? q.stride(dim - 2) : 0, (int32_t)B, (int32_t)T,
                                       (int32_t)Hq, static_cast<const int32_t *>(table.data_ptr()),
                                       B > 1 ? table.stride(0) : 0, (int32_t)table.size(1), pl, scale,
-                                      po, pe, ws.p, ws.bytes, stream_of(a.v[9], dev)));
+                                      po, pe, ws.p, ws.bytes, on.stream()));
         PyObject *t = PyTuple_New(2);
         PyTuple_SET_ITEM(t, 0, wrap(out, a.v[5], new_out));
         PyTuple_SET_ITEM(t, 1, want_lse ? wrap(lse, a.v[6], new_lse) : Py_NewRef(Py_None));
@@ -470,7 +498,7 @@ PyObject *beam_select(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         const int dev = cuda_device(logits);
         need(dev >= 0 && logits.dim() == 3 && (logits.stride(2) == 1 || logits.size(2) == 1),
              "logits must be a CUDA [batch][beams][N] tensor with contiguous rows");
-        const OnDevice on(dev);
+        const Place on(a.v[8], dev);
         const auto type = logits.scalar_type();
         need(type == kF32 || type == kBf16, "logits must be bf16 or fp32");
         const int64_t batch = logits.size(0), beams = logits.size(1), N = logits.size(2);
@@ -491,7 +519,7 @@ PyObject *beam_select(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
         for (int i = 0; i < 3; ++i) {
             const auto t = i == 0 ? kF32 : kI32;
             if (!given[i])
-                made[i] = make(got, t, logits);
+                made[i] = on.make(got, t, logits);
             p[i] = flat(given[i] ? *given[i] : made[i], got, t, dev, names[i]);
         }
         Workspace ws;
@@ -509,7 +537,7 @@ PyObject *beam_select(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject 
                   dvl_beam_select(logits.data_ptr(), type == kF32 ? DVL_F32 : DVL_BF16, logits.stride(0),
                                   logits.stride(1), p_in, (int32_t)batch, (int32_t)beams, (int32_t)N,
                                   (int32_t)k, pd, static_cast<float *>(p[0]), static_cast<int32_t *>(p[1]),
-                                  static_cast<int32_t *>(p[2]), ws.p, ws.bytes, stream_of(a.v[8], dev)));
+                                  static_cast<int32_t *>(p[2]), ws.p, ws.bytes, on.stream()));
         PyObject *t = PyTuple_New(3);
         for (int i = 0; i < 3; ++i)
             PyTuple_SET_ITEM(t, i, wrap(given[i], a.v[4 + i], made[i]));
@@ -549,7 +577,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
         const Tensor &parents = a.required(0, "parents");
         const int dev = cuda_device(parents);
         need(dev >= 0 && parents.dim() == 2, "parents must be a CUDA int32 [batch][k] tensor");
-        const OnDevice on(dev);
+        const Place on(a.v[9], dev);
         const int64_t batch = parents.size(0), k = parents.size(1);
         const auto *pp =
             static_cast<const int32_t *>(flat(parents, {batch, k}, kI32, dev, "parents"));
@@ -586,7 +614,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
             need(bytes > 0, "a state's rows must not be empty");
             st[i].src = flat(s, in, s.scalar_type(), dev, "a state");
             if (!a.v[2])
-                made[i] = make(to, s.scalar_type(), s);
+                made[i] = on.make(to, s.scalar_type(), s);
             st[i].dst = flat(a.v[2] ? THPVariable_Unpack(outs[i]) : made[i], to, s.scalar_type(), dev,
                              "a state's output");
             st[i].row_bytes = st[i].src_stride = st[i].dst_stride = bytes;
@@ -602,9 +630,9 @@ PyObject *beam_reorder(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
             const int64_t width = table->size(2);
             need(width <= INT32_MAX, "sizes past 2^31");
             if (!table_out)
-                new_table = make({batch, k, width}, kI32, parents);
+                new_table = on.make({batch, k, width}, kI32, parents);
             if (!lengths_out)
-                new_lengths = make({batch, k}, kI32, parents);
+                new_lengths = on.make({batch, k}, kI32, parents);
             auto ints = [&](const Tensor &t, at::IntArrayRef shape, const char *name) {
                 return static_cast<int32_t *>(flat(t, shape, kI32, dev, name));
             };
@@ -618,7 +646,7 @@ PyObject *beam_reorder(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
         if (batch > 0)
             check("dvl_beam_reorder",
                   dvl_beam_reorder(st, count, cache ? &pages : nullptr, cache, pp, (int32_t)batch,
-                                   (int32_t)beams, (int32_t)k, stream_of(a.v[9], dev)));
+                                   (int32_t)beams, (int32_t)k, on.stream()));
         PyObject *list = PyList_New(count);
         for (int i = 0; i < count; ++i)
             PyList_SET_ITEM(list, i, a.v[2] ? Py_NewRef(outs[i]) : THPVariable_Wrap(made[i]));

@@ -13,13 +13,15 @@ reordering of what belongs to a beam (include/dvl.h has the definitions).
 The four operators live in the compiled module _step (csrc/step_binding.cc),
 which checks and marshals their arguments in a few hundred nanoseconds; what
 is made once -- the cache's handle, the workspaces -- is here.  Output tensors
-can be passed in; the ones that are not are allocated."""
+can be passed in; the ones that are not are allocated.  With `stream`, a call
+runs on that stream, after what that stream holds; the caller orders it behind
+whatever else makes its inputs.  What the call allocates is that stream's own."""
 from __future__ import annotations
 
 import ctypes
 import os
 
-from . import _torch, workspace_init
+from . import _empty, _torch, workspace_init
 from ._native import DVL_BF16, DVL_FP8, DvlKVCache, lib
 
 _OPERATORS = ("add_rmsnorm", "paged_attention", "beam_select", "beam_reorder")
@@ -86,7 +88,7 @@ class KVCache:
 def _workspace(n: int, device, stream):
     """n zeroed bytes on the device."""
     torch = _t()
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = _empty(n, torch.uint8, device, stream)
     with torch.cuda.device(ws.device):
         workspace_init(ws, stream)
     return ws
