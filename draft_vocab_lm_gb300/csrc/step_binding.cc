@@ -715,6 +715,8 @@ PyMethodDef methods[] = {
                "[batch][k] (int32): the page tables and lengths move the same way, and the\n"
                "new beam gets its spare page in place of the parent's partly filled last\n"
                "page, with that page's tokens copied (in the cache, in place).\n"
+               "Outputs overlap neither inputs nor each other: nothing but the cache moves\n"
+               "in place.\n"
                "Returns (states, table, lengths) as tensors [batch][k][...]; the last two\n"
                "None without a cache."),
     {nullptr, nullptr, 0, nullptr}};

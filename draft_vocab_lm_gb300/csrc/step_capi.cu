@@ -68,6 +68,33 @@ size_t attention_bytes(int blocks, int rows, int D)
     return kWsSlots + kTicketBytes + (size_t)2 * blocks * part_floats(rows, D) * sizeof(float);
 }
 
+// `rows` rows of `bytes` consecutive bytes each, `stride` apart.
+struct Rows {
+    uintptr_t at;
+    int64_t rows, bytes, stride;
+    uintptr_t end() const { return at + (uintptr_t)(rows - 1) * (uintptr_t)stride + (uintptr_t)bytes; }
+};
+
+// Whether a byte lies in a row of both.  Rows of two tensors may lie between
+// each other's; only where the spans meet is row compared with row.
+bool overlap(const Rows &a, const Rows &b)
+{
+    if (a.rows < 1 || b.rows < 1 || a.end() <= b.at || b.end() <= a.at)
+        return false;
+    const Rows &few = a.rows <= b.rows ? a : b, &many = a.rows <= b.rows ? b : a;
+    for (int64_t i = 0; i < few.rows; ++i) {
+        const uintptr_t x = few.at + (uintptr_t)i * (uintptr_t)few.stride;
+        // the first of the other's rows that ends past x
+        int64_t j = 0;
+        if (x >= many.at + (uintptr_t)many.bytes)
+            j = (int64_t)((x - many.at - (uintptr_t)many.bytes) / (uintptr_t)many.stride) + 1;
+        if (j < many.rows &&
+            many.at + (uintptr_t)j * (uintptr_t)many.stride < x + (uintptr_t)few.bytes)
+            return true;
+    }
+    return false;
+}
+
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)
 {
     return batch >= 0 && beams >= 1 && beams <= DVL_MAX_BEAMS && N >= 1 &&
@@ -278,11 +305,6 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
         if (!s.src || !s.dst || s.row_bytes < 1 || s.row_bytes > 0x7fffffffLL ||
             s.src_stride < s.row_bytes || s.dst_stride < s.row_bytes)
             return DVL_ERR_INVALID_ARG;
-        const uintptr_t src = reinterpret_cast<uintptr_t>(s.src);
-        const uintptr_t dst = reinterpret_cast<uintptr_t>(s.dst);
-        if (src < dst + (uintptr_t)s.dst_stride * batch * k &&
-            dst < src + (uintptr_t)s.src_stride * batch * beams && batch > 0)
-            return DVL_ERR_INVALID_ARG;
         ReorderItem &it = a.item[a.n_items++];
         it.src = static_cast<const unsigned char *>(s.src);
         it.dst = static_cast<unsigned char *>(s.dst);
@@ -322,6 +344,27 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
     a.k = k;
     if (batch == 0 || a.n_items == 0)
         return DVL_OK;
+    // rows are copied in no order: an output meets neither an input nor another
+    // output
+    Rows in[DVL_MAX_STATES + 4], out[DVL_MAX_STATES + 2];
+    int n_in = 0;
+    for (int i = 0; i < a.n_items; ++i) {
+        const ReorderItem &it = a.item[i];
+        in[n_in++] = {reinterpret_cast<uintptr_t>(it.src), (int64_t)batch * beams, it.row_bytes,
+                      it.src_stride};
+        out[i] = {reinterpret_cast<uintptr_t>(it.dst), (int64_t)batch * k, it.row_bytes, it.dst_stride};
+    }
+    in[n_in++] = {reinterpret_cast<uintptr_t>(parents), 1, 4ll * batch * k, 4ll * batch * k};
+    if (pages)
+        in[n_in++] = {reinterpret_cast<uintptr_t>(pages->spare), 1, 4ll * batch * k, 4ll * batch * k};
+    for (int i = 0; i < a.n_items; ++i) {
+        for (int j = 0; j < n_in; ++j)
+            if (overlap(out[i], in[j]))
+                return DVL_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j]))
+                return DVL_ERR_INVALID_ARG;
+    }
     return done(launch_beam_reorder(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -430,7 +430,7 @@ dvl_status dvl_beam_select(const void *logits, int32_t dtype, int64_t batch_stri
                            void *stream);
 
 /* One tensor of per-beam rows: src [batch][beams] rows, dst [batch][k] rows,
- * each row row_bytes consecutive bytes.  src and dst do not overlap. */
+ * each row row_bytes consecutive bytes. */
 typedef struct dvl_state {
     const void *src;
     void *dst;
@@ -466,7 +466,10 @@ typedef struct dvl_beam_pages {
  *   parents: device int32 [batch][k].
  *   batch:   >= 0 (0 enqueues nothing).  beams, k: 1 .. DVL_MAX_BEAMS.
  * A page id outside the pool (a parent's or a spare one) copies nothing.
- * Outputs may not overlap inputs: the rows are copied in no order.
+ * Rows are copied in no order: a row of an output (of a state, table_out,
+ * lengths_out) may share no byte with a row of any input (of any state, table,
+ * lengths, spare, parents) or of another output; it is refused.  Rows of one
+ * tensor may lie between another's.
  * Errors: DVL_ERR_INVALID_ARG, DVL_ERR_CUDA. */
 dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl_beam_pages *pages,
                             const dvl_kv_cache *cache, const int32_t *parents, int32_t batch,
