@@ -390,7 +390,9 @@ __device__ __forceinline__ void pick(const BeamArgs &a, int64_t request, PickSha
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint64_t hi = s.c_hi[i], lo = s.c_lo[i];
         const int row = key_id(lo);
-        const int token = a.d2t ? a.d2t[row] : row;  // in flight while the rank is counted
+        // in flight while the rank is counted; a row past N is a key that another
+        // call left behind (a stale ticket lets the pick start too early)
+        const int token = (unsigned)row >= (unsigned)a.N ? -1 : a.d2t ? a.d2t[row] : row;
         int rank = 0;
 #pragma unroll 4
         for (int j = 0; j < n; ++j)
