@@ -109,8 +109,11 @@ class Beams:
         logits = torch.matmul(h, m.w_trim.t()).view(self.batch, self.beams, -1)
         self.scores, parents, tokens = dvl.beam_select(logits, self.scores, self.beams, d2t=m.d2t,
                                                        ws=self.select_ws)
+        spare = self.take()
         (self.history,), self.table, self.lengths = dvl.beam_reorder(
-            parents, [self.history], cache=self.cache, table=self.table, lengths=self.lengths, spare=self.take())
+            parents, [self.history], cache=self.cache, table=self.table, lengths=self.lengths, spare=spare)
+        # an unused slot's table is all page 0, another beam's: what it appends goes to its own page
+        self.table[:, :, 0] = torch.where(parents < 0, spare, self.table[:, :, 0])
         self.done += 1
         self.history[:, :, self.done] = tokens
         return tokens

@@ -460,7 +460,9 @@ typedef struct dvl_beam_pages {
  * L = the parent's length, s = L / page_size and r = L % page_size, page
  * spare[b][i] receives the first r tokens of the parent's page s (keys and
  * values) and table_out[b][i][s] = spare[b][i] (when s < width).  Full pages
- * stay shared.  One launch.
+ * stay shared.  An unused slot's table of zeros names page 0: a caller that
+ * keeps appending to such a slot puts a page of its own there first.  One
+ * launch.
  *   states:  HOST array of n_states (0 .. DVL_MAX_STATES), device pointers.
  *   pages:   HOST struct, or NULL; cache goes with it.
  *   parents: device int32 [batch][k].
