@@ -510,8 +510,9 @@ __all__ += _step_module.__all__
 
 def __getattr__(name):
     # the drafting step's operators, loaded with their first use
-    value = getattr(_step_module, name) if name in _step_module._OPERATORS else None
-    if value is None:
+    if name not in _step_module._OPERATORS:
         raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-    globals()[name] = value
+    value = getattr(_step_module, name)
+    if name in vars(_step_module):
+        globals()[name] = value
     return value

@@ -28,11 +28,9 @@ _OPERATORS = ("add_rmsnorm", "paged_attention", "beam_select", "beam_reorder")
 __all__ = [*_OPERATORS, "KVCache", "attention_workspace", "beam_workspace"]
 
 
-def __getattr__(name):
+def _load(name):
     # The compiled module needs PyTorch; it is loaded with the first use of an
     # operator.  There is no fallback: a missing module raises.
-    if name not in _OPERATORS:
-        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
     _torch()
     lib()
     path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_step.so")
@@ -43,6 +41,20 @@ def __getattr__(name):
     for op in _OPERATORS:
         globals()[op] = getattr(_step, op)
     return globals()[name]
+
+
+def __getattr__(name):
+    if name not in _OPERATORS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    try:
+        return _load(name)
+    except (ImportError, OSError, RuntimeError):
+        # Naming an operator, as `from .. import *` does, is no use of it: what
+        # is missing raises when it is called.
+        def later(*args, **kw):
+            return _load(name)(*args, **kw)
+        later.__name__ = later.__qualname__ = name
+        return later
 
 
 def _t():
