@@ -127,7 +127,13 @@ struct Args {
         return x;
     }
     // An absent truth value keeps its default; None counts as absent.
-    bool truth(int i, bool absent) const { return v[i] ? PyObject_IsTrue(v[i]) == 1 : absent; }
+    bool truth(int i, bool absent) const
+    {
+        const int x = v[i] ? PyObject_IsTrue(v[i]) : absent;
+        if (x < 0)
+            throw Raised{};
+        return x != 0;
+    }
 };
 
 // ---- tensors ------------------------------------------------------------

@@ -9,8 +9,17 @@ import subprocess
 from conftest import ROOT
 
 
+_loaded = []
+
+
 def load(folder):
-    """(the module of the operators, the module that drives it), built in `folder`."""
+    """(the module of the operators, the module that drives it), built in `folder` by the first call."""
+    if not _loaded:
+        _loaded.append(_load(folder))
+    return _loaded[0]
+
+
+def _load(folder):
     from draft_vocab_lm_gb300 import build
     so = os.path.join(folder, "_step.so")
     objs = []
