@@ -1,8 +1,9 @@
 """Build libdvl.so in place: nvcc for the CUDA sources (sm_103a only), g++
 for the host-only ranks builder, one shared library with the CUDA runtime
 linked statically; and _step.so, the Python module of the drafting step's
-operators (g++ against PyTorch's headers), which calls libdvl.so.  Object
-files go to _build/ next to this file."""
+operators (g++ against PyTorch's headers), which calls libdvl.so and is left
+out where there is no PyTorch with CUDA.  Object files go to _build/ next to
+this file."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -34,11 +35,13 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _torch_dir() -> str:
+def _torch_dir() -> str | None:
+    """Where a PyTorch with CUDA is installed, or None: libdvl.so needs none."""
     spec = importlib.util.find_spec("torch")
     if spec is None or spec.origin is None:
-        raise RuntimeError("PyTorch not found")
-    return os.path.dirname(spec.origin)
+        return None
+    torch = os.path.dirname(spec.origin)
+    return torch if os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")) else None
 
 
 def _step_compile(obj: str):
@@ -68,35 +71,42 @@ def _deps():
     cu, cpp = sources()
     hdr = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     hdr.append(os.path.join(INCLUDE, "dvl.h"))
-    hdr.append(os.path.join(CSRC, "step_binding.cc"))
     return cu + cpp + hdr + [os.path.abspath(__file__)]
 
 
+def _newer(out: str, deps) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
+
+
+def _step_up_to_date() -> bool:
+    return _torch_dir() is None or _newer(
+        STEP, [os.path.join(CSRC, "step_binding.cc"), os.path.join(INCLUDE, "dvl.h"), os.path.abspath(__file__)])
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(STEP):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(STEP))
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps()) and _step_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libdvl.so and _step.so if any source is newer."""
+    """Compile and link libdvl.so and _step.so, each where a source is newer."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
-    nvcc = _nvcc()
-    cu, cpp = sources()
+    with_lib = force or not _newer(LIB, _deps())
+    with_step = _torch_dir() is not None and (force or not _step_up_to_date())
     jobs = []
-    for src in cu:
-        obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        jobs.append(([nvcc, *NVCC_FLAGS, "-c", src, "-o", obj], obj, src))
-    for src in cpp:
-        obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-        jobs.append((["g++", *CXX_FLAGS, "-c", src, "-o", obj], obj, src))
-
     step_obj = os.path.join(BUILD, "step_binding.o")
-    # the longest compile first
-    jobs.insert(0, (_step_compile(step_obj), step_obj, "step_binding.cc"))
+    if with_step:  # the longest compile first
+        jobs.append((_step_compile(step_obj), step_obj, "step_binding.cc"))
+    if with_lib:
+        nvcc = _nvcc()
+        cu, cpp = sources()
+        for src in cu:
+            obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+            jobs.append(([nvcc, *NVCC_FLAGS, "-c", src, "-o", obj], obj, src))
+        for src in cpp:
+            obj = os.path.join(BUILD, os.path.basename(src) + ".o")
+            jobs.append((["g++", *CXX_FLAGS, "-c", src, "-o", obj], obj, src))
 
     def run(job):
         cmd, obj, src = job
@@ -107,19 +117,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             f.write(r.stdout + r.stderr)
         return obj
 
+    def link(cmd, out):
+        tmp = out + f".tmp{os.getpid()}"
+        r = subprocess.run(cmd(tmp), capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed: {os.path.basename(out)}\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, out)
+
     with cf.ThreadPoolExecutor(max(1, min(len(jobs), os.cpu_count() or 1))) as ex:
-        objs = list(ex.map(run, jobs))[1:]
-    tmp = LIB + f".tmp{os.getpid()}"
-    r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True,
-                       text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
-    tmp = STEP + f".tmp{os.getpid()}"
-    r = subprocess.run(_step_link(step_obj, tmp), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed: _step.so\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, STEP)
+        objs = [o for o in ex.map(run, jobs) if o != step_obj]
+    if with_lib:
+        link(lambda tmp: [nvcc, *ARCH, "-shared", "-o", tmp, *objs], LIB)
+    if with_step:
+        link(lambda tmp: _step_link(step_obj, tmp), STEP)
     if verbose:
         for o in objs:
             if os.path.exists(o + ".log"):
