@@ -21,6 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdvl.so")
 STEP = os.path.join(HERE, "_step.so")
+STEP_FOR = os.path.join(BUILD, "step_binding.for")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -78,8 +79,19 @@ def _newer(out: str, deps) -> bool:
     return os.path.exists(out) and all(os.path.getmtime(p) <= os.path.getmtime(out) for p in deps)
 
 
+def _step_made_for() -> str:
+    """The Python and the PyTorch that _step.so is compiled for: neither runs another's."""
+    torch = _torch_dir()
+    with open(os.path.join(torch, "version.py")) as f:
+        return f"{sysconfig.get_config_var('SOABI')}\n{torch}\n{f.read()}"
+
+
 def _step_up_to_date() -> bool:
-    return _torch_dir() is None or _newer(
+    if _torch_dir() is None:
+        return True
+    if not os.path.exists(STEP_FOR) or open(STEP_FOR).read() != _step_made_for():
+        return False
+    return _newer(
         STEP, [os.path.join(CSRC, "step_binding.cc"), os.path.join(INCLUDE, "dvl.h"), os.path.abspath(__file__)])
 
 
@@ -130,6 +142,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         link(lambda tmp: [nvcc, *ARCH, "-shared", "-o", tmp, *objs], LIB)
     if with_step:
         link(lambda tmp: _step_link(step_obj, tmp), STEP)
+        with open(STEP_FOR, "w") as f:
+            f.write(_step_made_for())
     if verbose:
         for o in objs:
             if os.path.exists(o + ".log"):

@@ -84,3 +84,22 @@ def test_the_library_needs_no_pytorch(b, missing):
     else:
         (b.torch / "lib" / "libc10_cuda.so").write_text("")
     assert not b.up_to_date() and again(b) == ["_step.so"]
+
+
+@pytest.mark.parametrize("what", ["version", "place", "python"])
+def test_the_module_is_remade_for_another_pytorch(b, monkeypatch, what):
+    b.build()
+    if what == "version":
+        old = os.path.getmtime(b.torch / "version.py")
+        (b.torch / "version.py").write_text("__version__ = '2'\n")
+        os.utime(b.torch / "version.py", (old, old))  # an older file than what was built
+    elif what == "place":
+        other = b.torch.with_name("elsewhere")
+        b.torch.rename(other)
+        b.torch.mkdir()
+        spec = types.SimpleNamespace(origin=str(other / "__init__.py"))
+        monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: spec)
+    else:
+        monkeypatch.setattr(b.sysconfig, "get_config_var", lambda name: "cpython-999")
+    assert not b.up_to_date() and again(b) == ["_step.so"]
+    assert b.up_to_date() and again(b) == []
