@@ -219,7 +219,7 @@ def make_workspace(M: int = DVL_MAX_M, k: int = DVL_MAX_TOPK, device=None, strea
     n = workspace_bytes(M, k)
     if n == 0:
         raise ValueError("M or k outside the library's limits")
-    ws = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+    ws = _empty(n, torch.uint8, device or "cuda", stream)
     workspace_init(ws, stream)
     return ws
 
@@ -236,9 +236,9 @@ def draft_topk(head: Head, h, k: int, *, ids=None, logits=None, ws=None, stream=
     _check_h(head, h)
     M = h.shape[0]
     if ids is None:
-        ids = _torch().empty((M, k), dtype=_torch().int32, device=h.device)
+        ids = _empty((M, k), _torch().int32, h.device, stream)
     if logits is None:
-        logits = _torch().empty((M, k), dtype=_torch().float32, device=h.device)
+        logits = _empty((M, k), _torch().float32, h.device, stream)
     if ws is None:
         ws = make_workspace(M, k, device=h.device, stream=stream)
     check("dvl_draft_topk",
@@ -255,9 +255,9 @@ def draft_argmax(head: Head, h, *, ids=None, logits=None, ws=None, stream=None):
     _check_h(head, h)
     M = h.shape[0]
     if ids is None:
-        ids = _torch().empty(M, dtype=_torch().int32, device=h.device)
+        ids = _empty(M, _torch().int32, h.device, stream)
     if logits is None:
-        logits = _torch().empty(M, dtype=_torch().float32, device=h.device)
+        logits = _empty(M, _torch().float32, h.device, stream)
     if ws is None:
         ws = make_workspace(M, 1, device=h.device, stream=stream)
     check("dvl_draft_argmax",
@@ -292,7 +292,7 @@ def score_ids(head: Head, h, ids, *, logits=None, stream=None):
         raise ValueError("ids must be a contiguous CUDA int32 [M][c] tensor")
     c = ids.shape[1]
     if logits is None:
-        logits = torch.empty((M, c), dtype=torch.float32, device=h.device)
+        logits = _empty((M, c), torch.float32, h.device, stream)
     check("dvl_score_ids",
           lib().dvl_score_ids(ctypes.byref(head.struct()), h.data_ptr(), M, ids.data_ptr(), c,
                               logits.data_ptr(), _stream_handle(stream, h.device)))
@@ -310,11 +310,11 @@ def trim_head(w_full, ranks, *, scales=None, fmt=None, stream=None):
     r = np.ascontiguousarray(np.asarray(ranks, dtype=np.int32))
     n = r.shape[0]
     full = Head(w_full, scales=scales, fmt=fmt)
-    w_trim = torch.empty((n, w_full.shape[1]), dtype=w_full.dtype, device=w_full.device)
+    w_trim = _empty((n, w_full.shape[1]), w_full.dtype, w_full.device, stream)
     s_trim = None
     if scales is not None:
-        s_trim = torch.empty((n, scales.shape[1]), dtype=scales.dtype, device=scales.device)
-    d2t = torch.empty(n, dtype=torch.int32, device=w_full.device)
+        s_trim = _empty((n, scales.shape[1]), scales.dtype, scales.device, stream)
+    d2t = _empty(n, torch.int32, w_full.device, stream)
     dup = ctypes.c_int32(0)
     st = full.struct()
     check("dvl_trim_head",
@@ -334,10 +334,10 @@ def quantize_head(w, fmt: str = "nvfp4", *, ws=None, stream=None):
     src = Head(w)
     N, K = src.N, src.K
     if fmt == "nvfp4":
-        dtype, codes = DVL_NVFP4, torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
-        scales = torch.empty((N, K // 16), dtype=torch.uint8, device=w.device)
+        dtype, codes = DVL_NVFP4, _empty((N, K // 2), torch.uint8, w.device, stream)
+        scales = _empty((N, K // 16), torch.uint8, w.device, stream)
     elif fmt == "fp8":
-        dtype, codes, scales = DVL_FP8, torch.empty((N, K), dtype=torch.uint8, device=w.device), None
+        dtype, codes, scales = DVL_FP8, _empty((N, K), torch.uint8, w.device, stream), None
     else:
         raise ValueError("fmt must be nvfp4 or fp8")
     if ws is None:
@@ -393,12 +393,11 @@ class Shortlist:
         self.fmt = fmt or ("nvfp4" if scales is not None else "bf16")
         self.global_scale = float(global_scale)
         self.stream = stream
-        self.w = torch.empty((capacity, w_full.shape[1]), dtype=w_full.dtype, device=w_full.device)
+        self.w = _empty((capacity, w_full.shape[1]), w_full.dtype, w_full.device, stream)
         self.scales = None
         if scales is not None:
-            self.scales = torch.empty((capacity, scales.shape[1]), dtype=scales.dtype,
-                                      device=scales.device)
-        self.d2t = torch.empty(capacity, dtype=torch.int32, device=w_full.device)
+            self.scales = _empty((capacity, scales.shape[1]), scales.dtype, scales.device, stream)
+        self.d2t = _empty(capacity, torch.int32, w_full.device, stream)
         # full id -> trimmed row (-1: not in the list), the table the C call keeps
         self.row_of = np.full(self.V, -1, dtype=np.int32)
         learn_rows(self.w_full, r, self.w, self.d2t, 0, scales=self.scales_full,
