@@ -10,7 +10,8 @@
 // tensor), keeps u in registers between the sum and the output, and reads
 // every input once.  Many small teams hide each other's latencies; a loop over
 // rows with the next row's inputs in flight cost the registers of the teams it
-// replaced (20,011 rows of 2,560, fp32 residual: 86.5 to 92 us against 87).
+// replaced (20,011 rows of 2,560, fp32 residual: 86.5 to 92 us against 87 then;
+// 80 now).
 //   - The sum of squares: per thread, butterfly per warp, then every warp
 //     adds the warps' partial sums itself (one block barrier).  fp32
 //     throughout.
@@ -22,7 +23,9 @@
 //   - Divisions are few, for the issue slots bound what HBM does not (67 % of
 //     them in use, at 0.64 of the copy rate, with IEEE divisions): the
 //     reciprocal root is the hardware's approximation (2^-22 relative), 448 / a
-//     one rounded reciprocal per thread and group.
+//     is 448 times one rounded reciprocal per thread and group, so it is rounded
+//     twice (up to 2^-23 relative): a value within that of the middle between
+//     two codes can take either.
 //   - The codes are cut from the fp32 y, not from its bf16 rounding.
 // Rows that 16-byte accesses do not fit (K % 8 != 0, an odd stride, a pointer
 // off a 16-byte boundary) run the same kernel with element accesses, a lane

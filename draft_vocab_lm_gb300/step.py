@@ -15,7 +15,9 @@ which checks and marshals their arguments in a few hundred nanoseconds; what
 is made once -- the cache's handle, the workspaces -- is here.  Output tensors
 can be passed in; the ones that are not are allocated.  With `stream`, a call
 runs on that stream, after what that stream holds; the caller orders it behind
-whatever else makes its inputs.  What the call allocates is that stream's own."""
+whatever else makes its inputs.  What the call allocates is that stream's own.
+None of the four has a backward pass: their results are detached, also from
+inputs that require gradients."""
 from __future__ import annotations
 
 import ctypes

@@ -320,9 +320,13 @@ typedef struct dvl_norm {
  *   out = y rounded to bf16;
  *   per group of a row: a = max |y|, scale = a / 448,
  *   code = RNE_e4m3(y * (448 / a)), saturating at 448,
- * so y ~ code * scale.  A group with a < 2^-119 has scale a / 448 and codes 0
- * (1 / scale is no fp32 number there).  A NaN or an infinity in a row shows:
- * the values it reaches are NaN, in scale and codes too.
+ * so y ~ code * scale.  All in fp32: the mean square, its reciprocal root and
+ * 448 / a are off by a few 2^-24, so a value as near as that to the middle
+ * between two codes can take either.  Squares above fp32's range make y 0; where
+ * all lie below it and eps is 0, y is infinite or NaN.  A group with a < 2^-119
+ * has scale a / 448 and codes 0 (1 / scale is no fp32 number there).  A NaN or
+ * an infinity in a row shows: the values it reaches are NaN, in scale and codes
+ * too.
  * Any K and any strides run; rows whose tensors all start on 16-byte
  * boundaries with K % 8 == 0 use 16-byte accesses.  No workspace.
  * Errors: DVL_ERR_INVALID_ARG (NULL x or weight; neither out nor codes; codes
