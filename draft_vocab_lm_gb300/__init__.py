@@ -502,7 +502,7 @@ def write_ranks_txt(path: str, ids) -> None:
 
 
 from . import step as _step_module  # noqa: E402  (uses this module's workspace helpers)
-from .step import KVCache, attention_workspace, beam_workspace  # noqa: E402
+from .step import KVCache, Rope, attention_workspace, beam_workspace  # noqa: E402
 
 __all__ += _step_module.__all__
 

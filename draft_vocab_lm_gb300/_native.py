@@ -41,6 +41,7 @@ EXPORTS = (
     "dvl_score_ids",
     "dvl_add_rmsnorm", "dvl_attention_workspace_bytes", "dvl_paged_attention",
     "dvl_beam_workspace_bytes", "dvl_beam_select", "dvl_beam_reorder",
+    "dvl_qk_norm_rope", "dvl_cache_keep",
     "dvl_trim_head", "dvl_learn_rows", "dvl_learn_missing", "dvl_quantize_head",
     "dvl_histogram",
     "dvl_build_ranks", "dvl_union_sorted",
@@ -103,6 +104,46 @@ class DvlKVCache(ctypes.Structure):
         ("v_head_stride", ctypes.c_int64),
         ("k_scale", ctypes.c_float),
         ("v_scale", ctypes.c_float),
+        ("k_blocks", ctypes.c_void_p),
+        ("v_blocks", ctypes.c_void_p),
+    ]
+
+
+class DvlQk(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("Hq", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("rot", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("k_head_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("v_head_stride", ctypes.c_int64),
+        ("q_weight", ctypes.c_void_p),
+        ("k_weight", ctypes.c_void_p),
+        ("freq", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_out_stride", ctypes.c_int64),
+        ("q_out_head_stride", ctypes.c_int64),
+        ("k_out", ctypes.c_void_p),
+        ("k_out_stride", ctypes.c_int64),
+        ("k_out_head_stride", ctypes.c_int64),
+        ("cache", ctypes.POINTER(DvlKVCache)),
+        ("table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64),
+        ("table_width", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("lengths", ctypes.c_void_p),
+        ("starts", ctypes.c_void_p),
     ]
 
 
@@ -180,6 +221,8 @@ def lib():
         L.dvl_beam_select.argtypes = [p, i32, i64, i64, p, i32, i32, i32, i32, p, p, p, p, p, sz, p]
         L.dvl_beam_reorder.argtypes = [ctypes.POINTER(DvlState), i32, ctypes.POINTER(DvlBeamPages), cp,
                                        p, i32, i32, i32, p]
+        L.dvl_qk_norm_rope.argtypes = [ctypes.POINTER(DvlQk), p]
+        L.dvl_cache_keep.argtypes = [cp, p, i64, i32, p, p, p, i64, p, i32, i32, p, p]
         L.dvl_trim_head.argtypes = [hp, p, i32, p, p, p, p, p]
         L.dvl_learn_rows.argtypes = [hp, p, i32, i32, p, p, p, p]
         L.dvl_learn_missing.argtypes = [hp, p, i32, p, p, i32, p, p, p, p, p, p]
@@ -191,6 +234,7 @@ def lib():
                    "dvl_draft_argmax_noalloc", "dvl_noalloc_status",
                    "dvl_draft_plan", "dvl_score_ids",
                    "dvl_add_rmsnorm", "dvl_paged_attention", "dvl_beam_select", "dvl_beam_reorder",
+                   "dvl_qk_norm_rope", "dvl_cache_keep",
                    "dvl_trim_head", "dvl_learn_rows", "dvl_learn_missing", "dvl_quantize_head", "dvl_histogram", "dvl_build_ranks", "dvl_union_sorted"):
             getattr(L, fn).restype = ctypes.c_int
         _lib = L

@@ -6,9 +6,11 @@
 namespace dvl {
 namespace attn {
 
-cudaError_t grid_blocks(bool fp8, int D, int rows, AttnConfig *cfg, int *blocks)
+cudaError_t grid_blocks(int dtype, int D, int rows, AttnConfig *cfg, int *blocks)
 {
-    cudaError_t e = fp8 ? config_fp8(D, rows, cfg) : config_bf16(D, rows, cfg);
+    cudaError_t e = dtype == DVL_FP8     ? config_fp8(D, rows, cfg)
+                    : dtype == DVL_NVFP4 ? config_fp4(D, rows, cfg)
+                                         : config_bf16(D, rows, cfg);
     DeviceInfo di;
     if (e == cudaSuccess)
         e = device_info(&di);

@@ -83,14 +83,21 @@
 namespace dvl {
 namespace attn {
 
+constexpr int kBf16 = 0, kFp8 = 1, kFp4 = 2;  // what a cache holds (FMT)
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr int kJoin = 16;  // parts per first-level join
-constexpr float kF16Weight = 32768.f;  // a weight of 1 among f16 operands (FP8 caches)
+constexpr float kF16Weight = 32768.f;  // a weight of 1 among f16 operands (FP8 and NVFP4 caches)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(valid ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? 4 : 0)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit()
@@ -141,6 +148,10 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v)
                  "r"(v.w)
                  : "memory");
 }
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint16_t lds16(uint32_t addr)
 {
     uint16_t v;
@@ -148,7 +159,7 @@ __device__ __forceinline__ uint16_t lds16(uint32_t addr)
     return v;
 }
 
-// D += A B, m16n8k16, fp32 accumulators; FP8 caches run it on f16 operands.
+// D += A B, m16n8k16, fp32 accumulators; FP8 and NVFP4 caches run it on f16 operands.
 template <bool F16>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                       uint32_t b1)
@@ -226,6 +237,25 @@ __device__ __forceinline__ void e4m3x4_f16x4(uint32_t x, uint32_t &lo, uint32_t 
         : "r"(x));
 }
 
+// The two values of a byte of E2M1 codes as f16 (exact), of a word's four bytes.
+__device__ __forceinline__ void e2m1x8_f16x8(uint32_t w, uint32_t (&f)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -266,9 +296,8 @@ constexpr int round_columns(int dp, int bytes, int room)
     return dp * bytes <= room ? dp : round_columns(dp / 2, bytes, room);
 }
 
-template <int DP, bool FP8, int RT, int TOK, int P, int G>
+template <int DP, int FMT, int RT, int TOK, int P, int G>
 struct Shape {
-    static constexpr int kElem = FP8 ? 1 : 2;
     static constexpr int kTile = TOK * G;
     static_assert(kTile <= 128, "lengths are limited so that a tile more fits 32 bits");
     static constexpr int kGroup = RT == 0 ? 32 : 32 * RT;  // threads
@@ -276,14 +305,18 @@ struct Shape {
     // Rows that one access phase touches lie on distinct banks.  bf16: the
     // 16-byte units of a row are permuted by its lowest three bits (8 rows of
     // an ldmatrix).  FP8: padded pitches (8-byte loads of 4 rows for K, 4-byte
-    // loads of every other row for V).
-    static constexpr int kKPitch = FP8 ? DP + 32 : DP * 2;
-    static constexpr int kVPitch = FP8 ? DP + 16 : DP * 2;
+    // loads of every other row for V).  NVFP4: rows without padding, in which
+    // the four 32-byte pieces of every 128 bytes change places (fp4_place()).
+    static constexpr int kKPitch = FMT == kFp4 ? DP / 2 : FMT == kFp8 ? DP + 32 : DP * 2;
+    static constexpr int kVPitch = FMT == kFp4 ? DP / 2 : FMT == kFp8 ? DP + 16 : DP * 2;
+    // Behind the rows of an NVFP4 entry: their scales.
+    static constexpr int kBlocks = FMT == kFp4 ? DP / 16 : 0;  // bytes per row
     static constexpr int kQPitch = DP * 2 + 16;
     static constexpr int kRows = RT == 0 ? 8 : 16 * RT;    // query rows kept
     static constexpr int kQRows = RT == 0 ? 16 : 16 * RT;  // rows of the operand
     // One ring entry: a chunk's keys or values; also 32 columns of the rows.
-    static constexpr int kEntry = max_of(TOK * kKPitch, kRows * 4 * 32);
+    static constexpr int kEntry = max_of(TOK * (kKPitch + kBlocks), kRows * 4 * 32);
+    static_assert(FMT != kFp4 || kEntry % 128 == 0, "fp4_place() permutes within 128 bytes");
     static constexpr int kEntries = 2 * P + 1;
     static constexpr int kRing = kEntries * kEntry;        // per group
     // At a pair's end every group lays its output rows, kRound columns at a
@@ -297,18 +330,30 @@ struct Shape {
     static constexpr int kBytes = kAddr + G * (P + 1) * 2 * TOK * 8;
 };
 
-// The output column of accumulator e (of a row) of column tile n.
-template <bool FP8>
+// Where byte x of an NVFP4 entry's rows lies: its 32-byte piece is permuted by
+// the 128-byte line, so that four rows that follow each other, and four that
+// are two apart, lie on distinct banks at any width.
+__device__ __forceinline__ int fp4_place(int x) { return x ^ (((x >> 7) ^ (x >> 9)) & 3) << 5; }
+
+// The place among the joined columns of accumulator e (of a row) of column
+// tile n, and the output column there.  They are the same but for NVFP4, where
+// a lane holds eight columns of a block of 64 and a round joins four of them.
+template <int FMT>
 __device__ __forceinline__ int out_col(int n, int c, int e)
 {
-    return FP8 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
+    return FMT != kBf16 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
+}
+template <int FMT>
+__device__ __forceinline__ int real_col(int v)
+{
+    return FMT == kFp4 ? (v & ~63) + ((v & 28) << 1) + ((v & 32) >> 3) + (v & 3) : v;
 }
 
 // The permutation of a row's columns while the groups' rows are joined.
-template <bool FP8>
+template <int FMT>
 __device__ __forceinline__ int swizzle(int r)
 {
-    return FP8 ? (r & 1) << 2 : (r & 3) << 3;
+    return FMT != kBf16 ? (r & 1) << 2 : (r & 3) << 3;
 }
 
 // Where a token's row starts, found by one thread per token a chunk before the
@@ -356,11 +401,26 @@ struct RowAddress {
 // others become zeros, and so do the padding columns of keys: they meet zeros
 // of Q and must hold no NaN, which whatever the entry held before may be.
 // at: the thread's place among the group's N threads.
-template <int DP, bool FP8, int TOK, int N, bool KEYS>
+// pool, blocks: of an NVFP4 cache, the rows' pool and their scales'.
+template <int DP, int FMT, int TOK, int N, bool KEYS>
 __device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *const *rows, int live,
-                                          int at, uint32_t dst, int pitch)
+                                          int at, uint32_t dst, int pitch, const unsigned char *pool,
+                                          const unsigned char *blocks)
 {
-    constexpr int kCols = DP * (FP8 ? 1 : 2) / 16;  // 16-byte units of a padded row
+    if constexpr (FMT == kFp4) {
+        // a row's scales, 4 bytes at a time; the padding's are zeros, too
+        constexpr int kUnits = DP / 64;
+#pragma unroll
+        for (int u0 = 0; u0 < TOK * kUnits; u0 += N) {
+            const int u = u0 + at, r = u / kUnits, unit = u % kUnits;
+            if (u < TOK * kUnits) {
+                const bool have = r < live && unit * 32 < row_bytes;
+                const unsigned char *from = blocks + ((rows[r] - pool) >> 3) + unit * 4;
+                cp_async4(dst + TOK * pitch + u * 4, have ? from : blocks, have);
+            }
+        }
+    }
+    constexpr int kCols = DP * (FMT == kFp4 ? 1 : FMT == kFp8 ? 2 : 4) / 32;  // 16-byte units of a padded row
     constexpr int kStep = N / kCols;                // rows per pass
     const int col = at % kCols, r0 = at / kCols;
     int from = col * 16;
@@ -374,8 +434,9 @@ __device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *co
 #pragma unroll
     for (int i = 0; i < (kStep < TOK ? TOK / kStep : 1); ++i) {
         const int r = r0 + i * kStep;
-        const int unit = FP8 ? col : col ^ (r & 7);
-        cp_async16(dst + r * pitch + unit * 16, rows[r] + from, r < live);
+        const int unit = FMT == kBf16 ? col ^ (r & 7) : col;
+        const int place = r * pitch + unit * 16;
+        cp_async16(dst + (FMT == kFp4 ? fp4_place(place) : place), rows[r] + from, r < live);
     }
 }
 
@@ -502,14 +563,14 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a)
 }
 
 // Four columns of a finished row: the sums over their weights' sum.
-template <bool FP8>
+template <int FMT>
 __device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, int d,
                                         const float4 &acc, float m, float sum)
 {
     const int t = a.token_of(r);
     const int64_t to = ((int64_t)b * a.T + t) * a.Hq + h * a.G + (r - t * a.G);
     // a row without positions (or of -inf scores only): 0
-    const float inv = sum == 0.f ? 0.f : a.v_scale / (FP8 ? sum * kF16Weight : sum);
+    const float inv = sum == 0.f ? 0.f : a.v_scale / (FMT != kBf16 ? sum * kF16Weight : sum);
     *reinterpret_cast<uint2 *>(a.out + to * a.D + d) =
         make_uint2(pack2<false>(acc.x * inv, acc.y * inv), pack2<false>(acc.z * inv, acc.w * inv));
     if (a.lse && d == 0)
@@ -522,7 +583,7 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, int b, int h, int r, 
 // that part's own.  Every thread takes 4 columns of R rows at a time and runs
 // through the parts with a running maximum, kBatch parts' loads in flight; no
 // shared memory and no barrier.
-template <int DP, bool FP8, int THREADS, int R>
+template <int DP, int FMT, int THREADS, int R>
 __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, int second,
                                            int stride, int stats, bool last, int b, int h)
 {
@@ -588,7 +649,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int n, int first, 
             if (r >= a.rows)
                 continue;
             if (last) {
-                put_row<FP8>(a, b, h, r, d, acc[k], m[k], sum[k]);
+                put_row<FMT>(a, b, h, r, d, acc[k], m[k], sum[k]);
             } else {
                 // (the part's own statistics may still be read by other threads)
                 *reinterpret_cast<float4 *>(to_part + r * a.D + d) = acc[k];
@@ -608,7 +669,7 @@ struct Part {
 
 // Count the part in; the last block of a group of parts joins them, the last
 // of the groups those.  Every thread calls it, after the part's last write.
-template <int DP, bool FP8, int THREADS, int R>
+template <int DP, int FMT, int THREADS, int R>
 __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &share, const Part &p,
                                             int *s_last)
 {
@@ -640,7 +701,7 @@ __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &shar
         if (!*s_last)
             return;
         const bool last_level = level == 1 || groups == 1;
-        join_parts<DP, FP8, THREADS, R>(a, parts, slot_a, slot_b, stride, stats, last_level, p.b, p.h);
+        join_parts<DP, FMT, THREADS, R>(a, parts, slot_a, slot_b, stride, stats, last_level, p.b, p.h);
         if (last_level)
             return;
         parts = groups;
@@ -652,14 +713,15 @@ __device__ __forceinline__ void finish_part(const AttnArgs &a, const Share &shar
     }
 }
 
-template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
-__global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCKS)
+template <int DP, int FMT, int RT, int TOK, int P, int G, int BLOCKS>
+__global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCKS)
     attention_kernel(const __grid_constant__ AttnArgs a)
 {
-    using S = Shape<DP, FP8, RT, TOK, P, G>;
+    using S = Shape<DP, FMT, RT, TOK, P, G>;
     constexpr int kThreads = S::kThreads;
     constexpr int kGroup = S::kGroup;
     constexpr int kWarps = kThreads / 32;
+    constexpr bool F16 = FMT != kBf16;   // the operands' type, else bf16
     constexpr int NJ = RT == 0 ? 1 : 2;  // row halves kept per MMA (rows g, g + 8)
     constexpr int kNT = DP / 8;          // MMA column tiles of the output
     constexpr int kSN = TOK / 8;         // MMA column tiles of the scores
@@ -715,7 +777,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             const int r = (i * kThreads + (int)threadIdx.x) / kUnits;
             const int d = ((int)threadIdx.x % kUnits) * 8;
             unsigned char *dst = smem + S::kQ + r * S::kQPitch;
-            if constexpr (FP8) {
+            if constexpr (F16) {
                 const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
                 uint32_t big = 0u;
 #pragma unroll
@@ -728,12 +790,14 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                 e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
                 const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
                 if (r < S::kQRows) {
-                    // place of value d in the permuted order: block of 32, lane
-                    // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2)
+                    // place of value d in the permuted order.  FP8: block of 32, lane
+                    // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2).  NVFP4:
+                    // block of 64, lane quarter (d / 16 % 4), step (d / 4 % 4), half
+                    const int to = FMT == kFp4 ? (d & ~63) + ((d >> 3) & 1) * 32 + ((d >> 4) & 3) * 2
+                                               : (d & ~31) + ((d >> 3) & 3) * 2;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        *reinterpret_cast<uint32_t *>(
-                            dst + 2 * ((d & ~31) + (e >> 1) * 16 + (e & 1) * 8 + ((d >> 3) & 3) * 2)) =
+                        *reinterpret_cast<uint32_t *>(dst + 2 * (to + (e >> 1) * 16 + (e & 1) * 8)) =
                             pack2<true>(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
                     if (d == 0)
                         row_scale[r] = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
@@ -752,7 +816,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     const unsigned char **addr = reinterpret_cast<const unsigned char **>(smem + S::kAddr) +
                                  group * (P + 1) * 2 * TOK;
     const uint32_t ring = base + group * S::kRing;
-    const int row_bytes = a.D * S::kElem;
+    const int row_bytes = FMT == kFp4 ? a.D / 2 : FMT == kFp8 ? a.D : a.D * 2;
     RowAddress row;
     Cursor<S::kTile> ahead = cur;  // of the row addresses
     Cursor<S::kTile> load = cur;   // of the copies
@@ -775,17 +839,17 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     int load_slot = 0, load_entry = 0;  // of addr, of the ring
     auto load_keys = [&]() {
         if (to_load > 0)
-            load_rows<DP, FP8, TOK, kGroup, true>(row_bytes, addr + load_slot * 2 * TOK,
+            load_rows<DP, FMT, TOK, kGroup, true>(row_bytes, addr + load_slot * 2 * TOK,
                                             load.len - load.t * S::kTile - TOK * group, at,
-                                            ring + load_entry * S::kEntry, S::kKPitch);
+                                            ring + load_entry * S::kEntry, S::kKPitch, a.k, a.kb);
         cp_async_commit();
         load_entry = load_entry + 1 == S::kEntries ? 0 : load_entry + 1;
     };
     auto load_values = [&]() {
         if (to_load > 0)
-            load_rows<DP, FP8, TOK, kGroup, false>(row_bytes, addr + load_slot * 2 * TOK + TOK,
+            load_rows<DP, FMT, TOK, kGroup, false>(row_bytes, addr + load_slot * 2 * TOK + TOK,
                                             load.len - load.t * S::kTile - TOK * group, at,
-                                            ring + load_entry * S::kEntry, S::kVPitch);
+                                            ring + load_entry * S::kEntry, S::kVPitch, a.v, a.vb);
         cp_async_commit();
         load_entry = load_entry + 1 == S::kEntries ? 0 : load_entry + 1;
         load_slot = load_slot + 1 == P + 1 ? 0 : load_slot + 1;
@@ -850,7 +914,33 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     acc[n][e] = 0.f;
             const uint32_t q_row =
                 base + S::kQ + (16 * mt + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
-            if constexpr (FP8) {
+            if constexpr (FMT == kFp4) {
+                // lane (g, c): token g of every eight, group c of every block of
+                // 64 values: 8 bytes of codes and one scale, four steps' operands
+#pragma unroll
+                for (int n = 0; n < kSN; ++n) {
+                    const int tok = 8 * n + g;
+                    uint32_t scales[DP / 64];
+#pragma unroll
+                    for (int blk = 0; blk < DP / 64; ++blk)
+                        scales[blk] = lds32(k_smem + TOK * S::kKPitch + tok * S::kBlocks + 4 * blk);
+#pragma unroll
+                    for (int blk = 0; blk < DP / 64; ++blk) {
+                        const uint2 x = lds64(k_smem + fp4_place(tok * S::kKPitch + 32 * blk) + 8 * c);
+                        const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(scales[blk], 0, c * 0x11));
+                        uint32_t f[2][4];
+                        e2m1x8_f16x8(x.x, f[0]);
+                        e2m1x8_f16x8(x.y, f[1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t qa[4];
+                            ldsm4(qa, q_row + (64 * blk + 16 * j) * 2);
+                            mma16<true>(acc[n], qa, mul_f16x2(f[j / 2][2 * (j & 1)], sc),
+                                        mul_f16x2(f[j / 2][2 * (j & 1) + 1], sc));
+                        }
+                    }
+                }
+            } else if constexpr (FMT == kFp8) {
                 const uint32_t k_row = k_smem + g * S::kKPitch + 8 * c;
 #pragma unroll
                 for (int d = 0; d < DP; d += 32) {
@@ -942,11 +1032,11 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
             }
 #pragma unroll
             for (int k = 0; k < TOK / 16; ++k) {
-                pa[k][0] = pack_weights<FP8>(s[2 * k][0], s[2 * k][1]);
+                pa[k][0] = pack_weights<F16>(s[2 * k][0], s[2 * k][1]);
                 pa[k][1] =
-                    NJ == 2 ? pack_weights<FP8>(s[2 * k][2 * NJ - 2], s[2 * k][2 * NJ - 1]) : 0u;
-                pa[k][2] = pack_weights<FP8>(s[2 * k + 1][0], s[2 * k + 1][1]);
-                pa[k][3] = NJ == 2 ? pack_weights<FP8>(s[2 * k + 1][2 * NJ - 2],
+                    NJ == 2 ? pack_weights<F16>(s[2 * k][2 * NJ - 2], s[2 * k][2 * NJ - 1]) : 0u;
+                pa[k][2] = pack_weights<F16>(s[2 * k + 1][0], s[2 * k + 1][1]);
+                pa[k][3] = NJ == 2 ? pack_weights<F16>(s[2 * k + 1][2 * NJ - 2],
                                                        s[2 * k + 1][2 * NJ - 1])
                                    : 0u;
             }
@@ -980,15 +1070,22 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                         float mine = tok & 8 ? pair[1] : pair[0];
                         if constexpr (kSN == 4)
                             mine = tok & 16 ? (tok & 8 ? pair[3] : pair[2]) : mine;
-                        w[j] = __shfl_sync(kFull, FP8 ? mine * kF16Weight : mine, src);
+                        w[j] = __shfl_sync(kFull, F16 ? mine * kF16Weight : mine, src);
                     }
 #pragma unroll
                     for (int n = 0; n < kNT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int d = out_col<FP8>(n, c, e);
+                            const int d = real_col<FMT>(out_col<FMT>(n, c, e));
                             float v;
-                            if constexpr (FP8)
+                            if constexpr (FMT == kFp4) {
+                                const uint16_t code = lds8(v_smem + fp4_place(tok * S::kVPitch + d / 2)) >>
+                                                      4 * (d & 1);
+                                const uint16_t sc = lds8(v_smem + TOK * S::kVPitch + tok * S::kBlocks + d / 16);
+                                uint32_t f[4];
+                                e2m1x8_f16x8(code & 15u, f);
+                                v = unpack1<true>((uint16_t)mul_f16x2(f[0], e4m3x2_f16x2(sc)));
+                            } else if constexpr (FMT == kFp8)
                                 v = unpack1<true>((uint16_t)e4m3x2_f16x2(
                                     lds8(v_smem + tok * S::kVPitch + d)));
                             else
@@ -1001,13 +1098,47 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                         }
                 }
                 group_sync<kGroup>(group);
-                for (int u = at; u < (to - from) * (S::kVPitch / 16); u += kGroup)
-                    sts128(v_smem + from * S::kVPitch + u * 16, make_uint4(0, 0, 0, 0));
+                if constexpr (FMT == kFp4) {  // a scale of 0 makes its values 0
+                    for (int u = at; u < (to - from) * (S::kBlocks / 4); u += kGroup)
+                        sts32(v_smem + TOK * S::kVPitch + from * S::kBlocks + u * 4, 0u);
+                } else {
+                    for (int u = at; u < (to - from) * (S::kVPitch / 16); u += kGroup)
+                        sts128(v_smem + from * S::kVPitch + u * 16, make_uint4(0, 0, 0, 0));
+                }
                 group_sync<kGroup>(group);
             }
 #pragma unroll
             for (int k = 0; k < TOK / 16; ++k) {
-                if constexpr (FP8) {
+                if constexpr (FMT == kFp4) {
+                    // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
+                    // 8 g .. 8 g + 7 of each block of 64; column tile j of a
+                    // block is columns 8 n + j.  The codes of two tokens are
+                    // paired before they are widened, so that a byte holds both.
+#pragma unroll
+                    for (int blk = 0; blk < DP / 64; ++blk) {
+                        uint32_t x[2][2][4];  // pair of tokens, odd column, half the column
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int tok = 16 * k + 8 * q + 2 * c;
+                            const int from = tok * S::kVPitch + 32 * blk;
+                            const uint32_t w0 = lds32(v_smem + fp4_place(from) + 4 * g);
+                            const uint32_t w1 = lds32(v_smem + fp4_place(from + S::kVPitch) + 4 * g);
+                            const uint32_t sa = v_smem + TOK * S::kVPitch + tok * S::kBlocks + 4 * blk;
+                            const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(
+                                lds32(sa), lds32(sa + S::kBlocks), (g >> 1) * 0x11 + 0x40));
+                            e2m1x8_f16x8((w0 & 0x0f0f0f0fu) | (w1 & 0x0f0f0f0fu) << 4, x[q][0]);
+                            e2m1x8_f16x8((w0 >> 4 & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), x[q][1]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                x[q][0][j] = mul_f16x2(x[q][0][j], sc);
+                                x[q][1][j] = mul_f16x2(x[q][1][j], sc);
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mma_rows<true, NJ>(o[8 * blk + j], pa[k], x[0][j & 1][j / 2], x[1][j & 1][j / 2]);
+                    }
+                } else if constexpr (FMT == kFp8) {
                     // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
                     // 4 g .. 4 g + 3 of each block of 32; column tile j of a
                     // block is columns 4 n + j
@@ -1084,18 +1215,18 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     const int r = 16 * mt + 8 * j + g;
                     float *dst = mine + r * S::kRound;
 #pragma unroll
-                    for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += FP8 ? 4 : 1) {
-                        if constexpr (FP8) {
+                    for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += F16 ? 4 : 1) {
+                        if constexpr (F16) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 *reinterpret_cast<float4 *>(
-                                    dst + ((out_col<true>(n0, c, e) - c0) ^ swizzle<true>(r))) =
+                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT>(r))) =
                                     make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
                                                 o[n0 + 2][2 * j + e] * f[j],
                                                 o[n0 + 3][2 * j + e] * f[j]);
                         } else {
                             *reinterpret_cast<float2 *>(
-                                dst + ((out_col<false>(n0, c, 0) - c0) ^ swizzle<false>(r))) =
+                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT>(r))) =
                                 make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
                         }
                     }
@@ -1103,7 +1234,8 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                 __syncthreads();
                 constexpr int kCols = S::kRound / 4;
                 const int d = 4 * ((int)threadIdx.x % kCols);
-                if (c0 + d < a.D) {
+                const int col = real_col<FMT>(c0 + d);
+                if (col < a.D) {
 #pragma unroll 2
                     for (int r = (int)threadIdx.x / kCols; r < a.rows; r += kThreads / kCols) {
                         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1112,7 +1244,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                         for (int w = 0; w < G; ++w) {
                             const float4 x = *reinterpret_cast<const float4 *>(
                                 free_entry + w * S::kRing +
-                                (r * S::kRound + (d ^ swizzle<FP8>(r))) * 4);
+                                (r * S::kRound + (d ^ swizzle<FMT>(r))) * 4);
                             acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
                             big = fmaxf(big, stat[w * S::kRows + r].x);
                         }
@@ -1122,10 +1254,10 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                             sum = fmaf(stat[w * S::kRows + r].y,
                                        ex2(stat[w * S::kRows + r].x - ref), sum);
                         if (whole) {
-                            put_row<FP8>(a, cur.b, cur.h, r, c0 + d, acc, big, sum);
+                            put_row<FMT>(a, cur.b, cur.h, r, col, acc, big, sum);
                         } else {
-                            *reinterpret_cast<float4 *>(part + r * a.D + c0 + d) = acc;
-                            if (c0 + d == 0)
+                            *reinterpret_cast<float4 *>(part + r * a.D + col) = acc;
+                            if (col == 0)
                                 reinterpret_cast<float2 *>(part + a.rows * a.D)[r] =
                                     make_float2(big, sum);
                         }
@@ -1135,7 +1267,7 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
                     __syncthreads();
             }
             if (!whole)
-                finish_part<DP, FP8, kThreads, BLOCKS >= 3 ? 1 : 2>(
+                finish_part<DP, FMT, kThreads, BLOCKS >= 3 ? 1 : 2>(
                     a, share, {share.u1 - left - cur.t, cur.tiles, cur.b, cur.h}, &s_last);
             if (left == 1)
                 break;
@@ -1154,12 +1286,12 @@ __global__ void __launch_bounds__(Shape<DP, FP8, RT, TOK, P, G>::kThreads, BLOCK
     write_empty<kThreads>(a);
 }
 
-template <int DP, bool FP8, int RT, int TOK, int P, int G, int BLOCKS>
+template <int DP, int FMT, int RT, int TOK, int P, int G, int BLOCKS>
 cudaError_t config(AttnConfig *out)
 {
-    using S = Shape<DP, FP8, RT, TOK, P, G>;
+    using S = Shape<DP, FMT, RT, TOK, P, G>;
     static_assert(BLOCKS * (S::kBytes + 1024 + 256) <= 228 * 1024, "shared memory per SM");
-    out->func = reinterpret_cast<const void *>(attention_kernel<DP, FP8, RT, TOK, P, G, BLOCKS>);
+    out->func = reinterpret_cast<const void *>(attention_kernel<DP, FMT, RT, TOK, P, G, BLOCKS>);
     out->smem = S::kBytes;
     out->threads = S::kThreads;
     out->tile = S::kTile;

@@ -11,6 +11,7 @@ struct AttnArgs {
     const uint16_t *q;        // bf16
     int64_t qb, qt, qh;       // strides in elements: sequence, token, head
     const unsigned char *k, *v;
+    const unsigned char *kb, *vb;  // NVFP4: the scales
     int64_t kp, vp;           // strides in bytes: page
     uint32_t kt, kh, vt, vh;  // token, head (within a page)
     const int32_t *table;
@@ -83,9 +84,10 @@ struct AttnConfig {
 // The kernel for padded head widths of 64, 128 and 256, by cache type.
 cudaError_t config_bf16(int D, int rows, AttnConfig *out);
 cudaError_t config_fp8(int D, int rows, AttnConfig *out);
+cudaError_t config_fp4(int D, int rows, AttnConfig *out);
 
 // The kernel and its grid on the current device.
-cudaError_t grid_blocks(bool fp8, int D, int rows, AttnConfig *cfg, int *blocks);
+cudaError_t grid_blocks(int dtype, int D, int rows, AttnConfig *cfg, int *blocks);
 cudaError_t launch_attention(AttnArgs &a, const AttnConfig &cfg, cudaStream_t s);
 
 }  // namespace attn

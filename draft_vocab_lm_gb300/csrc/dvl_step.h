@@ -1,5 +1,5 @@
-// Host-side declarations of the drafting step's operators (norm, attention,
-// beam selection and reordering), shared by their argument checks and their
+// Host-side declarations of the drafting step's operators (norms, attention,
+// beam selection and reordering, kept tokens), shared by their argument checks and their
 // kernel files.
 #pragma once
 
@@ -49,9 +49,55 @@ struct ReorderArgs {
     // the partly filled pages (pages.table == nullptr: none)
     dvl_beam_pages pages;
     dvl_kv_cache cache;
-    int elem;                           // bytes per cached value
-    int page_pieces;                    // per new beam, keys and values each
+    int elem4;                          // half bytes per cached value
+    int page_pieces, block_pieces;      // per new beam, keys and values each: of the
+                                        // rows, of an NVFP4 cache's scales
 };
 cudaError_t launch_beam_reorder(ReorderArgs &a, cudaStream_t s);
+
+// Norm and rotation of queries and keys, and the cache's new rows: dvl_qk's
+// arguments, checked, strides of tensors in elements, of the cache in bytes.
+struct QkArgs {
+    int64_t rows;
+    int Hq, H, D, rot, interleaved;
+    float eps;
+    const uint16_t *q, *k, *v;
+    int64_t qs, qh, ks, kh, vs, vh;     // row, head
+    const uint16_t *q_weight, *k_weight;
+    const uint64_t *freq;
+    const int32_t *positions;
+    uint16_t *q_out, *k_out;
+    int64_t qos, qoh, kos, koh;
+    // the cache; dtype -1: none
+    int dtype;
+    unsigned char *ck, *cv, *ckb, *cvb; // pools, NVFP4 scales
+    int64_t kp, kt, khead, vp, vt, vhead;
+    int pages, page_size, width, B;
+    const int32_t *table, *lengths, *starts;
+    int64_t table_stride;
+    int per_sequence;                   // rows of each without starts
+    float k_scale, v_scale, k_inv, v_inv;
+    int parts;                          // warps that share a row
+};
+cudaError_t launch_qk_norm_rope(QkArgs &a, cudaStream_t s);
+
+// Kept tokens.  A token of a pool is `cols` columns of 16 bytes (wide) or 4.
+struct KeepPool {
+    unsigned char *base;
+    int64_t page, token, head;          // strides in bytes
+    int units, cols;                    // columns per head, per token
+    int wide;
+    int first_block;
+};
+struct KeepArgs {
+    KeepPool pool[4];                   // keys, values, their NVFP4 scales
+    int n_pools;
+    int pages, page_size, width, B, M;
+    const int32_t *table, *lengths, *first, *keep, *counts;
+    int64_t table_stride, keep_stride;
+    int32_t *lengths_out;
+    int blocks;                         // per sequence
+};
+cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s);
 
 }  // namespace dvl

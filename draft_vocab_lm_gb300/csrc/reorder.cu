@@ -70,47 +70,52 @@ __device__ __forceinline__ void copy_table(const ReorderArgs &a, const ReorderIt
         dst[i] = from < 0 ? 0 : i == slot ? a.pages.spare[r] : src[i];
 }
 
-// Piece `blk` of the pages: keys, then values, of new beam r.
-__device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk)
+// Piece `blk` of the pages of new beam r: keys, then values, of the rows; of an
+// NVFP4 cache then those of the scales, which lie as the rows do, in an eighth
+// of the room, 4 bytes at a time.
+template <typename U>
+__device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int pieces, bool scales)
 {
     const dvl_kv_cache &c = a.cache;
-    const int64_t r = blk / (2 * a.page_pieces);
-    const int piece = (int)(blk - r * (2 * a.page_pieces));
-    const bool values = piece >= a.page_pieces;
+    const int64_t r = blk / (2 * pieces);
+    const int piece = (int)(blk - r * (2 * pieces));
+    const bool values = piece >= pieces;
     const int64_t from = source_row(a, r);
     if (from < 0)
         return;
     const int length = max(a.pages.lengths[from], 0);
     const int slot = length / c.page_size;
-    const int row16 = c.D * a.elem / 16;  // 16-byte units of one head of one token
-    const int total = length % c.page_size * c.heads * row16;
-    const int u0 = (piece - (values ? a.page_pieces : 0)) * (kPiece / 16);
+    const int shift = scales ? 4 : 1;  // half bytes to bytes, of the scales eight times fewer
+    const int units = (c.D * a.elem4 >> shift) / (int)sizeof(U);  // of one head of one token
+    const int total = length % c.page_size * c.heads * units;
+    const int u0 = (piece - (values ? pieces : 0)) * (kThreads * kLoads);
     if (u0 >= total || slot >= a.pages.width)
         return;
     const int src_page = a.pages.table[from * a.pages.width + slot];
     const int dst_page = a.pages.spare[r];
     if ((unsigned)src_page >= (unsigned)c.pages || (unsigned)dst_page >= (unsigned)c.pages)
         return;
-    const int64_t ps = values ? c.v_page_stride : c.k_page_stride;
-    const int64_t ts = values ? c.v_token_stride : c.k_token_stride;
-    const int64_t hs = values ? c.v_head_stride : c.k_head_stride;
-    unsigned char *base = static_cast<unsigned char *>(values ? c.v : c.k);
-    uint4 v[kLoads];
+    const int64_t ps = (values ? c.v_page_stride : c.k_page_stride) * a.elem4 >> shift;
+    const int64_t ts = (values ? c.v_token_stride : c.k_token_stride) * a.elem4 >> shift;
+    const int64_t hs = (values ? c.v_head_stride : c.k_head_stride) * a.elem4 >> shift;
+    unsigned char *base = static_cast<unsigned char *>(
+        scales ? (values ? c.v_blocks : c.k_blocks) : (values ? c.v : c.k));
+    U v[kLoads];
     int64_t at[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
         const int u = u0 + (int)threadIdx.x + j * kThreads;
         if (u < total) {
-            const int th = u / row16, unit = u - th * row16;
+            const int th = u / units, unit = u - th * units;
             const int tok = th / c.heads, head = th - tok * c.heads;
-            at[j] = (tok * ts + head * hs) * a.elem + unit * 16;
-            v[j] = *reinterpret_cast<const uint4 *>(base + src_page * ps * a.elem + at[j]);
+            at[j] = tok * ts + head * hs + unit * (int)sizeof(U);
+            v[j] = *reinterpret_cast<const U *>(base + src_page * ps + at[j]);
         }
     }
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
         if (u0 + (int)threadIdx.x + j * kThreads < total)
-            *reinterpret_cast<uint4 *>(base + dst_page * ps * a.elem + at[j]) = v[j];
+            *reinterpret_cast<U *>(base + dst_page * ps + at[j]) = v[j];
 }
 
 __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderArgs a)
@@ -119,7 +124,11 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_con
     pdl_wait();
     const int64_t blk = blockIdx.x;
     if (blk >= a.copy_blocks) {
-        copy_page(a, blk - a.copy_blocks);
+        const int64_t rows = (int64_t)a.batch * a.k * 2 * a.page_pieces;
+        if (blk - a.copy_blocks < rows)
+            copy_page<uint4>(a, blk - a.copy_blocks, a.page_pieces, false);
+        else
+            copy_page<uint32_t>(a, blk - a.copy_blocks - rows, a.block_pieces, true);
         return;
     }
     int i = a.n_items - 1;
@@ -147,11 +156,13 @@ cudaError_t launch_beam_reorder(ReorderArgs &a, cudaStream_t s)
         blocks += rows * it.pieces;
     }
     a.copy_blocks = blocks;
-    a.page_pieces = 0;
+    a.page_pieces = a.block_pieces = 0;
     if (a.pages.table) {
-        const int64_t bytes = (int64_t)(a.cache.page_size - 1) * a.cache.heads * a.cache.D * a.elem;
+        const int64_t bytes = (int64_t)(a.cache.page_size - 1) * a.cache.heads * a.cache.D * a.elem4 / 2;
         a.page_pieces = (int)((bytes + kPiece - 1) / kPiece);
-        blocks += rows * 2 * a.page_pieces;
+        if (a.cache.dtype == DVL_NVFP4)
+            a.block_pieces = (int)((bytes / 8 + kPiece / 4 - 1) / (kPiece / 4));
+        blocks += rows * 2 * (a.page_pieces + a.block_pieces);
     }
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;

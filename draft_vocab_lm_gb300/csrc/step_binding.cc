@@ -21,6 +21,15 @@
 
 #include "dvl.h"
 
+// Weak: a stand-in for the library that lacks them still links with this
+// module (a call then says so).
+extern "C" {
+__attribute__((weak)) dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
+__attribute__((weak)) dvl_status dvl_cache_keep(const dvl_kv_cache *, const int32_t *, int64_t, int32_t,
+                                                const int32_t *, const int32_t *, const int32_t *, int64_t,
+                                                const int32_t *, int32_t, int32_t, int32_t *, void *);
+}
+
 namespace {
 
 using at::Tensor;
@@ -40,7 +49,7 @@ void need(bool ok, const char *what)
 
 // ---- arguments ----------------------------------------------------------
 
-constexpr int kMost = 12;
+constexpr int kMost = 16;
 
 struct Signature {
     const char *name;
@@ -664,6 +673,223 @@ PyObject *beam_reorder(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject
     });
 }
 
+// ---- qk_norm_rope -------------------------------------------------------
+
+Signature qk_sig = {"qk_norm_rope", 3, 15,
+                    {"q", "k", "v", "rope", "q_weight", "k_weight", "eps", "positions", "cache", "table",
+                     "lengths", "starts", "q_out", "k_out", "stream"},
+                    {}};
+
+// A tensor [rows][heads][D] whose values of a head are contiguous, or the same
+// with the rows as [B][T], which must lie evenly.
+struct HeadRows {
+    const void *p = nullptr;
+    int64_t stride = 0, head_stride = 0;
+};
+HeadRows heads_of(const Tensor &t, at::IntArrayRef shape, int dev, const char *name)
+{
+    const int64_t n = (int64_t)shape.size();
+    bool ok = cuda_device(t) == dev && t.scalar_type() == kBf16 && t.sizes() == shape &&
+              (t.stride(n - 1) == 1 || t.numel() == 0);
+    if (ok && n == 4 && shape[0] > 1 && shape[1] > 1)
+        ok = t.stride(0) == shape[1] * t.stride(1);
+    if (!ok)
+        throw Refused{std::string(name) + " must be a bf16 tensor of shape " + shape_text(shape) +
+                      " on q's device, the values of a head contiguous and the rows evenly spaced"};
+    const int64_t rows = n == 4 ? shape[0] * shape[1] : shape[0];
+    HeadRows r;
+    r.p = t.data_ptr();
+    r.stride = rows > 1 ? (n == 4 && shape[1] == 1 ? t.stride(0) : t.stride(n - 3)) : 0;
+    r.head_stride = shape[n - 2] > 1 ? t.stride(n - 2) : 0;
+    return r;
+}
+
+// What a Rope object holds (step.py).
+struct RopeOf {
+    const Tensor *freq = nullptr;
+    int dim = 0;
+    bool interleaved = false;
+    PyObject *held = nullptr;  // keeps freq alive
+
+    RopeOf(PyObject *rope, int dev)
+    {
+        if (!rope)
+            return;
+        static PyObject *names[3] = {PyUnicode_InternFromString("freq"), PyUnicode_InternFromString("dim"),
+                                     PyUnicode_InternFromString("interleaved")};
+        held = PyObject_GetAttr(rope, names[0]);
+        PyObject *d = held ? PyObject_GetAttr(rope, names[1]) : nullptr;
+        PyObject *i = d ? PyObject_GetAttr(rope, names[2]) : nullptr;
+        const bool ok = i && THPVariable_Check(held);
+        if (ok) {
+            freq = &THPVariable_Unpack(held);
+            dim = (int)PyLong_AsLong(d);
+            interleaved = PyObject_IsTrue(i) == 1;
+        }
+        Py_XDECREF(d);
+        Py_XDECREF(i);
+        if (!ok || PyErr_Occurred()) {
+            PyErr_Clear();
+            Py_XDECREF(held);
+            throw Refused{"rope must be a Rope"};
+        }
+        if (cuda_device(*freq) != dev) {
+            Py_XDECREF(held);
+            throw Refused{"the Rope must be on q's device"};
+        }
+    }
+    ~RopeOf() { Py_XDECREF(held); }
+    RopeOf(const RopeOf &) = delete;
+    RopeOf &operator=(const RopeOf &) = delete;
+};
+
+PyObject *qk_norm_rope(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw)
+{
+    return guarded([&]() -> PyObject * {
+        const Args a(qk_sig, args, n, kw);
+        const Tensor &q = a.required(0, "q"), &k = a.required(1, "k");
+        const int dev = cuda_device(q);
+        const int64_t dim = q.dim();
+        need(dev >= 0 && (dim == 3 || dim == 4) && k.dim() == dim,
+             "q and k must be CUDA [rows][heads][D] or [B][T][heads][D] tensors");
+        const Place on(a.v[14], dev);
+        const at::IntArrayRef shape = q.sizes();
+        const int64_t rows = dim == 4 ? shape[0] * shape[1] : shape[0];
+        need(rows <= INT32_MAX && shape[dim - 1] <= INT32_MAX && shape[dim - 2] <= INT32_MAX &&
+                 k.size(dim - 2) <= INT32_MAX,
+             "sizes past 2^31");
+        std::vector<int64_t> kshape(shape.begin(), shape.end());
+        kshape[dim - 2] = k.size(dim - 2);
+        const int64_t D = shape[dim - 1];
+        dvl_qk p = {};
+        p.rows = rows;
+        p.Hq = (int32_t)shape[dim - 2];
+        p.H = (int32_t)kshape[dim - 2];
+        p.D = (int32_t)D;
+        p.eps = (float)a.number(6, 1e-6);
+        HeadRows r = heads_of(q, shape, dev, "q");
+        p.q = r.p, p.q_stride = r.stride, p.q_head_stride = r.head_stride;
+        r = heads_of(k, kshape, dev, "k");
+        p.k = r.p, p.k_stride = r.stride, p.k_head_stride = r.head_stride;
+        const Tensor *v = a.tensor(2, "v");
+        if (v) {
+            r = heads_of(*v, kshape, dev, "v");
+            p.v = r.p, p.v_stride = r.stride, p.v_head_stride = r.head_stride;
+        }
+        const RopeOf rope(a.v[3], dev);
+        if (rope.freq) {
+            need(rope.dim <= D, "the Rope rotates more values than a head has");
+            p.rot = rope.dim;
+            p.interleaved = rope.interleaved;
+            p.freq = static_cast<const uint64_t *>(flat(*rope.freq, {rope.dim / 2}, at::kLong, dev, "the Rope's freq"));
+        }
+        const Tensor *wq = a.tensor(4, "q_weight"), *wk = a.tensor(5, "k_weight");
+        if (wq)
+            p.q_weight = flat(*wq, {D}, kBf16, dev, "q_weight");
+        if (wk)
+            p.k_weight = flat(*wk, {D}, kBf16, dev, "k_weight");
+        if (const Tensor *positions = a.tensor(7, "positions")) {
+            if (dim == 4 && positions->dim() == 2)
+                p.positions = static_cast<const int32_t *>(flat(*positions, shape.slice(0, 2), kI32, dev, "positions"));
+            else
+                p.positions = static_cast<const int32_t *>(flat(*positions, {rows}, kI32, dev, "positions"));
+        }
+        const Tensor *table = a.tensor(9, "table"), *lengths = a.tensor(10, "lengths"),
+                     *starts = a.tensor(11, "starts");
+        if (a.v[8]) {
+            int cache_dev = -1;
+            p.cache = cache_of(a.v[8], &cache_dev);
+            need(cache_dev == dev, "the cache must be on q's device");
+            need(v && table && lengths, "a cache goes with v, table and lengths");
+            need(cuda_device(*table) == dev && table->scalar_type() == kI32 && table->dim() == 2 &&
+                     (table->stride(1) == 1 || table->size(1) == 1),
+                 "table must be a CUDA int32 [B][width] tensor with contiguous rows");
+            const int64_t B = table->size(0);
+            need(B <= INT32_MAX && table->size(1) <= INT32_MAX, "sizes past 2^31");
+            need(!starts || dim == 3, "starts goes with q as [rows][heads][D]");
+            need(dim == 3 || shape[0] == B, "q's first axis must be table's");
+            need(starts || (B > 0 ? rows % B == 0 : rows == 0), "rows without starts must be as many for each sequence");
+            p.table = static_cast<const int32_t *>(table->data_ptr());
+            p.table_stride = B > 1 ? table->stride(0) : 0;
+            p.table_width = (int32_t)table->size(1);
+            p.B = (int32_t)B;
+            p.lengths = static_cast<const int32_t *>(flat(*lengths, {B}, kI32, dev, "lengths"));
+            if (starts)
+                p.starts = static_cast<const int32_t *>(flat(*starts, {B + 1}, kI32, dev, "starts"));
+        } else {
+            need(!v && !table && !lengths && !starts, "v, table, lengths and starts go with a cache");
+            need(!rope.freq || p.positions, "without a cache a Rope goes with positions");
+        }
+        const Tensor *q_out = a.tensor(12, "q_out"), *k_out = a.tensor(13, "k_out");
+        const bool want_k = k_out || !a.v[8];
+        Tensor new_q, new_k;
+        if (!q_out)
+            new_q = on.make(shape, kBf16, q);
+        r = heads_of(q_out ? *q_out : new_q, shape, dev, "q_out");
+        p.q_out = const_cast<void *>(r.p), p.q_out_stride = r.stride, p.q_out_head_stride = r.head_stride;
+        if (want_k) {
+            if (!k_out)
+                new_k = on.make(kshape, kBf16, q);
+            r = heads_of(k_out ? *k_out : new_k, kshape, dev, "k_out");
+            p.k_out = const_cast<void *>(r.p), p.k_out_stride = r.stride, p.k_out_head_stride = r.head_stride;
+        }
+        if (rows > 0) {
+            need(dvl_qk_norm_rope != nullptr, "this build has no qk_norm_rope");
+            check("dvl_qk_norm_rope", dvl_qk_norm_rope(&p, on.stream()));
+        }
+        PyObject *t = PyTuple_New(2);
+        PyTuple_SET_ITEM(t, 0, wrap(q_out, a.v[12], new_q));
+        PyTuple_SET_ITEM(t, 1, want_k ? wrap(k_out, a.v[13], new_k) : Py_NewRef(Py_None));
+        return t;
+    });
+}
+
+// ---- cache_keep ---------------------------------------------------------
+
+Signature keep_sig = {"cache_keep", 6, 8,
+                      {"cache", "table", "lengths", "first", "keep", "counts", "lengths_out", "stream"},
+                      {}};
+
+PyObject *cache_keep(PyObject *, PyObject *const *args, Py_ssize_t n, PyObject *kw)
+{
+    return guarded([&]() -> PyObject * {
+        const Args a(keep_sig, args, n, kw);
+        need(a.v[0] != nullptr, "cache must be a KVCache");
+        int dev = -1;
+        const dvl_kv_cache *cache = cache_of(a.v[0], &dev);
+        const Place on(a.v[7], dev);
+        const Tensor &table = a.required(1, "table"), &lengths = a.required(2, "lengths"),
+                     &first = a.required(3, "first"), &keep = a.required(4, "keep"),
+                     &counts = a.required(5, "counts");
+        auto rows = [&](const Tensor &t) {
+            return cuda_device(t) == dev && t.scalar_type() == kI32 && t.dim() == 2 &&
+                   (t.stride(1) == 1 || t.size(1) <= 1) && t.size(0) <= INT32_MAX && t.size(1) <= INT32_MAX;
+        };
+        need(rows(table), "table must be a CUDA int32 [B][width] tensor with contiguous rows");
+        need(rows(keep) && keep.size(0) == table.size(0),
+             "keep must be a CUDA int32 [B][M] tensor with contiguous rows");
+        const int64_t B = table.size(0);
+        auto ints = [&](const Tensor &t, const char *name) {
+            return static_cast<int32_t *>(flat(t, {B}, kI32, dev, name));
+        };
+        const int32_t *pl = ints(lengths, "lengths"), *pf = ints(first, "first"), *pc = ints(counts, "counts");
+        const Tensor *out = a.tensor(6, "lengths_out");
+        Tensor made;
+        if (!out)
+            made = on.make({B}, kI32, lengths);
+        int32_t *po = ints(out ? *out : made, "lengths_out");
+        if (B > 0) {
+            need(dvl_cache_keep != nullptr, "this build has no cache_keep");
+            check("dvl_cache_keep",
+                  dvl_cache_keep(cache, static_cast<const int32_t *>(table.data_ptr()),
+                                 B > 1 ? table.stride(0) : 0, (int32_t)table.size(1), pl, pf,
+                                 static_cast<const int32_t *>(keep.data_ptr()), B > 1 ? keep.stride(0) : 0, pc,
+                                 (int32_t)B, (int32_t)keep.size(1), po, on.stream()));
+        }
+        return wrap(out, a.v[6], made);
+    });
+}
+
 // ---- module -------------------------------------------------------------
 
 #define DVL_METHOD(name, doc)                                                           \
@@ -725,6 +951,34 @@ PyMethodDef methods[] = {
                "in place.\n"
                "Returns (states, table, lengths) as tensors [batch][k][...]; the last two\n"
                "None without a cache."),
+    DVL_METHOD(qk_norm_rope,
+               "qk_norm_rope(q, k, v=None, *, rope=None, q_weight=None, k_weight=None, eps=1e-6,\n"
+               "             positions=None, cache=None, table=None, lengths=None, starts=None,\n"
+               "             q_out=None, k_out=None, stream=None)\n--\n\n"
+               "Norm of the new tokens' queries and keys for each head (with a weight),\n"
+               "rotation by their position (with a Rope), and with a cache the new keys and\n"
+               "values to their places there.\n\n"
+               "q, k, v: CUDA bf16 [rows][heads][D] or [B][T][heads][D]; heads and rows may be\n"
+               "         strided (views of one projection's output).\n"
+               "q_weight, k_weight: bf16 [D]; None: no norm.\n"
+               "cache, table [B][width], lengths [B] (int32): as in paged_attention; lengths\n"
+               "         counts the new tokens, whose places are the last ones.\n"
+               "starts:  int32 [B + 1], rising: sequence b's new tokens are rows starts[b] ..\n"
+               "         starts[b + 1] - 1; rows past starts[B] are padding, left as they are.\n"
+               "         None: as many for every sequence.\n"
+               "positions: int32 [rows] to rotate by in place of the tokens' places (a tree's\n"
+               "         depths); needed by a Rope without a cache.\n"
+               "q_out, k_out: may be q and k themselves.\n"
+               "Returns (q_out, k_out), bf16; k_out is None with a cache unless it is given."),
+    DVL_METHOD(cache_keep,
+               "cache_keep(cache, table, lengths, first, keep, counts, *, lengths_out=None,\n"
+               "           stream=None)\n--\n\n"
+               "Keep some of each sequence's newest tokens, without gaps: the token at place\n"
+               "first[b] + keep[b][i] moves to place first[b] + i for i < counts[b], in the\n"
+               "cache, in place.\n\n"
+               "table:   int32 [B][width]; lengths, first, counts: int32 [B].\n"
+               "keep:    int32 [B][M], strictly rising in each row.\n"
+               "Returns the new lengths, first + counts (int32 [B])."),
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_step", "The drafting step's operators.", -1, methods,
@@ -738,5 +992,7 @@ PyMODINIT_FUNC PyInit__step(void)
     intern(attention_sig);
     intern(select_sig);
     intern(reorder_sig);
+    intern(qk_sig);
+    intern(keep_sig);
     return PyModule_Create(&module);
 }

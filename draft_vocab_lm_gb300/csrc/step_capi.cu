@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstring>
 
 #include "dvl_attention.h"
@@ -22,14 +23,18 @@ bool row_ok(const void *p, int64_t stride, int64_t rows, int64_t least, int size
 
 dvl_status check_cache(const dvl_kv_cache *c)
 {
-    if (!c || (c->dtype != DVL_BF16 && c->dtype != DVL_FP8) || c->reserved != 0)
+    if (!c || (c->dtype != DVL_BF16 && c->dtype != DVL_FP8 && c->dtype != DVL_NVFP4) || c->reserved != 0)
         return DVL_ERR_INVALID_ARG;
     if (c->pages < 1 || c->page_size < 1 || c->heads < 1 || c->D < 16 || c->D % 16 != 0 ||
         c->D > DVL_MAX_HEAD_DIM)
         return DVL_ERR_INVALID_ARG;
     if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16))
         return DVL_ERR_INVALID_ARG;
-    const int64_t unit = c->dtype == DVL_BF16 ? 8 : 16;  // elements in 16 bytes
+    if (c->dtype == DVL_NVFP4 && (c->D % 64 != 0 || !c->k_blocks || !c->v_blocks ||
+                                  !aligned(c->k_blocks, 16) || !aligned(c->v_blocks, 16)))
+        return DVL_ERR_INVALID_ARG;
+    // elements in 16 bytes; NVFP4 rows of scales start on their own size
+    const int64_t unit = c->dtype == DVL_BF16 ? 8 : c->dtype == DVL_FP8 ? 16 : c->D;
     const int64_t strides[6] = {c->k_page_stride, c->k_token_stride, c->k_head_stride,
                                 c->v_page_stride, c->v_token_stride, c->v_head_stride};
     for (int64_t s : strides)
@@ -42,6 +47,12 @@ dvl_status check_cache(const dvl_kv_cache *c)
     if (!std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
         return DVL_ERR_INVALID_ARG;
     return DVL_OK;
+}
+
+// Half bytes per cached value.
+int half_bytes(const dvl_kv_cache *c)
+{
+    return c->dtype == DVL_BF16 ? 4 : c->dtype == DVL_FP8 ? 2 : 1;
 }
 
 // Query rows per cached head, or 0 when T and Hq are outside the limits.
@@ -93,6 +104,57 @@ bool overlap(const Rows &a, const Rows &b)
             return true;
     }
     return false;
+}
+
+// A tensor [rows][heads][D] of bf16 as dvl_qk has it, and the bytes of its rows.
+struct HeadRows {
+    const void *p;
+    int64_t stride, head_stride;  // elements
+    int heads;
+};
+bool heads_ok(const HeadRows &t, bool optional)
+{
+    if (!t.p)
+        return optional;
+    return aligned(t.p, 16) && t.stride % 8 == 0 && t.head_stride % 8 == 0 && t.stride >= 0 && t.head_stride >= 0;
+}
+// Whether no value of an output is another's: heads within rows, or rows
+// within heads.
+bool apart(const HeadRows &t, int64_t rows, int D)
+{
+    const int64_t in_row = (t.heads - 1) * t.head_stride + D, in_head = (rows - 1) * t.stride + D;
+    return (t.heads == 1 || t.head_stride >= D) && (rows == 1 || t.stride >= D) &&
+           (rows == 1 || t.heads == 1 || t.stride >= in_row || t.head_stride >= in_head);
+}
+bool same(const HeadRows &x, const HeadRows &y, int64_t rows)
+{
+    return x.p == y.p && (rows == 1 || x.stride == y.stride) &&
+           (x.heads == 1 || x.head_stride == y.head_stride) && x.heads == y.heads;
+}
+// Whether two of these tensors may share a byte: by rows where the heads of a
+// row lie together, else by the span of all.
+bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
+{
+    if (!x.p || !y.p)
+        return false;
+    auto bytes = [&](const HeadRows &t) {
+        const int64_t row = 2 * ((t.heads - 1) * t.head_stride + D);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(t.p);
+        if (rows == 1 || 2 * t.stride >= row)
+            return Rows{at, rows, row, rows == 1 ? row : 2 * t.stride};
+        const int64_t span = row + 2 * (rows - 1) * t.stride;
+        return Rows{at, 1, span, span};
+    };
+    const Rows a = bytes(x), b = bytes(y);
+    if (a.rows == rows && b.rows == rows && a.stride == b.stride) {
+        // the same stride: the rows' places within it tell
+        if (a.end() <= b.at || b.end() <= a.at)
+            return false;
+        const Rows &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
+        const int64_t off = (int64_t)((hi.at - lo.at) % (uintptr_t)a.stride);
+        return off < lo.bytes || off + hi.bytes > a.stride;
+    }
+    return overlap(a, b);
 }
 
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)
@@ -149,7 +211,7 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
     const int rows = query_rows(cache, T, Hq);
     attn::AttnConfig cfg;
     int blocks = 0;
-    if (rows == 0 || attn::grid_blocks(cache->dtype == DVL_FP8, cache->D, rows, &cfg, &blocks) !=
+    if (rows == 0 || attn::grid_blocks(cache->dtype, cache->D, rows, &cfg, &blocks) !=
                          cudaSuccess)
         return 0;
     return attention_bytes(blocks, rows, cache->D);
@@ -176,30 +238,33 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     if (q_batch_stride % 8 != 0 || q_token_stride % 8 != 0 || q_head_stride % 8 != 0 ||
         !std::isfinite(scale))
         return DVL_ERR_INVALID_ARG;
-    const bool fp8 = cache->dtype == DVL_FP8;
     attn::AttnArgs a;
     std::memset(&a, 0, sizeof a);
     attn::AttnConfig cfg;
-    const cudaError_t e = attn::grid_blocks(fp8, cache->D, rows, &cfg, &a.blocks);
+    const cudaError_t e = attn::grid_blocks(cache->dtype, cache->D, rows, &cfg, &a.blocks);
     if (e != cudaSuccess)
         return cuda_failed(e);
     if (!ws || !aligned(ws, 16) || ws_bytes < attention_bytes(a.blocks, rows, cache->D))
         return DVL_ERR_WORKSPACE;
     if (B == 0)
         return DVL_OK;
-    const int64_t size = fp8 ? 1 : 2;
+    const int64_t half = half_bytes(cache);
     a.q = static_cast<const uint16_t *>(q);
     a.qb = q_batch_stride;
     a.qt = q_token_stride;
     a.qh = q_head_stride;
     a.k = static_cast<const unsigned char *>(cache->k);
     a.v = static_cast<const unsigned char *>(cache->v);
-    a.kp = cache->k_page_stride * size;
-    a.kt = (uint32_t)(cache->k_token_stride * size);
-    a.kh = (uint32_t)(cache->k_head_stride * size);
-    a.vp = cache->v_page_stride * size;
-    a.vt = (uint32_t)(cache->v_token_stride * size);
-    a.vh = (uint32_t)(cache->v_head_stride * size);
+    a.kp = cache->k_page_stride * half / 2;
+    a.kt = (uint32_t)(cache->k_token_stride * half / 2);
+    a.kh = (uint32_t)(cache->k_head_stride * half / 2);
+    a.vp = cache->v_page_stride * half / 2;
+    a.vt = (uint32_t)(cache->v_token_stride * half / 2);
+    a.vh = (uint32_t)(cache->v_head_stride * half / 2);
+    if (cache->dtype == DVL_NVFP4) {
+        a.kb = static_cast<const unsigned char *>(cache->k_blocks);
+        a.vb = static_cast<const unsigned char *>(cache->v_blocks);
+    }
     a.table = table;
     a.table_stride = table_stride;
     a.lengths = lengths;
@@ -322,12 +387,13 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
             !aligned(pages->lengths, 4) || !aligned(pages->lengths_out, 4) ||
             !aligned(pages->spare, 4))
             return DVL_ERR_INVALID_ARG;
-        a.elem = cache->dtype == DVL_FP8 ? 1 : 2;
-        if ((int64_t)cache->page_size * cache->heads * cache->D * a.elem > 0x7fffffffLL ||
+        a.elem4 = half_bytes(cache);
+        if ((int64_t)cache->page_size * cache->heads * cache->D * a.elem4 / 2 > 0x7fffffffLL ||
             (int64_t)pages->width * 4 > 0x7fffffffLL)
             return DVL_ERR_INVALID_ARG;
         a.pages = *pages;
-        a.cache = *cache;
+        // (a caller's struct without the scales' pointers ends before them)
+        std::memcpy(&a.cache, cache, cache->dtype == DVL_NVFP4 ? sizeof a.cache : offsetof(dvl_kv_cache, k_blocks));
         const void *src[2] = {pages->table, pages->lengths};
         void *dst[2] = {pages->table_out, pages->lengths_out};
         const int64_t bytes[2] = {4ll * pages->width, 4};
@@ -366,6 +432,161 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
                 return DVL_ERR_INVALID_ARG;
     }
     return done(launch_beam_reorder(a, static_cast<cudaStream_t>(stream)));
+}
+
+dvl_status dvl_qk_norm_rope(const dvl_qk *p, void *stream)
+{
+    if (!p || p->rows < 0 || p->rows > 0x7fffffffLL || p->Hq < 1 || p->H < 1 || p->Hq > 65536 || p->H > 65536 ||
+        p->D < 16 || p->D % 16 != 0 || p->D > DVL_MAX_HEAD_DIM || p->rot < 0 || p->rot % 16 != 0 || p->rot > p->D ||
+        (p->interleaved != 0 && p->interleaved != 1) || !(p->eps >= 0.f) || !std::isfinite(p->eps))
+        return DVL_ERR_INVALID_ARG;
+    const HeadRows q = {p->q, p->q_stride, p->q_head_stride, p->Hq}, k = {p->k, p->k_stride, p->k_head_stride, p->H},
+                   v = {p->v, p->v_stride, p->v_head_stride, p->H},
+                   qo = {p->q_out, p->q_out_stride, p->q_out_head_stride, p->Hq},
+                   ko = {p->k_out, p->k_out_stride, p->k_out_head_stride, p->H};
+    if (!heads_ok(q, false) || !heads_ok(k, false) || !heads_ok(v, !p->cache) || !heads_ok(qo, false) ||
+        !heads_ok(ko, p->cache != nullptr) || (!p->cache && p->v) || !aligned(p->q_weight, 16) ||
+        !aligned(p->k_weight, 16) || !aligned(p->positions, 4) || !aligned(p->freq, 8) || (p->rot > 0 && !p->freq) ||
+        (p->rot > 0 && !p->cache && !p->positions))
+        return DVL_ERR_INVALID_ARG;
+    const int64_t rows = p->rows;
+    if (rows > 0 &&
+        (!apart(qo, rows, p->D) || (ko.p && !apart(ko, rows, p->D)) ||
+         (!same(qo, q, rows) && meet(qo, q, rows, p->D)) || meet(qo, k, rows, p->D) || meet(qo, v, rows, p->D) ||
+         meet(qo, ko, rows, p->D) || meet(ko, q, rows, p->D) ||
+         (ko.p && !same(ko, k, rows) && meet(ko, k, rows, p->D)) || meet(ko, v, rows, p->D)))
+        return DVL_ERR_INVALID_ARG;
+    QkArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.dtype = -1;
+    if (const dvl_kv_cache *c = p->cache) {
+        const dvl_status st = check_cache(c);
+        if (st != DVL_OK)
+            return st;
+        if (c->heads != p->H || c->D != p->D || p->B < 0 || p->table_width < 1 || p->table_stride < 0 ||
+            (int64_t)p->table_width * c->page_size > 0x7fffffffLL || !p->table || !aligned(p->table, 4) ||
+            !p->lengths || !aligned(p->lengths, 4) || !aligned(p->starts, 4) ||
+            (p->B == 0 ? rows > 0 && !p->starts : !p->starts && rows % p->B != 0))
+            return DVL_ERR_INVALID_ARG;
+        // reciprocals of the scales, and products with an E4M3 scale, stay normal numbers
+        for (float s : {c->k_scale, c->v_scale})
+            if (c->dtype != DVL_BF16 && !(s >= 0x1p-100f && s <= 0x1p100f))
+                return DVL_ERR_INVALID_ARG;
+        if (p->B == 0)
+            return DVL_OK;
+        const int64_t half = half_bytes(c);
+        a.dtype = c->dtype;
+        a.ck = static_cast<unsigned char *>(c->k);
+        a.cv = static_cast<unsigned char *>(c->v);
+        if (c->dtype == DVL_NVFP4) {
+            a.ckb = static_cast<unsigned char *>(c->k_blocks);
+            a.cvb = static_cast<unsigned char *>(c->v_blocks);
+        }
+        a.kp = c->k_page_stride * half / 2;
+        a.kt = c->k_token_stride * half / 2;
+        a.khead = c->k_head_stride * half / 2;
+        a.vp = c->v_page_stride * half / 2;
+        a.vt = c->v_token_stride * half / 2;
+        a.vhead = c->v_head_stride * half / 2;
+        a.pages = c->pages;
+        a.page_size = c->page_size;
+        a.width = p->table_width;
+        a.B = p->B;
+        a.table = p->table;
+        a.table_stride = p->table_stride;
+        a.lengths = p->lengths;
+        a.starts = p->starts;
+        a.per_sequence = p->starts ? 0 : (int)(rows / p->B);
+        a.k_scale = c->k_scale;
+        a.v_scale = c->v_scale;
+        a.k_inv = 1.f / c->k_scale;
+        a.v_inv = 1.f / c->v_scale;
+    }
+    if (rows == 0)
+        return DVL_OK;
+    a.rows = rows;
+    a.Hq = p->Hq;
+    a.H = p->H;
+    a.D = p->D;
+    a.rot = p->rot;
+    a.interleaved = p->interleaved;
+    a.eps = p->eps;
+    a.q = static_cast<const uint16_t *>(p->q);
+    a.k = static_cast<const uint16_t *>(p->k);
+    a.v = static_cast<const uint16_t *>(p->v);
+    a.qs = q.stride, a.qh = q.head_stride;
+    a.ks = k.stride, a.kh = k.head_stride;
+    a.vs = v.stride, a.vh = v.head_stride;
+    a.q_weight = static_cast<const uint16_t *>(p->q_weight);
+    a.k_weight = static_cast<const uint16_t *>(p->k_weight);
+    a.freq = p->freq;
+    a.positions = p->positions;
+    a.q_out = static_cast<uint16_t *>(p->q_out);
+    a.k_out = static_cast<uint16_t *>(p->k_out);
+    a.qos = qo.stride, a.qoh = qo.head_stride;
+    a.kos = ko.stride, a.koh = ko.head_stride;
+    return done(launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64_t table_stride,
+                          int32_t table_width, const int32_t *lengths, const int32_t *first,
+                          const int32_t *keep, int64_t keep_stride, const int32_t *counts,
+                          int32_t B, int32_t M, int32_t *lengths_out, void *stream)
+{
+    const dvl_status st = check_cache(cache);
+    if (st != DVL_OK)
+        return st;
+    if (B < 0 || M < 0 || M > 0x7fffffff - 64 || table_width < 1 || table_stride < 0 || (B > 1 && keep_stride < 0) ||
+        (int64_t)table_width * cache->page_size > 0x7fffffffLL || !table || !aligned(table, 4) || !lengths ||
+        !aligned(lengths, 4) || !first || !aligned(first, 4) || (M > 0 && !keep) || !aligned(keep, 4) || !counts ||
+        !aligned(counts, 4) || !aligned(lengths_out, 4))
+        return DVL_ERR_INVALID_ARG;
+    if (B == 0)
+        return DVL_OK;
+    if (lengths_out) {
+        const Rows to = {reinterpret_cast<uintptr_t>(lengths_out), 1, 4ll * B, 4ll * B};
+        auto span = [&](const int32_t *p, int64_t width, int64_t stride) {
+            const int64_t n = 4 * ((B - 1) * stride + width);
+            return Rows{reinterpret_cast<uintptr_t>(p), n > 0, n, n};
+        };
+        if (overlap(to, span(lengths, B, 0)) || overlap(to, span(first, B, 0)) || overlap(to, span(counts, B, 0)) ||
+            (M > 0 && overlap(to, span(keep, M, keep_stride))) || overlap(to, span(table, table_width, table_stride)))
+            return DVL_ERR_INVALID_ARG;
+    }
+    KeepArgs a;
+    std::memset(&a, 0, sizeof a);
+    const int64_t half = half_bytes(cache);
+    const int row = (int)(cache->D * half / 2);  // bytes of a head of a token
+    a.n_pools = cache->dtype == DVL_NVFP4 ? 4 : 2;
+    for (int i = 0; i < a.n_pools; ++i) {
+        KeepPool &p = a.pool[i];
+        const bool values = i & 1, scales = i >= 2;
+        const int64_t down = scales ? 16 : 2;
+        p.base = static_cast<unsigned char *>(scales ? (values ? cache->v_blocks : cache->k_blocks)
+                                                     : (values ? cache->v : cache->k));
+        p.page = (values ? cache->v_page_stride : cache->k_page_stride) * half / down;
+        p.token = (values ? cache->v_token_stride : cache->k_token_stride) * half / down;
+        p.head = (values ? cache->v_head_stride : cache->k_head_stride) * half / down;
+        p.wide = !scales;
+        p.units = scales ? row / 8 / 4 : row / 16;
+        if ((int64_t)p.units * cache->heads > 0x7fffffffLL - 32)
+            return DVL_ERR_INVALID_ARG;
+        p.cols = p.units * cache->heads;
+    }
+    a.pages = cache->pages;
+    a.page_size = cache->page_size;
+    a.width = table_width;
+    a.B = B;
+    a.M = M;
+    a.table = table;
+    a.table_stride = table_stride;
+    a.lengths = lengths;
+    a.first = first;
+    a.keep = keep;
+    a.keep_stride = keep_stride;
+    a.counts = counts;
+    a.lengths_out = lengths_out;
+    return done(launch_cache_keep(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

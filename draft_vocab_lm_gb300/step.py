@@ -1,33 +1,40 @@
-"""The drafting step around the head: attention of the new tokens over a paged
-key-value cache, residual addition with norm, beam selection, and the
-reordering of what belongs to a beam (include/dvl.h has the definitions).
+"""The drafting step around the head: norm and rotation of the new queries and
+keys and their way into a paged key-value cache, attention of the new tokens
+over it, residual addition with norm, beam selection, the reordering of what
+belongs to a beam, and the cached tokens that a verification keeps
+(include/dvl.h has the definitions).
 
     cache = KVCache(k, v)                          # CUDA [pages][page][heads][D]
+    rope = Rope(D, theta=1e6)
+    q, _ = qk_norm_rope(q, k_new, v_new, rope=rope, q_weight=wq, k_weight=wk,
+                        cache=cache, table=table, lengths=lengths)
     ws = attention_workspace(cache, B, T, Hq)
     o, lse = paged_attention(cache, q, table, lengths, ws=ws)
     h, residual, _, _ = add_rmsnorm(x, weight, residual)
     scores, parents, tokens = beam_select(logits, scores, k, d2t=d2t)
     states, table, lengths = beam_reorder(parents, states, cache=cache, table=table,
                                           lengths=lengths, spare=spare)
+    lengths = cache_keep(cache, table, lengths, first, keep, counts)
 
-The four operators live in the compiled module _step (csrc/step_binding.cc),
+The operators live in the compiled module _step (csrc/step_binding.cc),
 which checks and marshals their arguments in a few hundred nanoseconds; what
 is made once -- the cache's handle, the workspaces -- is here.  Output tensors
 can be passed in; the ones that are not are allocated.  With `stream`, a call
 runs on that stream, after what that stream holds; the caller orders it behind
 whatever else makes its inputs.  What the call allocates is that stream's own.
-None of the four has a backward pass: their results are detached, also from
-inputs that require gradients."""
+None has a backward pass: their results are detached, also from inputs that
+require gradients."""
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from . import _empty, _torch, workspace_init
-from ._native import DVL_BF16, DVL_FP8, DvlKVCache, lib
+from ._native import DVL_BF16, DVL_FP8, DVL_NVFP4, DvlKVCache, lib
 
-_OPERATORS = ("add_rmsnorm", "paged_attention", "beam_select", "beam_reorder")
-__all__ = [*_OPERATORS, "KVCache", "attention_workspace", "beam_workspace"]
+_OPERATORS = ("add_rmsnorm", "paged_attention", "beam_select", "beam_reorder", "qk_norm_rope", "cache_keep")
+__all__ = [*_OPERATORS, "KVCache", "Rope", "attention_workspace", "beam_workspace"]
 
 
 def _load(name):
@@ -74,18 +81,28 @@ class KVCache:
     k, v: bf16, or E4M3 (float8_e4m3fn, or uint8 codes), each
           [pages][page_size][heads][D]; the D values of a head are
           contiguous, the other strides are free (so a [pages][heads][page]
-          [D] pool goes in transposed), rows on 16-byte boundaries.
-    k_scale, v_scale: the value of code 1 of an E4M3 cache.
+          [D] pool goes in transposed), rows on 16-byte boundaries.  With
+          k_blocks and v_blocks an NVFP4 cache: uint8 [pages][page_size]
+          [heads][D / 2], two E2M1 codes to a byte (low nibble = even d), D a
+          multiple of 64, strides multiples of D / 2.
+    k_scale, v_scale: the value of code 1 of an E4M3 cache, the scale of all of
+          an NVFP4 one.
+    k_blocks, v_blocks: E4M3 (float8_e4m3fn or uint8) [pages][page_size][heads]
+          [D / 16], one scale per 16 values; strides an eighth of k's and v's.
     """
 
-    def __init__(self, k, v, *, k_scale: float = 1.0, v_scale: float = 1.0):
+    def __init__(self, k, v, *, k_scale: float = 1.0, v_scale: float = 1.0, k_blocks=None, v_blocks=None):
         torch = _t()
+        if k_blocks is not None or v_blocks is not None:
+            self._nvfp4(k, v, float(k_scale), float(v_scale), k_blocks, v_blocks)
+            return
         _need(k.is_cuda and k.dim() == 4 and v.shape == k.shape and v.dtype == k.dtype
               and v.device == k.device, "k and v must be CUDA [pages][page_size][heads][D] tensors alike")
         _need(k.dtype in (torch.bfloat16, torch.float8_e4m3fn, torch.uint8),
               "a cache holds bf16 or E4M3 (float8_e4m3fn or uint8) values")
         _need(k.stride(3) == 1 and v.stride(3) == 1, "the values of a head must be contiguous")
         self.k, self.v = k, v
+        self.nvfp4, self.k_blocks, self.v_blocks = False, None, None
         self.fp8 = k.dtype != torch.bfloat16
         _need(self.fp8 or (k_scale == 1.0 and v_scale == 1.0), "scales go with an E4M3 cache")
         self.pages, self.page_size, self.heads, self.D = k.shape
@@ -93,10 +110,72 @@ class KVCache:
         self.device = k.device
         self._struct = DvlKVCache(DVL_FP8 if self.fp8 else DVL_BF16, self.pages, self.page_size,
                                   self.heads, self.D, 0, k.data_ptr(), v.data_ptr(), *k.stride()[:3],
-                                  *v.stride()[:3], self.k_scale, self.v_scale)
+                                  *v.stride()[:3], self.k_scale, self.v_scale, None, None)
         # what the compiled module reads
         self._address = ctypes.addressof(self._struct)
         self._dev = k.get_device()
+
+    def _nvfp4(self, k, v, k_scale, v_scale, k_blocks, v_blocks):
+        torch = _t()
+        _need(k_blocks is not None and v_blocks is not None, "k_blocks and v_blocks go together")
+        _need(k.is_cuda and k.dim() == 4 and v.shape == k.shape and v.device == k.device and
+              k.dtype == v.dtype == torch.uint8 and k.shape[3] % 32 == 0,
+              "k and v of an NVFP4 cache must be CUDA uint8 [pages][page_size][heads][D / 2] tensors alike, "
+              "D a multiple of 64")
+        for codes, blocks in ((k, k_blocks), (v, v_blocks)):
+            _need(blocks.device == k.device and blocks.dtype in (torch.float8_e4m3fn, torch.uint8) and
+                  blocks.shape == (*k.shape[:3], k.shape[3] // 8),
+                  "k_blocks and v_blocks must be E4M3 [pages][page_size][heads][D / 16] tensors on k's device")
+            # (the stride of an axis of one is nobody's)
+            _need(codes.stride(3) == 1 and (blocks.stride(3) == 1 or blocks.shape[3] == 1) and
+                  all(n == 1 or s == 8 * t for n, s, t in zip(k.shape[:3], codes.stride(), blocks.stride())),
+                  "the values of a head must be contiguous, and the scales' strides an eighth of the codes'")
+        self.k, self.v, self.k_blocks, self.v_blocks = k, v, k_blocks, v_blocks
+        self.fp8, self.nvfp4 = False, True
+        self.pages, self.page_size, self.heads = k.shape[:3]
+        self.D = 2 * k.shape[3]
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.device = k.device
+        strides = [2 * s if n > 1 else 0 for x in (k, v) for n, s in zip(x.shape, x.stride()[:3])]  # in values
+        self._struct = DvlKVCache(DVL_NVFP4, self.pages, self.page_size, self.heads, self.D, 0, k.data_ptr(),
+                                  v.data_ptr(), *strides, k_scale, v_scale, k_blocks.data_ptr(),
+                                  v_blocks.data_ptr())
+        self._address = ctypes.addressof(self._struct)
+        self._dev = k.get_device()
+
+
+class Rope:
+    """The rotation frequencies of a model, for qk_norm_rope.
+
+    dim:   rotated values of a head (its first ones), a multiple of 16.
+    theta: pair i turns by theta^(-2 i / dim) radians per position, unless
+    freqs: the dim / 2 frequencies themselves, in radians per position.
+    interleaved: the pairs are (2i, 2i + 1) instead of (i, i + dim / 2).
+    """
+
+    def __init__(self, dim: int, *, theta: float = 10000.0, freqs=None, interleaved: bool = False, device="cuda",
+                 stream=None):
+        torch = _t()
+        _need(dim >= 16 and dim % 16 == 0, "dim must be a positive multiple of 16")
+        if freqs is None:
+            _need(theta > 0 and math.isfinite(theta), "theta must be positive")
+            freqs = [theta ** (-2 * i / dim) for i in range(dim // 2)]
+        freqs = [float(f) for f in freqs]
+        _need(len(freqs) == dim // 2 and all(math.isfinite(f) for f in freqs), "freqs must be dim / 2 finite numbers")
+        self.dim, self.interleaved = dim, bool(interleaved)
+        # turns per position as 64-bit fractions: position x freq, modulo one
+        # turn, is then an integer product that wraps
+        turns = [round(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64)) for f in freqs]
+        turns = [(t + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns]
+        self.freq = _empty(dim // 2, torch.int64, device, stream)
+        with torch.cuda.device(self.freq.device):
+            copy = torch.tensor(turns, dtype=torch.int64)
+            if stream is None:
+                self.freq.copy_(copy)
+            else:
+                handle = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+                with torch.cuda.stream(handle):
+                    self.freq.copy_(copy)
 
 
 def _workspace(n: int, device, stream):

@@ -273,10 +273,13 @@ dvl_status dvl_score_ids(const dvl_head *head, const void *h, int32_t M,
 /* ---------------------------------------------------------------------- */
 /* The drafting step around the head                                      */
 /*                                                                        */
-/* What a drafter's own layer runs between two draft calls: attention of  */
-/* the new tokens over its paged cache, the residual addition and norm in */
-/* front of a projection or of the head, the choice of the next beams     */
-/* from the head's logits, and the reordering of what belongs to a beam.  */
+/* What a drafter's own layer runs between two draft calls: the norm and  */
+/* position rotation of the new queries and keys, which go to the paged   */
+/* cache in the same pass, attention of the new tokens over the cache,    */
+/* the residual addition and norm in front of a projection or of the      */
+/* head, the choice of the next beams from the head's logits, the         */
+/* reordering of what belongs to a beam, and, after a verification, the   */
+/* cached tokens that were kept moving together.                          */
 /* The pages describe the step (M = 1 for a draft step, 3 for an MTP2     */
 /* verify step, a concurrent batch of 8), not these operators.            */
 /* ---------------------------------------------------------------------- */
@@ -340,9 +343,17 @@ dvl_status dvl_add_rmsnorm(const dvl_norm *args, void *stream);
  * values of a head are consecutive.  Every (page, token, head) row starts on a
  * 16-byte boundary, and a page spans at most 10^9 elements (page_size token
  * strides plus heads head strides: offsets within a page are 32-bit; pages may
- * lie any distance apart). */
+ * lie any distance apart).
+ * An NVFP4 cache holds E2M1 codes, two to a byte (low nibble = even d), one
+ * E4M3 scale per 16 consecutive values of a row, and one fp32 scale for all
+ * keys and one for all values: value = e2m1 * e4m3 * k_scale.  D and every
+ * stride are multiples of 64, strides of D too (elements are 4-bit values: a
+ * row is D / 2 bytes).  The scales lie as the codes do, in an eighth of the
+ * room: the scales of a row that starts at byte x of k start at byte x / 8 of
+ * k_blocks.  (The last two fields are read with DVL_NVFP4 alone.) */
 typedef struct dvl_kv_cache {
-    int32_t dtype;            /* DVL_BF16, or DVL_FP8 (E4M3 codes, one scale each) */
+    int32_t dtype;            /* DVL_BF16, DVL_FP8 (E4M3 codes, one scale each) or
+                                 DVL_NVFP4                                         */
     int32_t pages;            /* pages of the pool                                 */
     int32_t page_size;        /* tokens per page, >= 1                             */
     int32_t heads;            /* key-value heads                                   */
@@ -351,7 +362,10 @@ typedef struct dvl_kv_cache {
     void *k, *v;              /* [pages][page_size][heads][D]                      */
     int64_t k_page_stride, k_token_stride, k_head_stride;
     int64_t v_page_stride, v_token_stride, v_head_stride;
-    float k_scale, v_scale;   /* value of code 1 (DVL_FP8); 1 for bf16             */
+    float k_scale, v_scale;   /* value of code 1 (DVL_FP8), scale of all (DVL_NVFP4);
+                                 1 for bf16                                        */
+    void *k_blocks, *v_blocks; /* DVL_NVFP4: E4M3 [pages][page_size][heads][D/16],
+                                 16-byte aligned                                   */
 } dvl_kv_cache;
 
 /* Bytes of device workspace a dvl_paged_attention call with this cache, T new
@@ -371,11 +385,11 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
  *   lse = m + ln(sum_j exp(s_j - m))
  * n = 0 gives out 0 and lse -inf.  Positions at or above n are not read into
  * the result, whatever the cache holds there.  Sums and softmax statistics are
- * fp32.  Products are exact, except that with an FP8 cache query values below
- * 2^-29 of their row's largest are rounded to a grid of 2^-38 of it.  The
+ * fp32.  Products are exact, except that with an FP8 or NVFP4 cache query values
+ * below 2^-29 of their row's largest are rounded to a grid of 2^-38 of it.  The
  * weights exp(s_j - m) are rounded before they meet V: to bf16 (2^-8
- * relative), or with an FP8 cache to f16 (2^-11 relative down to 2^-29, a grid
- * of 2^-39 below).  The result does not depend on timing: the same call on the
+ * relative), or with an FP8 or NVFP4 cache to f16 (2^-11 relative down to 2^-29,
+ * a grid of 2^-39 below).  The result does not depend on timing: the same call on the
  * same device gives the same bits.
  *   q:        device bf16 [B][T][Hq][D]; strides in elements for the first
  *             three, the last is 1; 16-byte aligned rows.
@@ -480,6 +494,92 @@ typedef struct dvl_beam_pages {
 dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl_beam_pages *pages,
                             const dvl_kv_cache *cache, const int32_t *parents, int32_t batch,
                             int32_t beams, int32_t k, void *stream);
+
+/* Arguments of dvl_qk_norm_rope.  Tensors are device memory, cache is a HOST
+ * pointer; strides are in elements, multiples of 8, and rows of D consecutive
+ * values start on 16-byte boundaries. */
+typedef struct dvl_qk {
+    int64_t rows;             /* new tokens, 0 .. 2^31 - 1; 0 enqueues nothing     */
+    int32_t Hq, H, D;         /* query heads, key-value heads (the cache's), head
+                                 width: a multiple of 16, <= DVL_MAX_HEAD_DIM      */
+    int32_t rot;              /* the first rot values of a head are rotated: a
+                                 multiple of 16, <= D; 0: none                     */
+    int32_t interleaved;      /* pairs (2i, 2i + 1) instead of (i, i + rot / 2)    */
+    float eps;                /* added to the mean square, finite, >= 0            */
+    const void *q, *k, *v;    /* bf16 [rows][Hq][D], [rows][H][D], [rows][H][D];
+                                 v goes with a cache (NULL without)                */
+    int64_t q_stride, q_head_stride, k_stride, k_head_stride, v_stride, v_head_stride;
+    const void *q_weight, *k_weight; /* bf16 [D], 16-byte aligned, or NULL: no norm */
+    const uint64_t *freq;     /* [rot / 2]: turns per position in units of 2^-64   */
+    const int32_t *positions; /* [rows], or NULL: the token's place in its sequence */
+    void *q_out;              /* bf16 [rows][Hq][D] (out); may be q itself         */
+    int64_t q_out_stride, q_out_head_stride;
+    void *k_out;              /* bf16 [rows][H][D] (out), or NULL with a cache; may
+                                 be k itself                                       */
+    int64_t k_out_stride, k_out_head_stride;
+    const dvl_kv_cache *cache; /* HOST, or NULL                                    */
+    const int32_t *table;     /* with a cache: [B][table_width], rows table_stride
+                                 apart                                             */
+    int64_t table_stride;
+    int32_t table_width, B;
+    const int32_t *lengths;   /* [B]: cached tokens, the new ones included         */
+    const int32_t *starts;    /* [B + 1] rising: sequence b's new tokens are rows
+                                 [starts[b], starts[b + 1]); or NULL: rows / B each */
+} dvl_qk;
+
+/* Norm of the new tokens' queries and keys for each head, rotation by their
+ * position, and the new keys and values to their places of the cache, in one
+ * pass.  For every row and head, in fp32:
+ *   y = x w / sqrt(mean(x^2) + eps)          (y = x without a weight),
+ *   of each pair (y1, y2) of the first rot values, t = position * freq turns:
+ *   y1 cos t - y2 sin t,  y2 cos t + y1 sin t;   the other values stay.
+ * Values are not normed or rotated.  The turns' fractional part is exact to
+ * 2^-32 whatever the position; cos and sin are off by at most 2^-21 (less than
+ * a hundredth of a bf16 rounding).  q_out and k_out are rounded to bf16 once.
+ * With a cache, row r is the newest-but-(end - 1 - r) token of its sequence b
+ * (end: starts[b + 1]): its place is p = lengths[b] - (end - r), page
+ * table[b][p / page_size], slot p % page_size.  Keys and values go there in the
+ * cache's type, rounded once from fp32: to bf16; to E4M3, RNE_e4m3(y / scale),
+ * saturating at 448 (the quotient is a product with the fp32 reciprocal); or
+ * to NVFP4: per 16 values s = RNE_e4m3(max |y| / (6 scale)), code =
+ * RNE_e2m1(y / (s scale)), all codes 0 where s is 0, both saturating.  A NaN in
+ * y stays one in bf16 and E4M3, and makes its 16 values NaN in NVFP4 (an
+ * infinity becomes the largest number).
+ * A place below 0 or past the table, or a page outside the pool, is not written
+ * (q_out and k_out are).  Rows past starts[B] are left as they were, in all
+ * outputs.  Two rows with one place in the cache leave either's values there.
+ * Errors: DVL_ERR_INVALID_ARG (sizes, pointers or alignment outside the above;
+ * a key-value head count or D other than the cache's; rows not a multiple of B
+ * without starts; rot > 0 with neither cache nor positions; v without cache or
+ * the reverse; neither cache nor k_out; output strides that make rows overlap),
+ * DVL_ERR_CUDA. */
+dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
+
+/* Keep some of the newest tokens of every sequence, in order, without gaps:
+ * for sequence b and i < counts[b], the cached token at place first[b] +
+ * keep[b][i] moves to place first[b] + i, in place (keys, values and an NVFP4
+ * cache's scales), and
+ *   lengths_out[b] = first[b] + counts[b].
+ * After a verification first is the length before the drafted tokens and keep
+ * names the accepted ones (a path of a tree); with first 0 or a few tokens, keep
+ * names what remains of a long cache.  Tokens past the new length stay where
+ * they are, and so do the tables.
+ *   lengths: device int32 [B]: cached tokens of each sequence.  Above
+ *            table_width * page_size counts as that.
+ *   first:   device int32 [B], >= 0 (below counts as 0).
+ *   keep:    device int32 [B][M], rows keep_stride apart: places relative to
+ *            first, strictly rising (so keep[b][i] >= i).  A sequence whose row
+ *            does not rise holds unspecified tokens in [first, first + counts).
+ *   counts:  device int32 [B]: below 0 counts as 0, above M as M.
+ *   M:       >= 0, any size.  lengths_out: device int32 [B], or NULL; shares no
+ *            byte with an input.
+ * A place that is not below the sequence's length, or whose page id is outside
+ * the pool, moves nothing.  Sequences share no page that is written.
+ * Errors: DVL_ERR_INVALID_ARG, DVL_ERR_CUDA. */
+dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64_t table_stride,
+                          int32_t table_width, const int32_t *lengths, const int32_t *first,
+                          const int32_t *keep, int64_t keep_stride, const int32_t *counts,
+                          int32_t B, int32_t M, int32_t *lengths_out, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Load time                                                              */
