@@ -463,10 +463,13 @@ dvl_status dvl_qk_norm_rope(const dvl_qk *p, void *stream)
         const dvl_status st = check_cache(c);
         if (st != DVL_OK)
             return st;
-        if (c->heads != p->H || c->D != p->D || p->B < 0 || p->table_width < 1 || p->table_stride < 0 ||
-            (int64_t)p->table_width * c->page_size > 0x7fffffffLL || !p->table || !aligned(p->table, 4) ||
-            !p->lengths || !aligned(p->lengths, 4) || !aligned(p->starts, 4) ||
+        if (c->heads != p->H || c->D != p->D || p->B < 0 || !aligned(p->starts, 4) ||
             (p->B == 0 ? rows > 0 && !p->starts : !p->starts && rows % p->B != 0))
+            return DVL_ERR_INVALID_ARG;
+        if (p->B > 0 &&
+            (p->table_width < 1 || p->table_stride < 0 ||
+             (int64_t)p->table_width * c->page_size > 0x7fffffffLL || !p->table || !aligned(p->table, 4) ||
+             !p->lengths || !aligned(p->lengths, 4)))
             return DVL_ERR_INVALID_ARG;
         // reciprocals of the scales, and products with an E4M3 scale, stay normal numbers
         for (float s : {c->k_scale, c->v_scale})

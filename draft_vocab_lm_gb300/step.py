@@ -153,8 +153,7 @@ class Rope:
     interleaved: the pairs are (2i, 2i + 1) instead of (i, i + dim / 2).
     """
 
-    def __init__(self, dim: int, *, theta: float = 10000.0, freqs=None, interleaved: bool = False, device="cuda",
-                 stream=None):
+    def __init__(self, dim: int, *, theta: float = 10000.0, freqs=None, interleaved: bool = False, device="cuda"):
         torch = _t()
         _need(dim >= 16 and dim % 16 == 0, "dim must be a positive multiple of 16")
         if freqs is None:
@@ -167,15 +166,8 @@ class Rope:
         # turn, is then an integer product that wraps
         turns = [round(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64)) for f in freqs]
         turns = [(t + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns]
-        self.freq = _empty(dim // 2, torch.int64, device, stream)
-        with torch.cuda.device(self.freq.device):
-            copy = torch.tensor(turns, dtype=torch.int64)
-            if stream is None:
-                self.freq.copy_(copy)
-            else:
-                handle = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
-                with torch.cuda.stream(handle):
-                    self.freq.copy_(copy)
+        # (the copy has ended when this returns: any stream may use it)
+        self.freq = torch.tensor(turns, dtype=torch.int64).to(device)
 
 
 def _workspace(n: int, device, stream):

@@ -551,7 +551,8 @@ typedef struct dvl_qk {
  * Errors: DVL_ERR_INVALID_ARG (sizes, pointers or alignment outside the above;
  * a key-value head count or D other than the cache's; rows not a multiple of B
  * without starts; rot > 0 with neither cache nor positions; v without cache or
- * the reverse; neither cache nor k_out; output strides that make rows overlap),
+ * the reverse; neither cache nor k_out; an output that overlaps itself, the other
+ * or an input but its own),
  * DVL_ERR_CUDA. */
 dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
 
