@@ -28,7 +28,7 @@
 namespace dvl {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLoads = 4;  // 16-byte loads in flight per lane
 
@@ -155,8 +155,9 @@ __device__ __forceinline__ void to_cache(const QkArgs &a, unsigned char *pool, u
     }
 }
 
-template <int LPH>
-__global__ void __launch_bounds__(kThreads) qk_kernel(const __grid_constant__ QkArgs a)
+// PAIRS: the other value of a pair is its neighbour, not rot / 2 away.
+template <int LPH, bool PAIRS>
+__global__ void __launch_bounds__(kThreads, 5) qk_kernel(const __grid_constant__ QkArgs a)
 {
     constexpr int kHeads = 32 / LPH;  // heads of a warp's step
     pdl_launch_dependents();
@@ -174,21 +175,6 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const __grid_constant__ Qk
     const int nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.H + kHeads - 1) / kHeads;
     const int steps = nq + (a.dtype >= 0 ? 2 * nk : nk);
     const int from = (int)((int64_t)steps * part / a.parts), to = (int)((int64_t)steps * (part + 1) / a.parts);
-    auto load = [&](int i) {
-        const int kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
-        const int head = (kind == 0 ? i : i - nq - (kind - 1) * nk) * kHeads + sub;
-        const uint16_t *p = kind == 0 ? a.q + row * a.qs + (int64_t)head * a.qh
-                          : kind == 1 ? a.k + row * a.ks + (int64_t)head * a.kh
-                                      : a.v + row * a.vs + (int64_t)head * a.vh;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (i < to && live && head < (kind == 0 ? a.Hq : a.H))
-            x = *reinterpret_cast<const uint4 *>(p + d);
-        return x;
-    };
-    uint4 x[kLoads];
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u)
-        x[u] = load(from + u);
 
     // place in the sequence and in the cache
     int position = 0;
@@ -214,131 +200,145 @@ __global__ void __launch_bounds__(kThreads) qk_kernel(const __grid_constant__ Qk
 
     // cos and sin of the lane's values; the partner's sign goes with the sine
     const int half = a.rot / 2;
+    const bool turned = d < a.rot;
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         cs[e] = 1.f;
         sn[e] = 0.f;
     }
-    if (d < a.rot) {
+    if (turned) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int j = a.interleaved ? (d + e) / 2 : d < half ? d + e : d + e - half;
-            const bool second = a.interleaved ? e & 1 : d >= half;
+            if (PAIRS && (e & 1)) {
+                cs[e] = cs[e - 1];
+                sn[e] = -sn[e - 1];
+                continue;
+            }
+            const int j = PAIRS ? (d + e) / 2 : d < half ? d + e : d + e - half;
             const uint64_t turns = (uint64_t)(int64_t)position * __ldg(a.freq + j);
             constexpr float kTurn = 6.283185307179586f / 4294967296.f;
             float s, c;
             __sincosf((float)(int32_t)(turns >> 32) * kTurn, &s, &c);
             cs[e] = c;
-            sn[e] = second ? s : -s;
+            sn[e] = PAIRS || d < half ? -s : s;
         }
     }
-    const int partner = a.interleaved || d >= a.rot ? lane : d < half ? lane + half / 8 : lane - half / 8;
+    const int partner = PAIRS || !turned ? lane : d < half ? lane + half / 8 : lane - half / 8;
+    // a value that is not rotated meets no other (0 times an infinity is no 0)
+    const uint32_t meets = turned ? 0xffffffffu : 0u;
+    auto others = [&](const uint4 &x, const float (&own)[8], float (&other)[8]) {
+        if constexpr (PAIRS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                other[e] = turned ? own[e ^ 1] : 0.f;
+        } else {
+            uint4 o;
+            o.x = __shfl_sync(kFull, x.x, partner) & meets;
+            o.y = __shfl_sync(kFull, x.y, partner) & meets;
+            o.z = __shfl_sync(kFull, x.z, partner) & meets;
+            o.w = __shfl_sync(kFull, x.w, partner) & meets;
+            unpack8(o, other);
+        }
+    };
 
-    // out = (x A + partner B) / rms, the weights in A and B
-    float A[8], B[8];
-    auto coefficients = [&](const uint16_t *weight) {
-        if (!weight) {
+    // Queries, then keys: the heads of steps [first, last) of `heads`.  Each
+    // value is (x A + partner B) / rms, with the weights in A and B.
+    const float per = 1.f / (float)a.D;
+    auto normed = [&](int first, int last, int heads, const uint16_t *from, int64_t stride,
+                      const uint16_t *weight, auto &&store) {
+        float A[8], B[8];
+        if (weight) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live)
+                w = __ldg(reinterpret_cast<const uint4 *>(weight + d));
+            float own[8], other[8];
+            unpack8(w, own);
+            others(w, own, other);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                A[e] = own[e] * cs[e];
+                B[e] = other[e] * sn[e];
+            }
+        } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 A[e] = cs[e];
                 B[e] = sn[e];
             }
-            return;
         }
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (live)
-            w = __ldg(reinterpret_cast<const uint4 *>(weight + d));
-        float own[8], other[8];
-        unpack8(w, own);
-        if (a.interleaved) {
+        int head = first * kHeads + sub;
+        const uint16_t *at = from + head * stride + d;
+        for (int i = first; i < last; i += kLoads) {
+            uint4 x[kLoads];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                other[e] = own[e ^ 1];
-        } else {
-            w.x = __shfl_sync(kFull, w.x, partner);
-            w.y = __shfl_sync(kFull, w.y, partner);
-            w.z = __shfl_sync(kFull, w.z, partner);
-            w.w = __shfl_sync(kFull, w.w, partner);
-            unpack8(w, other);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            A[e] = own[e] * cs[e];
-            B[e] = other[e] * sn[e];
-        }
-    };
-
-    auto process = [&](int i, const uint4 &x) {
-        const int kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
-        const int head = (kind == 0 ? i : i - nq - (kind - 1) * nk) * kHeads + sub;
-        const bool have = live && head < (kind == 0 ? a.Hq : a.H);
-        float y[8];
-        unpack8(x, y);
-        if (kind == 2) {
-            to_cache(a, a.cv, a.cvb, v_at + (int64_t)head * a.vhead, l, put && have, y, a.v_inv, a.v_scale);
-            return;
-        }
-        float inv = 1.f;
-        if (kind == 0 ? a.q_weight != nullptr : a.k_weight != nullptr) {
-            float sum = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum = fmaf(y[e], y[e], sum);
-#pragma unroll
-            for (int off = LPH / 2; off >= 1; off >>= 1)
-                sum += __shfl_xor_sync(kFull, sum, off);
-            inv = rsqrtf(sum / (float)a.D + a.eps);
-        }
-        float p[8];
-        if (a.rot > 0 && !a.interleaved) {
-            uint4 o;
-            o.x = __shfl_sync(kFull, x.x, partner);
-            o.y = __shfl_sync(kFull, x.y, partner);
-            o.z = __shfl_sync(kFull, x.z, partner);
-            o.w = __shfl_sync(kFull, x.w, partner);
-            unpack8(o, p);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                p[e] = y[e ^ 1];
-        }
-        // a value that is not rotated meets no other (0 times an infinity is no 0)
-        const bool turned = d < a.rot;
-        float z[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            z[e] = (turned ? fmaf(p[e], B[e], y[e] * A[e]) : y[e] * A[e]) * inv;
-        if (kind == 0) {
-            if (have)
-                *reinterpret_cast<uint4 *>(a.q_out + row * a.qos + (int64_t)head * a.qoh + d) = pack8(z);
-            return;
-        }
-        if (a.k_out && have)
-            *reinterpret_cast<uint4 *>(a.k_out + row * a.kos + (int64_t)head * a.koh + d) = pack8(z);
-        if (a.dtype >= 0)
-            to_cache(a, a.ck, a.ckb, k_at + (int64_t)head * a.khead, l, put && have, z, a.k_inv, a.k_scale);
-    };
-
-    int kind_of = -1;  // of the coefficients
-    for (int i0 = from; i0 < to; i0 += kLoads) {
-        uint4 now[kLoads];
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            now[u] = x[u];
-            x[u] = load(i0 + kLoads + u);
-        }
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-            const int i = i0 + u;
-            if (i >= to)
-                break;
-            const int kind = i < nq ? 0 : i < nq + nk ? 1 : 2;
-            if (kind != kind_of && kind < 2) {
-                coefficients(kind == 0 ? a.q_weight : a.k_weight);
-                kind_of = kind;
+            for (int u = 0; u < kLoads; ++u) {
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (i + u < last && live && head + u * kHeads < heads)
+                    x[u] = *reinterpret_cast<const uint4 *>(at);
+                at += kHeads * stride;
             }
-            process(i, now[u]);
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                if (i + u >= last)
+                    break;
+                float y[8], p[8];
+                unpack8(x[u], y);
+                others(x[u], y, p);
+                float inv = 1.f;
+                if (weight) {
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum = fmaf(y[e], y[e], sum);
+#pragma unroll
+                    for (int off = LPH / 2; off >= 1; off >>= 1)
+                        sum += __shfl_xor_sync(kFull, sum, off);
+                    inv = rsqrtf(fmaf(sum, per, a.eps));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = fmaf(p[e], B[e], y[e] * A[e]) * inv;
+                store(head, live && head < heads, y);
+                head += kHeads;
+            }
+        }
+    };
+    if (from < nq)
+        normed(from, min(to, nq), a.Hq, a.q + row * a.qs, a.qh, a.q_weight,
+               [&](int head, bool have, const float (&y)[8]) {
+                   if (have)
+                       *reinterpret_cast<uint4 *>(a.q_out + row * a.qos + head * a.qoh + d) = pack8(y);
+               });
+    if (to > nq && from < nq + nk)
+        normed(max(from, nq) - nq, min(to, nq + nk) - nq, a.H, a.k + row * a.ks, a.kh, a.k_weight,
+               [&](int head, bool have, const float (&y)[8]) {
+                   if (a.k_out && have)
+                       *reinterpret_cast<uint4 *>(a.k_out + row * a.kos + head * a.koh + d) = pack8(y);
+                   if (a.dtype >= 0)
+                       to_cache(a, a.ck, a.ckb, k_at + head * a.khead, l, put && have, y, a.k_inv, a.k_scale);
+               });
+    if (to > nq + nk) {
+        const int first = max(from, nq + nk) - nq - nk, last = to - nq - nk;
+        for (int i = first; i < last; i += kLoads) {
+            uint4 x[kLoads];
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int head = (i + u) * kHeads + sub;
+                x[u] = make_uint4(0, 0, 0, 0);
+                if (i + u < last && live && head < a.H)
+                    x[u] = *reinterpret_cast<const uint4 *>(a.v + row * a.vs + head * a.vh + d);
+            }
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                if (i + u >= last)
+                    break;
+                const int head = (i + u) * kHeads + sub;
+                float y[8];
+                unpack8(x[u], y);
+                to_cache(a, a.cv, a.cvb, v_at + head * a.vhead, l, put && live && head < a.H, y, a.v_inv,
+                         a.v_scale);
+            }
         }
     }
 }
@@ -361,8 +361,13 @@ cudaError_t launch_qk_norm_rope(QkArgs &a, cudaStream_t s)
     const int64_t blocks = (a.rows * a.parts + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    void (*kernel)(QkArgs) = lanes == 2 ? qk_kernel<2> : lanes == 4 ? qk_kernel<4> : lanes == 8 ? qk_kernel<8>
-                           : lanes == 16 ? qk_kernel<16> : qk_kernel<32>;
+    void (*const kernels[2][5])(QkArgs) = {
+        {qk_kernel<2, false>, qk_kernel<4, false>, qk_kernel<8, false>, qk_kernel<16, false>, qk_kernel<32, false>},
+        {qk_kernel<2, true>, qk_kernel<4, true>, qk_kernel<8, true>, qk_kernel<16, true>, qk_kernel<32, true>}};
+    int at = 0;
+    while (2 << at < lanes)
+        ++at;
+    const auto kernel = kernels[a.interleaved][at];
     return launch_pdl(kernel, (unsigned)blocks, kThreads, 0, s, a);
 }
 
