@@ -96,6 +96,8 @@ struct KeepArgs {
     const int32_t *table, *lengths, *first, *keep, *counts;
     int64_t table_stride, keep_stride;
     int32_t *lengths_out;
+    uint32_t page_mul;                  // pos / page_size = pos * page_mul >> page_shift
+    int page_shift;
     int blocks;                         // per sequence
 };
 cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s);

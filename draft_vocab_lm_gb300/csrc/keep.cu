@@ -9,8 +9,8 @@
 // keep[i] >= i: what a step of consecutive i reads lies at or past what it and
 // every earlier step writes, and one barrier between a step's reads and its
 // writes is all the order there is to keep -- among the threads that touch the
-// same bytes.  Those are one block: a block owns 32 columns (16 bytes each) of
-// a token, of one sequence, and walks its list, so blocks never meet.
+// same bytes.  Those are one block: a block owns a few columns (16 bytes each)
+// of a token, of one sequence, and walks its list, so blocks never meet.
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"
@@ -21,57 +21,82 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 8;  // of a warp's step
+constexpr int kRows = 8;  // loads in flight per lane
 
-template <typename U>
-__device__ __forceinline__ void keep_columns(const KeepArgs &a, const KeepPool &pool, int b, int col)
+// Where a row of the list lies and goes in the block's columns, in bytes from
+// the pool's start; from < 0: nowhere.
+struct Move {
+    int64_t from, to;
+};
+
+// A step: every warp moves kRows * (32 / COLS) rows, 32 / COLS at a time.
+template <typename U, int COLS>
+__device__ __forceinline__ void keep_columns(const KeepArgs &a, const KeepPool &pool, int b, int col0)
 {
+    constexpr int kAtOnce = 32 / COLS;             // rows of a load
+    constexpr int kMine = kRows * kAtOnce;         // rows of a warp's step
+    constexpr int kLook = (kMine + 31) / 32;       // looked up by a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int count = max(0, min(a.counts[b], a.M));
     const int first = max(0, a.first[b]);
     const int64_t length = min((int64_t)a.lengths[b], (int64_t)a.width * a.page_size);
+    const int32_t *keep = a.keep + b * a.keep_stride, *table = a.table + b * a.table_stride;
+    const int col = col0 + lane % COLS;
     const bool mine = col < pool.cols;
     const int head = col / pool.units;
-    unsigned char *at = pool.base + (int64_t)head * pool.head + (col - head * pool.units) * (int)sizeof(U);
-    for (int i0 = 0; i0 < count; i0 += kWarps * kRows) {
-        // lanes 0 .. kRows - 1 look up where the warp's rows are, the next
-        // kRows where they go
-        const int i = i0 + warp * kRows + lane % kRows;
-        int64_t place = -1, other = -1;
-        if (lane < 2 * kRows && i < count) {
-            const int from = a.keep[b * a.keep_stride + i];
-            const int64_t source = from < 0 ? -1 : (int64_t)first + from;
-            place = lane < kRows ? source : (int64_t)first + i;
-            other = lane < kRows ? (int64_t)first + i : source;
-        }
-        int page = -1, slot = 0;
-        if (place >= 0 && place != other && place < length) {
-            const int entry = (int)place / a.page_size;
-            slot = (int)place - entry * a.page_size;
-            page = a.table[b * a.table_stride + entry];
-            if ((unsigned)page >= (unsigned)a.pages)
-                page = -1;
-        }
-        U v[kRows];
-        unsigned char *dst[kRows];
+    unsigned char *at = pool.base + head * pool.head + (col - head * pool.units) * (int)sizeof(U);
+
+    auto place = [&](int64_t pos) -> int64_t {
+        const int entry = (int)((uint64_t)(uint32_t)pos * a.page_mul >> a.page_shift);
+        const int page = table[entry];
+        return (unsigned)page < (unsigned)a.pages ? page * pool.page + (pos - entry * a.page_size) * pool.token
+                                                  : -1;
+    };
+    auto look_up = [&](int i0, Move (&m)[kLook]) {
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int sp = __shfl_sync(kFull, page, j), ss = __shfl_sync(kFull, slot, j);
-            const int dp = __shfl_sync(kFull, page, kRows + j), ds = __shfl_sync(kFull, slot, kRows + j);
-            dst[j] = nullptr;
-            if (mine && sp >= 0 && dp >= 0) {
-                dst[j] = at + dp * pool.page + (int64_t)ds * pool.token;
-                v[j] = *reinterpret_cast<const U *>(at + sp * pool.page + (int64_t)ss * pool.token);
+        for (int k = 0; k < kLook; ++k) {
+            const int r = 32 * k + lane, i = i0 + warp * kMine + r;
+            m[k].from = m[k].to = -1;
+            if ((kMine >= 32 || r < kMine) && i < count) {
+                const int from = keep[i];
+                const int64_t src = (int64_t)first + from, dst = (int64_t)first + i;
+                if (from >= 0 && src != dst && src < length && dst < length) {
+                    m[k].from = place(src);
+                    m[k].to = place(dst);
+                    if (m[k].to < 0)
+                        m[k].from = -1;
+                }
             }
         }
+    };
+    Move now[kLook];
+    look_up(0, now);
+    for (int i0 = 0; i0 < count; i0 += kWarps * kMine) {
+        U v[kRows];
+        int64_t to[kRows];
+#pragma unroll
+        for (int j = 0; j < kRows; ++j) {
+            const int r = j * kAtOnce + lane / COLS;  // of the warp's rows
+            const int64_t from = __shfl_sync(kFull, now[j * kAtOnce / 32].from, r & 31);
+            to[j] = __shfl_sync(kFull, now[j * kAtOnce / 32].to, r & 31);
+            if (from < 0 || !mine)
+                to[j] = -1;
+            else
+                v[j] = *reinterpret_cast<const U *>(at + from);
+        }
+        // the next step's places are looked up while its rows are on their way
+        // (past the list's end none are)
+        if (i0 + kWarps * kMine < count)
+            look_up(i0 + kWarps * kMine, now);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
-            if (dst[j])
-                *reinterpret_cast<U *>(dst[j]) = v[j];
+            if (to[j] >= 0)
+                *reinterpret_cast<U *>(at + to[j]) = v[j];
     }
 }
 
+template <int COLS>
 __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const __grid_constant__ KeepArgs a)
 {
     pdl_launch_dependents();
@@ -83,25 +108,41 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const __grid_const
     while (blk < a.pool[p].first_block)
         --p;
     const KeepPool &pool = a.pool[p];
-    const int col = (blk - pool.first_block) * 32 + (threadIdx.x & 31);
+    const int col = (blk - pool.first_block) * COLS;
     if (pool.wide)
-        keep_columns<uint4>(a, pool, b, col);
+        keep_columns<uint4, COLS>(a, pool, b, col);
     else
-        keep_columns<uint32_t>(a, pool, b, col);
+        keep_columns<uint32_t, COLS>(a, pool, b, col);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s)
 {
-    a.blocks = 0;
+    DeviceInfo di;
+    const cudaError_t e = device_info(&di);
+    if (e != cudaSuccess)
+        return e;
+    auto blocks = [&](int cols) {
+        int64_t n = 0;
+        for (int p = 0; p < a.n_pools; ++p)
+            n += (a.pool[p].cols + cols - 1) / cols;
+        return n;
+    };
+    int cols = 32;
+    if (a.M > 8 * kWarps)
+        while (cols > 2 && a.B * blocks(cols) < 2 * di.sms)
+            cols /= 4;
+    int64_t n = 0;
     for (int p = 0; p < a.n_pools; ++p) {
-        a.pool[p].first_block = a.blocks;
-        a.blocks += (a.pool[p].cols + 31) / 32;
+        a.pool[p].first_block = (int)n;
+        n += (a.pool[p].cols + cols - 1) / cols;
     }
-    if ((int64_t)a.blocks * a.B > 0x7fffffffLL)
+    if (n * a.B > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
-    return launch_pdl(cache_keep_kernel, (unsigned)(a.blocks * a.B), kThreads, 0, s, a);
+    a.blocks = (int)n;
+    const auto kernel = cols == 32 ? cache_keep_kernel<32> : cols == 8 ? cache_keep_kernel<8> : cache_keep_kernel<2>;
+    return launch_pdl(kernel, (unsigned)(n * a.B), kThreads, 0, s, a);
 }
 
 }  // namespace dvl

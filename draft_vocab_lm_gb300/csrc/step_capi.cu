@@ -55,6 +55,17 @@ int half_bytes(const dvl_kv_cache *c)
     return c->dtype == DVL_BF16 ? 4 : c->dtype == DVL_FP8 ? 2 : 1;
 }
 
+// pos / page_size for 0 <= pos < 2^31: multiply by 2^(31 + s) / page_size
+// rounded up, s = ceil(log2 page_size); the error stays below one unit.
+void page_division(int page_size, uint32_t *mul, int *shift)
+{
+    int s = 0;
+    while ((1ll << s) < page_size)
+        ++s;
+    *shift = 31 + s;
+    *mul = (uint32_t)((1ull << *shift) / (uint64_t)page_size + 1);
+}
+
 // Query rows per cached head, or 0 when T and Hq are outside the limits.
 int query_rows(const dvl_kv_cache *c, int32_t T, int32_t Hq)
 {
@@ -286,13 +297,7 @@ dvl_status dvl_paged_attention(const dvl_kv_cache *cache, const void *q, int64_t
     a.pages = cache->pages;
     a.page_size = cache->page_size;
     a.max_len = table_width * cache->page_size;
-    // pos / page_size for 0 <= pos < 2^31: multiply by 2^(31 + s) / page_size
-    // rounded up, s = ceil(log2 page_size); the error stays below one unit
-    int s = 0;
-    while ((1ll << s) < cache->page_size)
-        ++s;
-    a.page_shift = 31 + s;
-    a.page_mul = (uint32_t)((1ull << a.page_shift) / (uint64_t)cache->page_size + 1);
+    page_division(cache->page_size, &a.page_mul, &a.page_shift);
     a.qk_scale = scale * cache->k_scale * 1.4426950408889634f;
     a.v_scale = cache->v_scale;
     return done(attn::launch_attention(a, cfg, static_cast<cudaStream_t>(stream)));
@@ -539,7 +544,7 @@ dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64
     const dvl_status st = check_cache(cache);
     if (st != DVL_OK)
         return st;
-    if (B < 0 || M < 0 || M > 0x7fffffff - 64 || table_width < 1 || table_stride < 0 || (B > 1 && keep_stride < 0) ||
+    if (B < 0 || M < 0 || M > 0x7fffffff - 65536 || table_width < 1 || table_stride < 0 || (B > 1 && keep_stride < 0) ||
         (int64_t)table_width * cache->page_size > 0x7fffffffLL || !table || !aligned(table, 4) || !lengths ||
         !aligned(lengths, 4) || !first || !aligned(first, 4) || (M > 0 && !keep) || !aligned(keep, 4) || !counts ||
         !aligned(counts, 4) || !aligned(lengths_out, 4))
@@ -589,6 +594,7 @@ dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64
     a.keep_stride = keep_stride;
     a.counts = counts;
     a.lengths_out = lengths_out;
+    page_division(cache->page_size, &a.page_mul, &a.page_shift);
     return done(launch_cache_keep(a, static_cast<cudaStream_t>(stream)));
 }
 
