@@ -41,7 +41,12 @@
 // its values while the values are used, which keeps P chunks per group in
 // flight in the least shared memory, hence the most warps per SM.
 // Up to 8 query rows (RT = 0) the upper half of every MMA is padding: its
-// softmax is left out and its accumulators are not kept.
+// softmax is left out and its accumulators are not kept.  With an NVFP4 cache
+// the products are turned round there: tokens are the 16 rows of the first
+// (S^T = K Q^T), columns of V those of the second (O^T = V^T P^T), the query
+// rows the 8 columns, so no half is padding and no accumulator is moved in and
+// out.  The weights change places between the two by an 8 x 8 transposition of
+// registers.
 //
 // Weights are rounded to the MMA operand type, at most 2^-8 relative for bf16
 // and 2^-11 for f16, independently per position; sums and statistics stay
@@ -94,10 +99,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
                  "r"(valid ? 16 : 0)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid)
+template <int BYTES>  // 4 or 8
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src, bool valid)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(valid ? 4 : 0)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
+                 "r"(valid ? BYTES : 0), "n"(BYTES)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit()
@@ -141,6 +147,20 @@ __device__ __forceinline__ uint16_t lds8(uint32_t addr)
     uint16_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
     return v;
+}
+// N words (1, 2 or 4) at once.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t addr, uint32_t (&w)[N])
+{
+    if constexpr (N == 1)
+        w[0] = lds32(addr);
+    else if constexpr (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr)
+                     : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint4 &v)
 {
@@ -256,6 +276,14 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t x, uint32_t y)
     return r;
 }
 
+// An 8 x 8 matrix of f16, row g's values 2c and 2c + 1 with lane (g, c), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -302,6 +330,7 @@ struct Shape {
     static_assert(kTile <= 128, "lengths are limited so that a tile more fits 32 bits");
     static constexpr int kGroup = RT == 0 ? 32 : 32 * RT;  // threads
     static constexpr int kThreads = kGroup * G;
+    static constexpr bool kTurned = FMT == kFp4 && RT == 0;  // S^T and O^T
     // Rows that one access phase touches lie on distinct banks.  bf16: the
     // 16-byte units of a row are permuted by its lowest three bits (8 rows of
     // an ldmatrix).  FP8: padded pitches (8-byte loads of 4 rows for K, 4-byte
@@ -313,7 +342,7 @@ struct Shape {
     static constexpr int kBlocks = FMT == kFp4 ? DP / 16 : 0;  // bytes per row
     static constexpr int kQPitch = DP * 2 + 16;
     static constexpr int kRows = RT == 0 ? 8 : 16 * RT;    // query rows kept
-    static constexpr int kQRows = RT == 0 ? 16 : 16 * RT;  // rows of the operand
+    static constexpr int kQRows = kTurned ? 8 : RT == 0 ? 16 : 16 * RT;  // rows of the operand
     // One ring entry: a chunk's keys or values; also 32 columns of the rows.
     static constexpr int kEntry = max_of(TOK * (kKPitch + kBlocks), kRows * 4 * 32);
     static_assert(FMT != kFp4 || kEntry % 128 == 0, "fp4_place() permutes within 128 bytes");
@@ -332,8 +361,12 @@ struct Shape {
 
 // Where byte x of an NVFP4 entry's rows lies: its 32-byte piece is permuted by
 // the 128-byte line, so that four rows that follow each other, and four that
-// are two apart, lie on distinct banks at any width.
-__device__ __forceinline__ int fp4_place(int x) { return x ^ (((x >> 7) ^ (x >> 9)) & 3) << 5; }
+// are two apart, lie on distinct banks at any width.  The permutation of a sum
+// of rows is the permutations one after the other where the sum carries into
+// neither's bits (rows of less than a step of 4 or 8, and steps of that), so
+// that an address takes one xor with a constant: fp4_step().
+__host__ __device__ constexpr int fp4_step(int x) { return (((x >> 7) ^ (x >> 9)) & 3) << 5; }
+__device__ __forceinline__ int fp4_place(int x) { return x ^ fp4_step(x); }
 
 // The place among the joined columns of accumulator e (of a row) of column
 // tile n, and the output column there.  They are the same but for NVFP4, where
@@ -350,10 +383,10 @@ __device__ __forceinline__ int real_col(int v)
 }
 
 // The permutation of a row's columns while the groups' rows are joined.
-template <int FMT>
+template <int FMT, bool TURNED>
 __device__ __forceinline__ int swizzle(int r)
 {
-    return FMT != kBf16 ? (r & 1) << 2 : (r & 3) << 3;
+    return TURNED ? (r >> 1 & 3) << 3 : FMT != kBf16 ? (r & 1) << 2 : (r & 3) << 3;
 }
 
 // Where a token's row starts, found by one thread per token a chunk before the
@@ -408,15 +441,17 @@ __device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *co
                                           const unsigned char *blocks)
 {
     if constexpr (FMT == kFp4) {
-        // a row's scales, 4 bytes at a time; the padding's are zeros, too
-        constexpr int kUnits = DP / 64;
+        // a row's scales, 8 bytes at a time at a width of 128, else 4 (192 has
+        // 12); the padding's are zeros, too
+        constexpr int kBytes = DP == 128 ? 8 : 4;
+        constexpr int kUnits = DP / 16 / kBytes;
 #pragma unroll
         for (int u0 = 0; u0 < TOK * kUnits; u0 += N) {
             const int u = u0 + at, r = u / kUnits, unit = u % kUnits;
             if (u < TOK * kUnits) {
-                const bool have = r < live && unit * 32 < row_bytes;
-                const unsigned char *from = blocks + ((rows[r] - pool) >> 3) + unit * 4;
-                cp_async4(dst + TOK * pitch + u * 4, have ? from : blocks, have);
+                const bool have = r < live && unit * 8 * kBytes < row_bytes;
+                const unsigned char *from = blocks + ((rows[r] - pool) >> 3) + unit * kBytes;
+                cp_async_small<kBytes>(dst + TOK * pitch + u * kBytes, have ? from : blocks, have);
             }
         }
     }
@@ -435,8 +470,11 @@ __device__ __forceinline__ void load_rows(int row_bytes, const unsigned char *co
     for (int i = 0; i < (kStep < TOK ? TOK / kStep : 1); ++i) {
         const int r = r0 + i * kStep;
         const int unit = FMT == kBf16 ? col ^ (r & 7) : col;
-        const int place = r * pitch + unit * 16;
-        cp_async16(dst + (FMT == kFp4 ? fp4_place(place) : place), rows[r] + from, r < live);
+        const uint32_t to = FMT == kFp4
+                                ? ((dst + fp4_place(r0 * pitch + unit * 16)) ^ fp4_step(i * kStep * pitch)) +
+                                      i * kStep * pitch
+                                : dst + r * pitch + unit * 16;
+        cp_async16(to, rows[r] + from, r < live);
     }
 }
 
@@ -722,8 +760,12 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     constexpr int kGroup = S::kGroup;
     constexpr int kWarps = kThreads / 32;
     constexpr bool F16 = FMT != kBf16;   // the operands' type, else bf16
+    constexpr bool kTurned = S::kTurned;
     constexpr int NJ = RT == 0 ? 1 : 2;  // row halves kept per MMA (rows g, g + 8)
+    // rows whose softmax a lane takes part in: 16 mt + 8 j + g, or turned 2 c + j
+    constexpr int NS = kTurned ? 2 : NJ;
     constexpr int kNT = DP / 8;          // MMA column tiles of the output
+    constexpr int kOT = kTurned ? DP / 16 : kNT;  // its tiles
     constexpr int kSN = TOK / 8;         // MMA column tiles of the scores
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t s_scan[2 + kWarps];
@@ -862,26 +904,28 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         load_values();
     }
 
-    float o[kNT][2 * NJ];
-    float m[NJ], l[NJ];
-    int sees[NJ], sees_least = 0;
+    constexpr int kOE = kTurned ? 4 : 2 * NJ;  // accumulators kept of a tile
+    float o[kOT][kOE];
+    float m[NS], l[NS];
+    int sees[NS], sees_least = 0;
+    auto row_of = [&](int j) { return kTurned ? 2 * c + j : 16 * mt + 8 * j + g; };
     auto reset = [&]() {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
+        for (int j = 0; j < NS; ++j) {
             m[j] = kNegInf;
             l[j] = 0.f;
         }
 #pragma unroll
-        for (int n = 0; n < kNT; ++n)
+        for (int n = 0; n < kOT; ++n)
 #pragma unroll
-            for (int e = 0; e < 2 * NJ; ++e)
+            for (int e = 0; e < kOE; ++e)
                 o[n][e] = 0.f;
     };
     // Visible positions per row of the (sequence, head) that starts.
     auto start_pair = [&](int len) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int r = 16 * mt + 8 * j + g;
+        for (int j = 0; j < NS; ++j) {
+            const int r = row_of(j);
             sees[j] = r < a.rows ? len - (a.T - 1 - a.token_of(r)) : 0;
         }
         sees_least = len - (a.T - 1);
@@ -890,6 +934,117 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     start_pair(cur.len);
     store_q();
     __syncthreads();
+    // Value d of token tok of an NVFP4 entry.
+    auto fp4_value = [&](uint32_t entry, int tok, int d) {
+        const uint16_t code = lds8(entry + fp4_place(tok * S::kVPitch + d / 2)) >> 4 * (d & 1);
+        uint32_t x[4];
+        e2m1x8_f16x8(code & 15u, x);
+        return unpack1<true>((uint16_t)mul_f16x2(
+            x[0], e4m3x2_f16x2(lds8(entry + TOK * S::kVPitch + tok * S::kBlocks + d / 16))));
+    };
+    // The scores of a chunk's tokens with tokens as rows -- lane (g, c) holds
+    // tokens g and g + 8 of every 16 for query rows 2 c and 2 c + 1 -- and their
+    // weights in units of 2^-15, also as the second product's operand.  The
+    // lanes of a row compare their maxima only where one is above the running
+    // maximum, which after the first chunks is rare.
+    auto turned_weights = [&](uint32_t k_smem, int pos0, auto &s, auto &pa) {
+        constexpr int kTM = TOK / 16;
+#pragma unroll
+        for (int t = 0; t < kTM; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[t][e] = 0.f;
+        const uint32_t q_row = base + S::kQ + (lane & 7) * S::kQPitch + (lane >> 3) * 16;
+        const uint32_t k_row = k_smem + fp4_place(g * S::kKPitch) + 8 * c;
+        uint32_t scales[kTM][2][DP / 64];
+#pragma unroll
+        for (int t = 0; t < kTM; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                lds_words(k_smem + TOK * S::kKPitch + (16 * t + 8 * h + g) * S::kBlocks, scales[t][h]);
+#pragma unroll
+        for (int blk = 0; blk < DP / 64; ++blk) {
+            uint32_t qb[2][4];  // two steps each
+            ldsm4(qb[0], q_row + 128 * blk);
+            ldsm4(qb[1], q_row + 128 * blk + 64);
+#pragma unroll
+            for (int t = 0; t < kTM; ++t) {
+                uint32_t f[2][2][4];  // token half, word, pair of codes
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int step = (16 * t + 8 * h) * S::kKPitch;
+                    const uint2 x = lds64((k_row ^ (fp4_step(step) ^ blk << 5)) + step);
+                    const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(scales[t][h][blk], 0, c * 0x11));
+                    e2m1x8_f16x8(x.x, f[h][0]);
+                    e2m1x8_f16x8(x.y, f[h][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[h][0][i] = mul_f16x2(f[h][0][i], sc);
+                        f[h][1][i] = mul_f16x2(f[h][1][i], sc);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int w = j / 2, i = 2 * (j & 1);
+                    const uint32_t ka[4] = {f[0][w][i], f[1][w][i], f[0][w][i + 1], f[1][w][i + 1]};
+                    mma16<true>(s[t], ka, qb[w][i], qb[w][i + 1]);
+                }
+            }
+        }
+        float big[2] = {kNegInf, kNegInf};
+        const float2 sc = *reinterpret_cast<const float2 *>(row_scale + 2 * c);
+#pragma unroll
+        for (int t = 0; t < kTM; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[t][e] *= e & 1 ? sc.y : sc.x;
+        if (pos0 + TOK > sees_least) {  // some position is masked for some row
+#pragma unroll
+            for (int t = 0; t < kTM; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (pos0 + 16 * t + 8 * (e >> 1) + g >= sees[e & 1])
+                        s[t][e] = kNegInf;
+        }
+#pragma unroll
+        for (int t = 0; t < kTM; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                big[e & 1] = fmaxf(big[e & 1], s[t][e]);
+        if (__any_sync(kFull, big[0] > m[0] || big[1] > m[1])) {
+            float alpha[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                big[j] = fmaxf(big[j], m[j]);
+                big[j] = fmaxf(big[j], __shfl_xor_sync(kFull, big[j], 4));
+                big[j] = fmaxf(big[j], __shfl_xor_sync(kFull, big[j], 8));
+                big[j] = fmaxf(big[j], __shfl_xor_sync(kFull, big[j], 16));
+                alpha[j] = ex2(m[j] - (big[j] == kNegInf ? 0.f : big[j]));
+                m[j] = big[j];
+                l[j] *= alpha[j];
+            }
+#pragma unroll
+            for (int n = 0; n < kOT; ++n)
+#pragma unroll
+                for (int e = 0; e < kOE; ++e)
+                    o[n][e] *= alpha[e & 1];
+        }
+        float ref[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            ref[j] = m[j] == kNegInf ? 0.f : m[j] - 15.f;
+#pragma unroll
+        for (int t = 0; t < kTM; ++t) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[t][e] = ex2(s[t][e] - ref[e & 1]);
+                l[e & 1] += s[t][e];
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                pa[t][h] = transpose8(pack2<true>(s[t][2 * h], s[t][2 * h + 1]));
+        }
+    };
     bool first_part = true;  // still in the block's first (sequence, head)
     int t_first = cur.t;
     int entry = 0;
@@ -902,9 +1057,13 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         load_keys();  // into the entry of the previous values
         const uint32_t k_smem = ring + entry * S::kEntry;
         entry = entry + 1 == S::kEntries ? 0 : entry + 1;
-        uint32_t pa[TOK / 16][4];  // the weights as the second product's operand
-        float s[kSN][2 * NJ];
-        if (pos0 < cur.len) {
+        uint32_t pa[TOK / 16][kTurned ? 2 : 4];  // the weights as the second product's operand
+        float s[kTurned ? TOK / 16 : kSN][kTurned ? 4 : 2 * NJ];
+        if constexpr (kTurned) {
+            if (pos0 < cur.len) {
+                turned_weights(k_smem, pos0, s, pa);
+            }
+        } else if (pos0 < cur.len) {
             // scores
             float acc[kSN][4];
 #pragma unroll
@@ -917,16 +1076,15 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
             if constexpr (FMT == kFp4) {
                 // lane (g, c): token g of every eight, group c of every block of
                 // 64 values: 8 bytes of codes and one scale, four steps' operands
+                const uint32_t k_row = k_smem + fp4_place(g * S::kKPitch) + 8 * c;
 #pragma unroll
                 for (int n = 0; n < kSN; ++n) {
-                    const int tok = 8 * n + g;
                     uint32_t scales[DP / 64];
-#pragma unroll
-                    for (int blk = 0; blk < DP / 64; ++blk)
-                        scales[blk] = lds32(k_smem + TOK * S::kKPitch + tok * S::kBlocks + 4 * blk);
+                    lds_words(k_smem + TOK * S::kKPitch + (8 * n + g) * S::kBlocks, scales);
 #pragma unroll
                     for (int blk = 0; blk < DP / 64; ++blk) {
-                        const uint2 x = lds64(k_smem + fp4_place(tok * S::kKPitch + 32 * blk) + 8 * c);
+                        const uint2 x = lds64((k_row ^ (fp4_step(8 * n * S::kKPitch) ^ blk << 5)) +
+                                              8 * n * S::kKPitch);
                         const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(scales[blk], 0, c * 0x11));
                         uint32_t f[2][4];
                         e2m1x8_f16x8(x.x, f[0]);
@@ -1059,8 +1217,28 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 const int from = max(max(sees_least, 0) - pos0, 0);
                 const int to = min(cur.len - pos0, TOK);
                 for (int tok = from; tok < to; ++tok) {
+                    float w[NS];
+                    if constexpr (kTurned) {
+#pragma unroll
+                        for (int j = 0; j < NS; ++j) {
+                            float mine = tok & 8 ? s[0][2 + j] : s[0][j];
+                            if constexpr (TOK == 32)
+                                mine = tok & 16 ? (tok & 8 ? s[1][2 + j] : s[1][j]) : mine;
+                            w[j] = __shfl_sync(kFull, mine, (tok & 7) * 4 + c);
+                        }
+#pragma unroll
+                        for (int n = 0; n < kOT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float v = fp4_value(v_smem, tok, n / 4 * 64 + 8 * g + 2 * (n % 4) + e);
+#pragma unroll
+                                for (int j = 0; j < NS; ++j)
+                                    if (pos0 + tok < sees[j])
+                                        o[n][2 * e + j] = fmaf(w[j], v, o[n][2 * e + j]);
+                            }
+                        continue;
+                    } else {
                     const int src = (lane & ~3) + ((tok & 7) >> 1);
-                    float w[NJ];
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) {
                         float pair[kSN];
@@ -1078,14 +1256,9 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         for (int e = 0; e < 2; ++e) {
                             const int d = real_col<FMT>(out_col<FMT>(n, c, e));
                             float v;
-                            if constexpr (FMT == kFp4) {
-                                const uint16_t code = lds8(v_smem + fp4_place(tok * S::kVPitch + d / 2)) >>
-                                                      4 * (d & 1);
-                                const uint16_t sc = lds8(v_smem + TOK * S::kVPitch + tok * S::kBlocks + d / 16);
-                                uint32_t f[4];
-                                e2m1x8_f16x8(code & 15u, f);
-                                v = unpack1<true>((uint16_t)mul_f16x2(f[0], e4m3x2_f16x2(sc)));
-                            } else if constexpr (FMT == kFp8)
+                            if constexpr (FMT == kFp4)
+                                v = fp4_value(v_smem, tok, d);
+                            else if constexpr (FMT == kFp8)
                                 v = unpack1<true>((uint16_t)e4m3x2_f16x2(
                                     lds8(v_smem + tok * S::kVPitch + d)));
                             else
@@ -1096,6 +1269,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                                 if (pos0 + tok < sees[j])
                                     o[n][2 * j + e] = fmaf(w[j], v, o[n][2 * j + e]);
                         }
+                    }
                 }
                 group_sync<kGroup>(group);
                 if constexpr (FMT == kFp4) {  // a scale of 0 makes its values 0
@@ -1112,20 +1286,28 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 if constexpr (FMT == kFp4) {
                     // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
                     // 8 g .. 8 g + 7 of each block of 64; column tile j of a
-                    // block is columns 8 n + j.  The codes of two tokens are
+                    // block is columns 8 n + j, or turned, row tile j columns
+                    // 8 n + 2 j and 8 n + 2 j + 1.  The codes of two tokens are
                     // paired before they are widened, so that a byte holds both.
+                    const uint32_t v_row[2] = {v_smem + fp4_place(2 * c * S::kVPitch) + 4 * g,
+                                               v_smem + fp4_place((2 * c + 1) * S::kVPitch) + 4 * g};
+                    uint32_t scales[2][2][DP / 64];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            lds_words(v_smem + TOK * S::kVPitch + (16 * k + 8 * q + 2 * c + t) * S::kBlocks,
+                                      scales[q][t]);
 #pragma unroll
                     for (int blk = 0; blk < DP / 64; ++blk) {
                         uint32_t x[2][2][4];  // pair of tokens, odd column, half the column
 #pragma unroll
                         for (int q = 0; q < 2; ++q) {
-                            const int tok = 16 * k + 8 * q + 2 * c;
-                            const int from = tok * S::kVPitch + 32 * blk;
-                            const uint32_t w0 = lds32(v_smem + fp4_place(from) + 4 * g);
-                            const uint32_t w1 = lds32(v_smem + fp4_place(from + S::kVPitch) + 4 * g);
-                            const uint32_t sa = v_smem + TOK * S::kVPitch + tok * S::kBlocks + 4 * blk;
+                            const int step = (16 * k + 8 * q) * S::kVPitch;
+                            const uint32_t w0 = lds32((v_row[0] ^ (fp4_step(step) ^ blk << 5)) + step);
+                            const uint32_t w1 = lds32((v_row[1] ^ (fp4_step(step) ^ blk << 5)) + step);
                             const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(
-                                lds32(sa), lds32(sa + S::kBlocks), (g >> 1) * 0x11 + 0x40));
+                                scales[q][0][blk], scales[q][1][blk], (g >> 1) * 0x11 + 0x40));
                             e2m1x8_f16x8((w0 & 0x0f0f0f0fu) | (w1 & 0x0f0f0f0fu) << 4, x[q][0]);
                             e2m1x8_f16x8((w0 >> 4 & 0x0f0f0f0fu) | (w1 & 0xf0f0f0f0u), x[q][1]);
 #pragma unroll
@@ -1134,9 +1316,18 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                                 x[q][1][j] = mul_f16x2(x[q][1][j], sc);
                             }
                         }
+                        if constexpr (kTurned) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mma_rows<true, NJ>(o[8 * blk + j], pa[k], x[0][j & 1][j / 2], x[1][j & 1][j / 2]);
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t va[4] = {x[0][0][j], x[0][1][j], x[1][0][j], x[1][1][j]};
+                                mma16<true>(o[4 * blk + j], va, pa[k][0], pa[k][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                mma_rows<true, NJ>(o[8 * blk + j], pa[k], x[0][j & 1][j / 2],
+                                                   x[1][j & 1][j / 2]);
+                        }
                     }
                 } else if constexpr (FMT == kFp8) {
                     // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
@@ -1185,20 +1376,27 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 load_q(after.b, after.h);
             }
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                l[j] += __shfl_xor_sync(kFull, l[j], 1);
-                l[j] += __shfl_xor_sync(kFull, l[j], 2);
-                if (c == 0)
-                    stat[group * S::kRows + 16 * mt + 8 * j + g] = make_float2(m[j], l[j]);
+            for (int j = 0; j < NS; ++j) {
+                if constexpr (kTurned) {
+                    l[j] += __shfl_xor_sync(kFull, l[j], 4);
+                    l[j] += __shfl_xor_sync(kFull, l[j], 8);
+                    l[j] += __shfl_xor_sync(kFull, l[j], 16);
+                    l[j] *= 1.f / kF16Weight;
+                } else {
+                    l[j] += __shfl_xor_sync(kFull, l[j], 1);
+                    l[j] += __shfl_xor_sync(kFull, l[j], 2);
+                }
+                if ((kTurned ? g : c) == 0)
+                    stat[group * S::kRows + row_of(j)] = make_float2(m[j], l[j]);
             }
             __syncthreads();
-            float f[NJ];
+            float f[NS];
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
+            for (int j = 0; j < NS; ++j) {
                 float big = kNegInf;
 #pragma unroll
                 for (int w = 0; w < G; ++w)
-                    big = fmaxf(big, stat[w * S::kRows + 16 * mt + 8 * j + g].x);
+                    big = fmaxf(big, stat[w * S::kRows + row_of(j)].x);
                 f[j] = ex2(m[j] - (big == kNegInf ? 0.f : big));
             }
             const bool whole = ends && t_first == 0;
@@ -1211,24 +1409,34 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 // columns are permuted by the row so that a store's lanes hit
                 // distinct banks
 #pragma unroll
-                for (int j = 0; j < NJ; ++j) {
-                    const int r = 16 * mt + 8 * j + g;
+                for (int j = 0; j < NS; ++j) {
+                    const int r = row_of(j);
                     float *dst = mine + r * S::kRound;
+                    if constexpr (kTurned) {
+                        // tiles n and n + 1: four columns of 8 g .. 8 g + 7
+#pragma unroll
+                        for (int n = c0 / 16; n < (c0 + S::kRound) / 16; n += 2)
+                            *reinterpret_cast<float4 *>(dst + ((16 * n - c0 + 4 * g) ^ swizzle<FMT, true>(r))) =
+                                make_float4(o[n][j] * f[j], o[n][2 + j] * f[j], o[n + 1][j] * f[j],
+                                            o[n + 1][2 + j] * f[j]);
+                        continue;
+                    } else {
 #pragma unroll
                     for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += F16 ? 4 : 1) {
                         if constexpr (F16) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 *reinterpret_cast<float4 *>(
-                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT>(r))) =
+                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT, false>(r))) =
                                     make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
                                                 o[n0 + 2][2 * j + e] * f[j],
                                                 o[n0 + 3][2 * j + e] * f[j]);
                         } else {
                             *reinterpret_cast<float2 *>(
-                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT>(r))) =
+                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT, false>(r))) =
                                 make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
                         }
+                    }
                     }
                 }
                 __syncthreads();
@@ -1244,7 +1452,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         for (int w = 0; w < G; ++w) {
                             const float4 x = *reinterpret_cast<const float4 *>(
                                 free_entry + w * S::kRing +
-                                (r * S::kRound + (d ^ swizzle<FMT>(r))) * 4);
+                                (r * S::kRound + (d ^ swizzle<FMT, kTurned>(r))) * 4);
                             acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
                             big = fmaxf(big, stat[w * S::kRows + r].x);
                         }
