@@ -42,10 +42,10 @@
 // flight in the least shared memory, hence the most warps per SM.
 // Up to 8 query rows (RT = 0) the upper half of every MMA is padding: its
 // softmax is left out and its accumulators are not kept.  With an NVFP4 cache
-// the products are turned round there: tokens are the 16 rows of the first
-// (S^T = K Q^T), columns of V those of the second (O^T = V^T P^T), the query
-// rows the 8 columns, so no half is padding and no accumulator is moved in and
-// out.  The weights change places between the two by an 8 x 8 transposition of
+// the products are turned round: tokens are the 16 rows of the first
+// (S^T = K Q^T), columns of V those of the second (O^T = V^T P^T), 8 query rows
+// the columns, so no half is padding and no accumulator is moved in and out.
+// The weights change places between the two by an 8 x 8 transposition of
 // registers.
 //
 // Weights are rounded to the MMA operand type, at most 2^-8 relative for bf16
@@ -196,6 +196,13 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Four of an array of accumulators.
+template <int N>
+__device__ __forceinline__ float (&tile(float (&x)[N], int i))[4]
+{
+    return *reinterpret_cast<float(*)[4]>(x + 4 * i);
+}
+
 // The same where only rows g (NJ = 1) or rows g and g + 8 are kept.
 template <bool F16, int NJ>
 __device__ __forceinline__ void mma_rows(float (&o)[2 * NJ], const uint32_t (&a)[4], uint32_t b0,
@@ -330,7 +337,7 @@ struct Shape {
     static_assert(kTile <= 128, "lengths are limited so that a tile more fits 32 bits");
     static constexpr int kGroup = RT == 0 ? 32 : 32 * RT;  // threads
     static constexpr int kThreads = kGroup * G;
-    static constexpr bool kTurned = FMT == kFp4 && RT == 0;  // S^T and O^T
+    static constexpr bool kTurned = FMT == kFp4;  // S^T and O^T
     // Rows that one access phase touches lie on distinct banks.  bf16: the
     // 16-byte units of a row are permuted by its lowest three bits (8 rows of
     // an ldmatrix).  FP8: padded pitches (8-byte loads of 4 rows for K, 4-byte
@@ -342,7 +349,7 @@ struct Shape {
     static constexpr int kBlocks = FMT == kFp4 ? DP / 16 : 0;  // bytes per row
     static constexpr int kQPitch = DP * 2 + 16;
     static constexpr int kRows = RT == 0 ? 8 : 16 * RT;    // query rows kept
-    static constexpr int kQRows = kTurned ? 8 : RT == 0 ? 16 : 16 * RT;  // rows of the operand
+    static constexpr int kQRows = kTurned ? kRows : RT == 0 ? 16 : 16 * RT;  // rows of the operand
     // One ring entry: a chunk's keys or values; also 32 columns of the rows.
     static constexpr int kEntry = max_of(TOK * (kKPitch + kBlocks), kRows * 4 * 32);
     static_assert(FMT != kFp4 || kEntry % 128 == 0, "fp4_place() permutes within 128 bytes");
@@ -368,14 +375,15 @@ struct Shape {
 __host__ __device__ constexpr int fp4_step(int x) { return (((x >> 7) ^ (x >> 9)) & 3) << 5; }
 __device__ __forceinline__ int fp4_place(int x) { return x ^ fp4_step(x); }
 
-// The place among the joined columns of accumulator e (of a row) of column
-// tile n, and the output column there.  They are the same but for NVFP4, where
-// a lane holds eight columns of a block of 64 and a round joins four of them.
+// The output column of accumulator e (of a row) of column tile n.
 template <int FMT>
 __device__ __forceinline__ int out_col(int n, int c, int e)
 {
-    return FMT != kBf16 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
+    return FMT == kFp8 ? n / 4 * 32 + 4 * (2 * c + e) + n % 4 : 8 * n + 2 * c + e;
 }
+// The output column at place v of the joined ones.  They are the same but for
+// NVFP4, where a lane holds eight columns of a block of 64 and a round joins
+// four of each.
 template <int FMT>
 __device__ __forceinline__ int real_col(int v)
 {
@@ -383,10 +391,10 @@ __device__ __forceinline__ int real_col(int v)
 }
 
 // The permutation of a row's columns while the groups' rows are joined.
-template <int FMT, bool TURNED>
+template <int FMT>
 __device__ __forceinline__ int swizzle(int r)
 {
-    return TURNED ? (r >> 1 & 3) << 3 : FMT != kBf16 ? (r & 1) << 2 : (r & 3) << 3;
+    return FMT == kFp4 ? (r >> 1 & 3) << 3 : FMT == kFp8 ? (r & 1) << 2 : (r & 3) << 3;
 }
 
 // Where a token's row starts, found by one thread per token a chunk before the
@@ -762,8 +770,10 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     constexpr bool F16 = FMT != kBf16;   // the operands' type, else bf16
     constexpr bool kTurned = S::kTurned;
     constexpr int NJ = RT == 0 ? 1 : 2;  // row halves kept per MMA (rows g, g + 8)
-    // rows whose softmax a lane takes part in: 16 mt + 8 j + g, or turned 2 c + j
-    constexpr int NS = kTurned ? 2 : NJ;
+    // rows whose softmax a lane takes part in: 16 mt + 8 j + g, or turned two of
+    // every column tile of 8, 16 mt + 8 (j / 2) + 2 c + j % 2
+    constexpr int NQ = RT == 0 ? 1 : 2;  // column tiles
+    constexpr int NS = kTurned ? 2 * NQ : NJ;
     constexpr int kNT = DP / 8;          // MMA column tiles of the output
     constexpr int kOT = kTurned ? DP / 16 : kNT;  // its tiles
     constexpr int kSN = TOK / 8;         // MMA column tiles of the scores
@@ -830,7 +840,18 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                     big = max(big, __shfl_xor_sync(kFull, big, off));
                 int e2 = (int)(big >> 23) - 127;
                 e2 = e2 < -100 ? -100 : e2 > 127 ? 127 : e2;
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                float up = __uint_as_float((uint32_t)(127 + 14 - e2) << 23);
+                float down = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
+                if constexpr (kTurned) {
+                    // maxima are taken before the scale, which has to keep their
+                    // order: Q takes its sign, and a masked score's -inf times it
+                    // must not be NaN
+                    if (a.qk_scale < 0.f) {
+                        up = -up;
+                        down = -down;
+                    }
+                    down = fmaxf(down, 0x1p-120f);
+                }
                 if (r < S::kQRows) {
                     // place of value d in the permuted order.  FP8: block of 32, lane
                     // quarter (d / 8 % 4), step (d / 4 % 2), half (d / 2 % 2).  NVFP4:
@@ -842,7 +863,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         *reinterpret_cast<uint32_t *>(dst + 2 * (to + (e >> 1) * 16 + (e & 1) * 8)) =
                             pack2<true>(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
                     if (d == 0)
-                        row_scale[r] = a.qk_scale * __uint_as_float((uint32_t)(127 + e2 - 14) << 23);
+                        row_scale[r] = down;
                 }
             } else if (r < S::kQRows) {
                 *reinterpret_cast<uint4 *>(dst + 2 * d) = qv[i];
@@ -904,11 +925,11 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         load_values();
     }
 
-    constexpr int kOE = kTurned ? 4 : 2 * NJ;  // accumulators kept of a tile
+    constexpr int kOE = kTurned ? 4 * NQ : 2 * NJ;  // accumulators kept of a tile
     float o[kOT][kOE];
     float m[NS], l[NS];
     int sees[NS], sees_least = 0;
-    auto row_of = [&](int j) { return kTurned ? 2 * c + j : 16 * mt + 8 * j + g; };
+    auto row_of = [&](int j) { return 16 * mt + (kTurned ? 8 * (j >> 1) + 2 * c + (j & 1) : 8 * j + g); };
     auto reset = [&]() {
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -952,9 +973,9 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
 #pragma unroll
         for (int t = 0; t < kTM; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < kOE; ++e)
                 s[t][e] = 0.f;
-        const uint32_t q_row = base + S::kQ + (lane & 7) * S::kQPitch + (lane >> 3) * 16;
+        const uint32_t q_row = base + S::kQ + (16 * mt + (lane & 7)) * S::kQPitch + (lane >> 3) * 16;
         const uint32_t k_row = k_smem + fp4_place(g * S::kKPitch) + 8 * c;
         uint32_t scales[kTM][2][DP / 64];
 #pragma unroll
@@ -964,9 +985,12 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 lds_words(k_smem + TOK * S::kKPitch + (16 * t + 8 * h + g) * S::kBlocks, scales[t][h]);
 #pragma unroll
         for (int blk = 0; blk < DP / 64; ++blk) {
-            uint32_t qb[2][4];  // two steps each
-            ldsm4(qb[0], q_row + 128 * blk);
-            ldsm4(qb[1], q_row + 128 * blk + 64);
+            uint32_t qb[NQ][2][4];  // two steps each
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                ldsm4(qb[q][0], q_row + 8 * q * S::kQPitch + 128 * blk);
+                ldsm4(qb[q][1], q_row + 8 * q * S::kQPitch + 128 * blk + 64);
+            }
 #pragma unroll
             for (int t = 0; t < kTM; ++t) {
                 uint32_t f[2][2][4];  // token half, word, pair of codes
@@ -987,34 +1011,39 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 for (int j = 0; j < 4; ++j) {
                     const int w = j / 2, i = 2 * (j & 1);
                     const uint32_t ka[4] = {f[0][w][i], f[1][w][i], f[0][w][i + 1], f[1][w][i + 1]};
-                    mma16<true>(s[t], ka, qb[w][i], qb[w][i + 1]);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+                        mma16<true>(tile(s[t], q), ka, qb[q][w][i], qb[q][w][i + 1]);
                 }
             }
         }
-        float big[2] = {kNegInf, kNegInf};
-        const float2 sc = *reinterpret_cast<const float2 *>(row_scale + 2 * c);
-#pragma unroll
-        for (int t = 0; t < kTM; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[t][e] *= e & 1 ? sc.y : sc.x;
+        // accumulator 4 q + e: token 16 t + 8 (e / 2) + g, row 2 q + e % 2 of the lane's
         if (pos0 + TOK > sees_least) {  // some position is masked for some row
 #pragma unroll
             for (int t = 0; t < kTM; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (pos0 + 16 * t + 8 * (e >> 1) + g >= sees[e & 1])
+                for (int e = 0; e < kOE; ++e)
+                    if (pos0 + 16 * t + 8 * (e >> 1 & 1) + g >= sees[2 * (e >> 2) + (e & 1)])
                         s[t][e] = kNegInf;
         }
+        float big[NS], sc[NS];
+        bool raised = false;
 #pragma unroll
-        for (int t = 0; t < kTM; ++t)
+        for (int j = 0; j < NS; ++j) {
+            sc[j] = row_scale[row_of(j)];
+            big[j] = kNegInf;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                big[e & 1] = fmaxf(big[e & 1], s[t][e]);
-        if (__any_sync(kFull, big[0] > m[0] || big[1] > m[1])) {
-            float alpha[2];
+            for (int t = 0; t < kTM; ++t)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+                for (int h = 0; h < 2; ++h)
+                    big[j] = fmaxf(big[j], s[t][4 * (j >> 1) + 2 * h + (j & 1)]);
+            big[j] *= sc[j];
+            raised |= big[j] > m[j];
+        }
+        if (__any_sync(kFull, raised)) {
+            float alpha[NS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
                 big[j] = fmaxf(big[j], m[j]);
                 big[j] = fmaxf(big[j], __shfl_xor_sync(kFull, big[j], 4));
                 big[j] = fmaxf(big[j], __shfl_xor_sync(kFull, big[j], 8));
@@ -1027,22 +1056,23 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
             for (int n = 0; n < kOT; ++n)
 #pragma unroll
                 for (int e = 0; e < kOE; ++e)
-                    o[n][e] *= alpha[e & 1];
+                    o[n][e] *= alpha[2 * (e >> 2) + (e & 1)];
         }
-        float ref[2];
+        float up[NS];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            ref[j] = m[j] == kNegInf ? 0.f : m[j] - 15.f;
+        for (int j = 0; j < NS; ++j)
+            up[j] = m[j] == kNegInf ? 0.f : 15.f - m[j];
 #pragma unroll
         for (int t = 0; t < kTM; ++t) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[t][e] = ex2(s[t][e] - ref[e & 1]);
-                l[e & 1] += s[t][e];
+            for (int e = 0; e < kOE; ++e) {
+                const int j = 2 * (e >> 2) + (e & 1);
+                s[t][e] = ex2(fmaf(s[t][e], sc[j], up[j]));
+                l[j] += s[t][e];
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                pa[t][h] = transpose8(pack2<true>(s[t][2 * h], s[t][2 * h + 1]));
+            for (int i = 0; i < 2 * NQ; ++i)
+                pa[t][i] = transpose8(pack2<true>(s[t][2 * i], s[t][2 * i + 1]));
         }
     };
     bool first_part = true;  // still in the block's first (sequence, head)
@@ -1057,8 +1087,8 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         load_keys();  // into the entry of the previous values
         const uint32_t k_smem = ring + entry * S::kEntry;
         entry = entry + 1 == S::kEntries ? 0 : entry + 1;
-        uint32_t pa[TOK / 16][kTurned ? 2 : 4];  // the weights as the second product's operand
-        float s[kTurned ? TOK / 16 : kSN][kTurned ? 4 : 2 * NJ];
+        uint32_t pa[TOK / 16][kTurned ? 2 * NQ : 4];  // the weights as the second product's operand
+        float s[kTurned ? TOK / 16 : kSN][kTurned ? 4 * NQ : 2 * NJ];
         if constexpr (kTurned) {
             if (pos0 < cur.len) {
                 turned_weights(k_smem, pos0, s, pa);
@@ -1073,32 +1103,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                     acc[n][e] = 0.f;
             const uint32_t q_row =
                 base + S::kQ + (16 * mt + (lane & 15)) * S::kQPitch + (lane >> 4) * 16;
-            if constexpr (FMT == kFp4) {
-                // lane (g, c): token g of every eight, group c of every block of
-                // 64 values: 8 bytes of codes and one scale, four steps' operands
-                const uint32_t k_row = k_smem + fp4_place(g * S::kKPitch) + 8 * c;
-#pragma unroll
-                for (int n = 0; n < kSN; ++n) {
-                    uint32_t scales[DP / 64];
-                    lds_words(k_smem + TOK * S::kKPitch + (8 * n + g) * S::kBlocks, scales);
-#pragma unroll
-                    for (int blk = 0; blk < DP / 64; ++blk) {
-                        const uint2 x = lds64((k_row ^ (fp4_step(8 * n * S::kKPitch) ^ blk << 5)) +
-                                              8 * n * S::kKPitch);
-                        const uint32_t sc = e4m3x2_f16x2((uint16_t)__byte_perm(scales[blk], 0, c * 0x11));
-                        uint32_t f[2][4];
-                        e2m1x8_f16x8(x.x, f[0]);
-                        e2m1x8_f16x8(x.y, f[1]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t qa[4];
-                            ldsm4(qa, q_row + (64 * blk + 16 * j) * 2);
-                            mma16<true>(acc[n], qa, mul_f16x2(f[j / 2][2 * (j & 1)], sc),
-                                        mul_f16x2(f[j / 2][2 * (j & 1) + 1], sc));
-                        }
-                    }
-                }
-            } else if constexpr (FMT == kFp8) {
+            if constexpr (FMT == kFp8) {
                 const uint32_t k_row = k_smem + g * S::kKPitch + 8 * c;
 #pragma unroll
                 for (int d = 0; d < DP; d += 32) {
@@ -1221,9 +1226,10 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                     if constexpr (kTurned) {
 #pragma unroll
                         for (int j = 0; j < NS; ++j) {
-                            float mine = tok & 8 ? s[0][2 + j] : s[0][j];
+                            const int at = 4 * (j >> 1) + (j & 1);
+                            float mine = tok & 8 ? s[0][at + 2] : s[0][at];
                             if constexpr (TOK == 32)
-                                mine = tok & 16 ? (tok & 8 ? s[1][2 + j] : s[1][j]) : mine;
+                                mine = tok & 16 ? (tok & 8 ? s[1][at + 2] : s[1][at]) : mine;
                             w[j] = __shfl_sync(kFull, mine, (tok & 7) * 4 + c);
                         }
 #pragma unroll
@@ -1234,7 +1240,8 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
 #pragma unroll
                                 for (int j = 0; j < NS; ++j)
                                     if (pos0 + tok < sees[j])
-                                        o[n][2 * e + j] = fmaf(w[j], v, o[n][2 * e + j]);
+                                        o[n][4 * (j >> 1) + 2 * e + (j & 1)] =
+                                            fmaf(w[j], v, o[n][4 * (j >> 1) + 2 * e + (j & 1)]);
                             }
                         continue;
                     } else {
@@ -1254,11 +1261,9 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                     for (int n = 0; n < kNT; ++n)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int d = real_col<FMT>(out_col<FMT>(n, c, e));
+                            const int d = out_col<FMT>(n, c, e);
                             float v;
-                            if constexpr (FMT == kFp4)
-                                v = fp4_value(v_smem, tok, d);
-                            else if constexpr (FMT == kFp8)
+                            if constexpr (FMT == kFp8)
                                 v = unpack1<true>((uint16_t)e4m3x2_f16x2(
                                     lds8(v_smem + tok * S::kVPitch + d)));
                             else
@@ -1285,10 +1290,9 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
             for (int k = 0; k < TOK / 16; ++k) {
                 if constexpr (FMT == kFp4) {
                     // lane (g, c): tokens 2c, 2c + 1, 2c + 8, 2c + 9, columns
-                    // 8 g .. 8 g + 7 of each block of 64; column tile j of a
-                    // block is columns 8 n + j, or turned, row tile j columns
-                    // 8 n + 2 j and 8 n + 2 j + 1.  The codes of two tokens are
-                    // paired before they are widened, so that a byte holds both.
+                    // 8 g .. 8 g + 7 of each block of 64; row tile j of a block is
+                    // columns 8 n + 2 j and 8 n + 2 j + 1.  The codes of two tokens
+                    // are paired before they are widened, so that a byte holds both.
                     const uint32_t v_row[2] = {v_smem + fp4_place(2 * c * S::kVPitch) + 4 * g,
                                                v_smem + fp4_place((2 * c + 1) * S::kVPitch) + 4 * g};
                     uint32_t scales[2][2][DP / 64];
@@ -1316,17 +1320,12 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                                 x[q][1][j] = mul_f16x2(x[q][1][j], sc);
                             }
                         }
-                        if constexpr (kTurned) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t va[4] = {x[0][0][j], x[0][1][j], x[1][0][j], x[1][1][j]};
-                                mma16<true>(o[4 * blk + j], va, pa[k][0], pa[k][1]);
-                            }
-                        } else {
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t va[4] = {x[0][0][j], x[0][1][j], x[1][0][j], x[1][1][j]};
 #pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                mma_rows<true, NJ>(o[8 * blk + j], pa[k], x[0][j & 1][j / 2],
-                                                   x[1][j & 1][j / 2]);
+                            for (int q = 0; q < NQ; ++q)
+                                mma16<true>(tile(o[4 * blk + j], q), va, pa[k][2 * q], pa[k][2 * q + 1]);
                         }
                     }
                 } else if constexpr (FMT == kFp8) {
@@ -1416,9 +1415,11 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         // tiles n and n + 1: four columns of 8 g .. 8 g + 7
 #pragma unroll
                         for (int n = c0 / 16; n < (c0 + S::kRound) / 16; n += 2)
-                            *reinterpret_cast<float4 *>(dst + ((16 * n - c0 + 4 * g) ^ swizzle<FMT, true>(r))) =
-                                make_float4(o[n][j] * f[j], o[n][2 + j] * f[j], o[n + 1][j] * f[j],
-                                            o[n + 1][2 + j] * f[j]);
+                            *reinterpret_cast<float4 *>(dst + ((16 * n - c0 + 4 * g) ^ swizzle<FMT>(r))) =
+                                make_float4(o[n][4 * (j >> 1) + (j & 1)] * f[j],
+                                            o[n][4 * (j >> 1) + 2 + (j & 1)] * f[j],
+                                            o[n + 1][4 * (j >> 1) + (j & 1)] * f[j],
+                                            o[n + 1][4 * (j >> 1) + 2 + (j & 1)] * f[j]);
                         continue;
                     } else {
 #pragma unroll
@@ -1427,13 +1428,13 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
                                 *reinterpret_cast<float4 *>(
-                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT, false>(r))) =
+                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT>(r))) =
                                     make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
                                                 o[n0 + 2][2 * j + e] * f[j],
                                                 o[n0 + 3][2 * j + e] * f[j]);
                         } else {
                             *reinterpret_cast<float2 *>(
-                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT, false>(r))) =
+                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT>(r))) =
                                 make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
                         }
                     }
@@ -1452,7 +1453,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         for (int w = 0; w < G; ++w) {
                             const float4 x = *reinterpret_cast<const float4 *>(
                                 free_entry + w * S::kRing +
-                                (r * S::kRound + (d ^ swizzle<FMT, kTurned>(r))) * 4);
+                                (r * S::kRound + (d ^ swizzle<FMT>(r))) * 4);
                             acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
                             big = fmaxf(big, stat[w * S::kRows + r].x);
                         }
