@@ -405,36 +405,31 @@ struct RowAddress {
     int id;         // page id, not yet checked
     bool has;       // a cached token
 
+    // (Straight-line code: what depends on `has` is chosen, not branched
+    // around, and a bad page is reported once, at the block's end.)
     template <int TILE>
     __device__ __forceinline__ void fetch(const AttnArgs &a, const Cursor<TILE> &it, int r)
     {
         const int pos = it.t * TILE + r;
         has = it.b < a.B && pos < it.len;
-        if (!has)
-            return;
         const int page = a.page_of(pos);
-        id = __ldg(a.table + it.b * a.table_stride + page);
+        id = 0;
+        if (has)
+            id = __ldg(a.table + it.b * a.table_stride + page);
         const uint32_t slot = pos - page * a.page_size;
-        k = slot * a.kt + it.h * a.kh;
-        v = slot * a.vt + it.h * a.vh;
+        k = has ? slot * a.kt + it.h * a.kh : 0u;
+        v = has ? slot * a.vt + it.h * a.vh : 0u;
     }
     // The row's addresses.  A page outside the pool is reported, and read as
     // page 0; past the length nothing is read through the address.
-    __device__ __forceinline__ void resolve(const AttnArgs &a, const unsigned char **rows,
-                                            int tok) const
+    __device__ __forceinline__ void resolve(const AttnArgs &a, const unsigned char **rows, int tok,
+                                            bool &bad) const
     {
-        const unsigned char *pk = a.k, *pv = a.v;
-        if (has) {
-            int page = id;
-            if ((unsigned)page >= (unsigned)a.pages) {
-                set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
-                page = 0;
-            }
-            pk += page * a.kp + k;
-            pv += page * a.vp + v;
-        }
-        rows[0] = pk;
-        rows[tok] = pv;
+        const bool in = (unsigned)id < (unsigned)a.pages;
+        bad |= !in;
+        const int page = in ? id : 0;
+        rows[0] = a.k + page * a.kp + k;
+        rows[tok] = a.v + page * a.vp + v;
     }
 };
 
@@ -884,6 +879,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     Cursor<S::kTile> ahead = cur;  // of the row addresses
     Cursor<S::kTile> load = cur;   // of the copies
     const bool finds = at < TOK;
+    bool bad_page = false;
     if (finds) {
         RowAddress first[P + 1];
 #pragma unroll
@@ -895,7 +891,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         ahead.next(a);
 #pragma unroll
         for (int i = 0; i < P + 1; ++i)
-            first[i].resolve(a, addr + i * 2 * TOK + at, TOK);
+            first[i].resolve(a, addr + i * 2 * TOK + at, TOK, bad_page);
     }
     group_sync<kGroup>(group);
     int64_t to_load = n_units;
@@ -1210,7 +1206,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         group_sync<kGroup>(group);
         load_values();  // into the entry of these keys
         if (finds) {    // the chunk after: its addresses are read after the next barrier
-            row.resolve(a, addr + load_slot * 2 * TOK + at, TOK);
+            row.resolve(a, addr + load_slot * 2 * TOK + at, TOK, bad_page);
             row.fetch(a, ahead, TOK * group + at);
             ahead.next(a);
         }
@@ -1492,6 +1488,8 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         }
         cur.next(a);
     }
+    if (bad_page)
+        set_status(a.ws, 1u << DVL_ERR_OUT_OF_RANGE);
     write_empty<kThreads>(a);
 }
 
