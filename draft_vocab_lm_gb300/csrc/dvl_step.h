@@ -49,7 +49,10 @@ struct ReorderArgs {
     // the partly filled pages (pages.table == nullptr: none)
     dvl_beam_pages pages;
     dvl_kv_cache cache;
-    int elem4;                          // half bytes per cached value
+    struct {
+        int64_t page, token, head;
+    } strides[2];                       // of keys and values, in bytes
+    int head_bytes;                     // of one head of one token
     int page_pieces, block_pieces;      // per new beam, keys and values each: of the
                                         // rows, of an NVFP4 cache's scales
 };

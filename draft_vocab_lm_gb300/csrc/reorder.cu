@@ -71,10 +71,10 @@ __device__ __forceinline__ void copy_table(const ReorderArgs &a, const ReorderIt
 }
 
 // Piece `blk` of the pages of new beam r: keys, then values, of the rows; of an
-// NVFP4 cache then those of the scales, which lie as the rows do, in an eighth
-// of the room, 4 bytes at a time.
-template <typename U>
-__device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int pieces, bool scales)
+// NVFP4 cache also of their scales, which lie as the rows do, in an eighth of
+// the room, 4 bytes at a time.
+template <typename U, bool SCALES>
+__device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int pieces)
 {
     const dvl_kv_cache &c = a.cache;
     const int64_t r = blk / (2 * pieces);
@@ -85,8 +85,8 @@ __device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int
         return;
     const int length = max(a.pages.lengths[from], 0);
     const int slot = length / c.page_size;
-    const int shift = scales ? 4 : 1;  // half bytes to bytes, of the scales eight times fewer
-    const int units = (c.D * a.elem4 >> shift) / (int)sizeof(U);  // of one head of one token
+    constexpr int kDown = SCALES ? 3 : 0;
+    const int units = (a.head_bytes >> kDown) / (int)sizeof(U);  // of one head of one token
     const int total = length % c.page_size * c.heads * units;
     const int u0 = (piece - (values ? pieces : 0)) * (kThreads * kLoads);
     if (u0 >= total || slot >= a.pages.width)
@@ -95,13 +95,14 @@ __device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int
     const int dst_page = a.pages.spare[r];
     if ((unsigned)src_page >= (unsigned)c.pages || (unsigned)dst_page >= (unsigned)c.pages)
         return;
-    const int64_t ps = (values ? c.v_page_stride : c.k_page_stride) * a.elem4 >> shift;
-    const int64_t ts = (values ? c.v_token_stride : c.k_token_stride) * a.elem4 >> shift;
-    const int64_t hs = (values ? c.v_head_stride : c.k_head_stride) * a.elem4 >> shift;
+    const int64_t ps = a.strides[values].page >> kDown;
+    // (offsets within a page are below 2^31)
+    const uint32_t ts = (uint32_t)(a.strides[values].token >> kDown);
+    const uint32_t hs = (uint32_t)(a.strides[values].head >> kDown);
     unsigned char *base = static_cast<unsigned char *>(
-        scales ? (values ? c.v_blocks : c.k_blocks) : (values ? c.v : c.k));
+        SCALES ? (values ? c.v_blocks : c.k_blocks) : (values ? c.v : c.k));
     U v[kLoads];
-    int64_t at[kLoads];
+    uint32_t at[kLoads];
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
         const int u = u0 + (int)threadIdx.x + j * kThreads;
@@ -118,17 +119,25 @@ __device__ __forceinline__ void copy_page(const ReorderArgs &a, int64_t blk, int
             *reinterpret_cast<U *>(base + dst_page * ps + at[j]) = v[j];
 }
 
-__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const __grid_constant__ ReorderArgs a)
+// FOUR: the cache is NVFP4.  (Copies live from the threads an SM holds: 32
+// registers let it hold all 2,048; at 36, 128 rows of 517 KB took 2 % longer,
+// with the scales' code in the same kernel 4 %.)
+template <bool FOUR>
+__global__ void __launch_bounds__(kThreads, 8) beam_reorder_kernel(const __grid_constant__ ReorderArgs a)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int64_t blk = blockIdx.x;
     if (blk >= a.copy_blocks) {
-        const int64_t rows = (int64_t)a.batch * a.k * 2 * a.page_pieces;
-        if (blk - a.copy_blocks < rows)
-            copy_page<uint4>(a, blk - a.copy_blocks, a.page_pieces, false);
-        else
-            copy_page<uint32_t>(a, blk - a.copy_blocks - rows, a.block_pieces, true);
+        const int64_t at = blk - a.copy_blocks;
+        if constexpr (FOUR) {
+            const int64_t rows = (int64_t)a.batch * a.k * 2 * a.page_pieces;
+            if (at >= rows) {
+                copy_page<uint32_t, true>(a, at - rows, a.block_pieces);
+                return;
+            }
+        }
+        copy_page<uint4, false>(a, at, a.page_pieces);
         return;
     }
     int i = a.n_items - 1;
@@ -158,7 +167,7 @@ cudaError_t launch_beam_reorder(ReorderArgs &a, cudaStream_t s)
     a.copy_blocks = blocks;
     a.page_pieces = a.block_pieces = 0;
     if (a.pages.table) {
-        const int64_t bytes = (int64_t)(a.cache.page_size - 1) * a.cache.heads * a.cache.D * a.elem4 / 2;
+        const int64_t bytes = (int64_t)(a.cache.page_size - 1) * a.cache.heads * a.head_bytes;
         a.page_pieces = (int)((bytes + kPiece - 1) / kPiece);
         if (a.cache.dtype == DVL_NVFP4)
             a.block_pieces = (int)((bytes / 8 + kPiece / 4 - 1) / (kPiece / 4));
@@ -168,7 +177,7 @@ cudaError_t launch_beam_reorder(ReorderArgs &a, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     if (blocks == 0)
         return cudaSuccess;
-    return launch_pdl(beam_reorder_kernel, (unsigned)blocks, kThreads, 0, s, a);
+    return launch_pdl(a.block_pieces ? beam_reorder_kernel<true> : beam_reorder_kernel<false>, (unsigned)blocks, kThreads, 0, s, a);
 }
 
 }  // namespace dvl

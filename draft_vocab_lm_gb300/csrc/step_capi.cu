@@ -392,8 +392,13 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
             !aligned(pages->lengths, 4) || !aligned(pages->lengths_out, 4) ||
             !aligned(pages->spare, 4))
             return DVL_ERR_INVALID_ARG;
-        a.elem4 = half_bytes(cache);
-        if ((int64_t)cache->page_size * cache->heads * cache->D * a.elem4 / 2 > 0x7fffffffLL ||
+        const int64_t half = half_bytes(cache);
+        a.head_bytes = (int)(cache->D * half / 2);
+        a.strides[0] = {cache->k_page_stride * half / 2, cache->k_token_stride * half / 2,
+                        cache->k_head_stride * half / 2};
+        a.strides[1] = {cache->v_page_stride * half / 2, cache->v_token_stride * half / 2,
+                        cache->v_head_stride * half / 2};
+        if ((int64_t)cache->page_size * cache->heads * a.head_bytes > 0x7fffffffLL ||
             (int64_t)pages->width * 4 > 0x7fffffffLL)
             return DVL_ERR_INVALID_ARG;
         a.pages = *pages;
