@@ -7,13 +7,26 @@
 // each, so many rows are bound by HBM and a few by the chain of dependent
 // loads (sequence -> length -> page -> store).
 //
-// Split.  A head takes D / 8 lanes (rounded up to a power of two), 8 values
-// each: the sum of squares is a butterfly over them and the other half of a
-// pair (rot / 2 values away) lies in another lane's register.  A warp walks
-// heads of ONE row, queries, then keys, then values, because a lane's cos and
-// sin depend on the row and on its place in the head alone: computed once,
-// they serve all of the row's heads.  Where rows are few, several warps share
-// a row's heads, each with its own cos and sin.
+// Split.  A head takes D / 16 lanes (rounded up to a power of two), two chunks
+// of 8 values each: of the rotated ones a chunk and the one rot / 2 values on,
+// so that both values of every pair are in one lane (of the others one of each
+// half of them: 16 bytes of neighbouring lanes are neighbours), and the sum of
+// squares is a butterfly over the lanes.  (One chunk to a lane, the pair's
+// other half fetched by shuffles, took 62 million warp instructions against 47
+// for 16,381 rows of 40 + 2 x 8 heads of 128.)  A warp walks heads of ONE row,
+// queries, then keys, then values, because a lane's cos and sin depend on the
+// row and on its place in the head alone: computed once, they serve all of the
+// row's heads.  Where rows are few, several warps share a row's heads, each
+// with its own cos and sin, up to 16 warps an SM.
+//
+// Measured (GB300, wall time a call back to back): those 16,381 rows, bf16, 82
+// us (460 MB, 0.83 of the copy rate; 75 with the arithmetic left out); 192 rows
+// to an E4M3 cache 4.4 us; one row 3.1, the host's side of the call.  8,191 rows
+// of 16 + 2 x 2 heads of 256, a quarter rotated, E4M3, no norm: 37 us (0.62; a
+// row is four trips to memory there, and its end and the next row's start are
+// not overlapped within a warp; with one chunk to a lane 33).  Equal or slower:
+// 3 or 5 blocks an SM, two warps a row, loads of the next step before a step's
+// arithmetic, rows looked up 32 at a time.
 //
 // Angles.  freq is in turns per position, as a 64-bit fraction, so position x
 // freq modulo one turn is an integer product that wraps: its upper 32 bits are
@@ -30,7 +43,8 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kLoads = 4;  // 16-byte loads in flight per lane
+constexpr int kBlocks = 4;  // per SM: 128 registers a thread
+constexpr int kLoads = 5;  // steps whose values a lane has in flight, 32 bytes each
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
@@ -111,53 +125,97 @@ __device__ __forceinline__ bool find_sequence(const QkArgs &a, int64_t r, int la
     return r < *end && r >= a.starts[lo];
 }
 
-// Eight values of a head, `live` ones, in the cache's type.
+// A lane's place in a head: its two chunks of 8 values, and for NVFP4 where the
+// other halves of their groups of 16 are: the lane, and which of its chunks.
+struct Chunks {
+    int first, second;
+    bool live;
+    int lane[2];
+    bool of_second[2];
+};
+template <int LPH>
+__device__ __forceinline__ Chunks chunks_of(int D, int rot, int lane)
+{
+    const int l = lane % LPH, turned = rot / 16;  // lanes with pairs
+    Chunks c;
+    c.live = 16 * l < D;
+    const int rest = D / 16 - turned;  // lanes without
+    c.first = l < turned ? l : turned + l;
+    c.second = c.first + (l < turned ? turned : rest);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int mate = (i ? c.second : c.first) ^ 1;
+        const bool pairs = mate < 2 * turned;
+        const int half = pairs ? turned : rest, at = pairs ? mate : mate - 2 * turned;
+        c.of_second[i] = at >= half;
+        c.lane[i] = c.live ? lane - l + (pairs ? 0 : turned) + (c.of_second[i] ? at - half : at) : lane;
+    }
+    return c;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
+{
+    return e4m3x2(a, b) | (uint32_t)e4m3x2(c, d) << 16;
+}
+
+// A lane's sixteen values of a head in the cache's type.
 // at: the place of the row's head in the pool, in bytes (of NVFP4: of codes).
 __device__ __forceinline__ void to_cache(const QkArgs &a, unsigned char *pool, unsigned char *blocks,
-                                         int64_t at, int l, bool put, const float (&y)[8],
+                                         int64_t at, const Chunks &c, bool put, const float (&y)[2][8],
                                          float inv_scale, float scale)
 {
+    const int chunk[2] = {c.first, c.second};
     if (a.dtype == DVL_BF16) {
-        if (put)
-            *reinterpret_cast<uint4 *>(pool + at + 16 * l) = pack8(y);
+        if (put) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint4 *>(pool + at + 16 * chunk[i]) = pack8(y[i]);
+        }
     } else if (a.dtype == DVL_FP8) {
-        uint32_t w[2];
+        if (put) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                *reinterpret_cast<uint2 *>(pool + at + 8 * chunk[i]) = make_uint2(
+                    e4m3x4(y[i][0] * inv_scale, y[i][1] * inv_scale, y[i][2] * inv_scale, y[i][3] * inv_scale),
+                    e4m3x4(y[i][4] * inv_scale, y[i][5] * inv_scale, y[i][6] * inv_scale, y[i][7] * inv_scale));
+        }
+    } else {
+        // a NaN's bits are above every number's, so a maximum of bits keeps it
+        uint32_t big[2] = {0u, 0u};
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            w[i] = e4m3x2(y[4 * i] * inv_scale, y[4 * i + 1] * inv_scale) |
-                   (uint32_t)e4m3x2(y[4 * i + 2] * inv_scale, y[4 * i + 3] * inv_scale) << 16;
-        if (put)
-            *reinterpret_cast<uint2 *>(pool + at + 8 * l) = make_uint2(w[0], w[1]);
-    } else {
-        float big = 0.f;
-        bool nan = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            big = fmaxf(big, fabsf(y[e]));
-            nan |= y[e] != y[e];
+            for (int e = 0; e < 8; ++e)
+                big[i] = max(big[i], __float_as_uint(y[i][e]) & 0x7fffffffu);
+        uint32_t mate[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t x0 = __shfl_sync(kFull, big[0], c.lane[i]);
+            const uint32_t x1 = __shfl_sync(kFull, big[1], c.lane[i]);
+            mate[i] = c.of_second[i] ? x1 : x0;
         }
-        // 16 values are two lanes'
-        big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
-        nan = __shfl_xor_sync(kFull, (int)nan, 1) | (int)nan;
-        const uint16_t s = nan ? 0x7f : e4m3x2(big * (inv_scale * (1.f / 6.f)), 0.f) & 0xff;
-        const float unit = e4m3_value(s) * scale;
-        const float inv = s == 0 ? 0.f : 1.f / unit;
-        float z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            z[e] = s == 0 ? 0.f : y[e] * inv;
-        const uint32_t w = e2m1x8(z);
-        if (put) {
-            *reinterpret_cast<uint32_t *>(pool + at + 4 * l) = w;
-            if ((l & 1) == 0)
-                blocks[(at >> 3) + (l >> 1)] = (unsigned char)s;
+        for (int i = 0; i < 2; ++i) {
+            const float m = __uint_as_float(max(big[i], mate[i]));
+            const uint16_t s = e4m3x2(m * (inv_scale * (1.f / 6.f)), 0.f) & 0xff;  // NaN stays NaN
+            const float inv = s == 0 ? 0.f : 1.f / (e4m3_value(s) * scale);
+            float z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                z[e] = s == 0 ? 0.f : y[i][e] * inv;
+            const uint32_t w = e2m1x8(z);
+            if (put) {
+                *reinterpret_cast<uint32_t *>(pool + at + 4 * chunk[i]) = w;
+                if ((chunk[i] & 1) == 0)
+                    blocks[(at >> 3) + (chunk[i] >> 1)] = (unsigned char)s;
+            }
         }
     }
 }
 
 // PAIRS: the other value of a pair is its neighbour, not rot / 2 away.
 template <int LPH, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 5) qk_kernel(const __grid_constant__ QkArgs a)
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_kernel(const __grid_constant__ QkArgs a)
 {
     constexpr int kHeads = 32 / LPH;  // heads of a warp's step
     pdl_launch_dependents();
@@ -168,13 +226,32 @@ __global__ void __launch_bounds__(kThreads, 5) qk_kernel(const __grid_constant__
     const int part = (int)(unit - row * a.parts);
     if (row >= a.rows)
         return;
-    const int sub = lane / LPH, l = lane % LPH, d = 8 * l;
-    const bool live = d < a.D;
+    const int sub = lane / LPH;
+    const Chunks c = chunks_of<LPH>(a.D, a.rot, lane);
+    const bool turned = 16 * (lane % LPH) < a.rot;
 
     // the steps of a row: queries, keys, values, kHeads heads each
     const int nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.H + kHeads - 1) / kHeads;
     const int steps = nq + (a.dtype >= 0 ? 2 * nk : nk);
     const int from = (int)((int64_t)steps * part / a.parts), to = (int)((int64_t)steps * (part + 1) / a.parts);
+
+    // the first heads' values are on their way while the row's place is found
+    uint4 x[kLoads][2];
+    auto load = [&](int i, int last, int heads, const uint16_t *at, int64_t stride) {
+        const int head = i * kHeads + sub;
+        at += head * stride;
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+            if (i + u < last && c.live && head + u * kHeads < heads) {
+                x[u][0] = *reinterpret_cast<const uint4 *>(at + 8 * c.first);
+                x[u][1] = *reinterpret_cast<const uint4 *>(at + 8 * c.second);
+            }
+            at += kHeads * stride;
+        }
+    };
+    if (from < nq)
+        load(from, min(to, nq), a.Hq, a.q + row * a.qs, a.qh);
 
     // place in the sequence and in the cache
     int position = 0;
@@ -198,145 +275,124 @@ __global__ void __launch_bounds__(kThreads, 5) qk_kernel(const __grid_constant__
     if (a.positions)
         position = a.positions[row];
 
-    // cos and sin of the lane's values; the partner's sign goes with the sine
-    const int half = a.rot / 2;
-    const bool turned = d < a.rot;
+    // cos and sin of the lane's eight pairs; values that are not rotated keep
+    // 1 and 0
     float cs[8], sn[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         cs[e] = 1.f;
         sn[e] = 0.f;
-    }
-    if (turned) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (PAIRS && (e & 1)) {
-                cs[e] = cs[e - 1];
-                sn[e] = -sn[e - 1];
-                continue;
-            }
-            const int j = PAIRS ? (d + e) / 2 : d < half ? d + e : d + e - half;
-            const uint64_t turns = (uint64_t)(int64_t)position * __ldg(a.freq + j);
+        if (turned) {
+            const int pair = PAIRS ? 4 * (e < 4 ? c.first : c.second) + (e & 3) : 8 * c.first + e;
+            const uint64_t turns = (uint64_t)(int64_t)position * __ldg(a.freq + pair);
             constexpr float kTurn = 6.283185307179586f / 4294967296.f;
-            float s, c;
-            __sincosf((float)(int32_t)(turns >> 32) * kTurn, &s, &c);
-            cs[e] = c;
-            sn[e] = PAIRS || d < half ? -s : s;
+            __sincosf((float)(int32_t)(turns >> 32) * kTurn, &sn[e], &cs[e]);
         }
     }
-    const int partner = PAIRS || !turned ? lane : d < half ? lane + half / 8 : lane - half / 8;
-    // a value that is not rotated meets no other (0 times an infinity is no 0)
-    const uint32_t meets = turned ? 0xffffffffu : 0u;
-    auto others = [&](const uint4 &x, const float (&own)[8], float (&other)[8]) {
-        if constexpr (PAIRS) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                other[e] = turned ? own[e ^ 1] : 0.f;
-        } else {
-            uint4 o;
-            o.x = __shfl_sync(kFull, x.x, partner) & meets;
-            o.y = __shfl_sync(kFull, x.y, partner) & meets;
-            o.z = __shfl_sync(kFull, x.z, partner) & meets;
-            o.w = __shfl_sync(kFull, x.w, partner) & meets;
-            unpack8(o, other);
-        }
-    };
 
-    // Queries, then keys: the heads of steps [first, last) of `heads`.  Each
-    // value is (x A + partner B) / rms, with the weights in A and B.
+    // Queries, then keys: the heads of steps [first, last) of `heads`.  With the
+    // weights in them, a pair's four coefficients are A and B:
+    //   y1 = (x1 A1 + x2 B1) / rms,  y2 = (x2 A2 + x1 B2) / rms.
     const float per = 1.f / (float)a.D;
-    auto normed = [&](int first, int last, int heads, const uint16_t *from, int64_t stride,
+    auto normed = [&](bool loaded, int first, int last, int heads, const uint16_t *from, int64_t stride,
                       const uint16_t *weight, auto &&store) {
-        float A[8], B[8];
-        if (weight) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live)
-                w = __ldg(reinterpret_cast<const uint4 *>(weight + d));
-            float own[8], other[8];
-            unpack8(w, own);
-            others(w, own, other);
+        float A[2][8], B[2][8];
+        {
+            float w[2][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                A[e] = own[e] * cs[e];
-                B[e] = other[e] * sn[e];
+            for (int i = 0; i < 2; ++i) {
+                uint4 p = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // ones
+                if (weight && c.live)
+                    p = __ldg(reinterpret_cast<const uint4 *>(weight) + (i ? c.second : c.first));
+                unpack8(p, w[i]);
             }
-        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                A[e] = cs[e];
-                B[e] = sn[e];
-            }
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // the pair, and whether this is its second value
+                    const int pair = PAIRS ? 4 * i + e / 2 : e;
+                    const bool second = PAIRS ? e & 1 : i;
+                    const float other = PAIRS ? w[i][e ^ 1] : w[1 - i][e];
+                    A[i][e] = w[i][e] * cs[pair];
+                    B[i][e] = other * (second ? sn[pair] : -sn[pair]);
+                }
         }
         int head = first * kHeads + sub;
-        const uint16_t *at = from + head * stride + d;
         for (int i = first; i < last; i += kLoads) {
-            uint4 x[kLoads];
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (i + u < last && live && head + u * kHeads < heads)
-                    x[u] = *reinterpret_cast<const uint4 *>(at);
-                at += kHeads * stride;
-            }
+            if (!loaded)
+                load(i, last, heads, from, stride);
+            loaded = false;
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 if (i + u >= last)
                     break;
-                float y[8], p[8];
-                unpack8(x[u], y);
-                others(x[u], y, p);
+                float v[2][8], y[2][8];
+                unpack8(x[u][0], v[0]);
+                unpack8(x[u][1], v[1]);
                 float inv = 1.f;
                 if (weight) {
-                    float sum = 0.f;
+                    float sum[2] = {0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum = fmaf(y[e], y[e], sum);
+                    for (int e = 0; e < 8; ++e) {
+                        sum[0] = fmaf(v[0][e], v[0][e], sum[0]);
+                        sum[1] = fmaf(v[1][e], v[1][e], sum[1]);
+                    }
+                    sum[0] += sum[1];
 #pragma unroll
                     for (int off = LPH / 2; off >= 1; off >>= 1)
-                        sum += __shfl_xor_sync(kFull, sum, off);
-                    inv = rsqrtf(fmaf(sum, per, a.eps));
+                        sum[0] += __shfl_xor_sync(kFull, sum[0], off);
+                    inv = rsqrtf(fmaf(sum[0], per, a.eps));
                 }
+                if (turned) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = fmaf(p[e], B[e], y[e] * A[e]) * inv;
-                store(head, live && head < heads, y);
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[k][e] = fmaf(PAIRS ? v[k][e ^ 1] : v[1 - k][e], B[k][e], v[k][e] * A[k][e]) * inv;
+                } else {  // a value that is not rotated meets no other: 0 times an infinity is no 0
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            y[k][e] = v[k][e] * A[k][e] * inv;
+                }
+                store(head, c.live && head < heads, y);
                 head += kHeads;
             }
         }
     };
+    auto put_bf16 = [&](uint16_t *to, const float (&y)[2][8]) {
+        *reinterpret_cast<uint4 *>(to + 8 * c.first) = pack8(y[0]);
+        *reinterpret_cast<uint4 *>(to + 8 * c.second) = pack8(y[1]);
+    };
     if (from < nq)
-        normed(from, min(to, nq), a.Hq, a.q + row * a.qs, a.qh, a.q_weight,
-               [&](int head, bool have, const float (&y)[8]) {
+        normed(true, from, min(to, nq), a.Hq, a.q + row * a.qs, a.qh, a.q_weight,
+               [&](int head, bool have, const float (&y)[2][8]) {
                    if (have)
-                       *reinterpret_cast<uint4 *>(a.q_out + row * a.qos + head * a.qoh + d) = pack8(y);
+                       put_bf16(a.q_out + row * a.qos + head * a.qoh, y);
                });
     if (to > nq && from < nq + nk)
-        normed(max(from, nq) - nq, min(to, nq + nk) - nq, a.H, a.k + row * a.ks, a.kh, a.k_weight,
-               [&](int head, bool have, const float (&y)[8]) {
+        normed(false, max(from, nq) - nq, min(to, nq + nk) - nq, a.H, a.k + row * a.ks, a.kh, a.k_weight,
+               [&](int head, bool have, const float (&y)[2][8]) {
                    if (a.k_out && have)
-                       *reinterpret_cast<uint4 *>(a.k_out + row * a.kos + head * a.koh + d) = pack8(y);
+                       put_bf16(a.k_out + row * a.kos + head * a.koh, y);
                    if (a.dtype >= 0)
-                       to_cache(a, a.ck, a.ckb, k_at + head * a.khead, l, put && have, y, a.k_inv, a.k_scale);
+                       to_cache(a, a.ck, a.ckb, k_at + head * a.khead, c, put && have, y, a.k_inv, a.k_scale);
                });
     if (to > nq + nk) {
         const int first = max(from, nq + nk) - nq - nk, last = to - nq - nk;
         for (int i = first; i < last; i += kLoads) {
-            uint4 x[kLoads];
-#pragma unroll
-            for (int u = 0; u < kLoads; ++u) {
-                const int head = (i + u) * kHeads + sub;
-                x[u] = make_uint4(0, 0, 0, 0);
-                if (i + u < last && live && head < a.H)
-                    x[u] = *reinterpret_cast<const uint4 *>(a.v + row * a.vs + head * a.vh + d);
-            }
+            load(i, last, a.H, a.v + row * a.vs, a.vh);
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 if (i + u >= last)
                     break;
                 const int head = (i + u) * kHeads + sub;
-                float y[8];
-                unpack8(x[u], y);
-                to_cache(a, a.cv, a.cvb, v_at + head * a.vhead, l, put && live && head < a.H, y, a.v_inv,
+                float y[2][8];
+                unpack8(x[u][0], y[0]);
+                unpack8(x[u][1], y[1]);
+                to_cache(a, a.cv, a.cvb, v_at + head * a.vhead, c, put && c.live && head < a.H, y, a.v_inv,
                          a.v_scale);
             }
         }
@@ -351,8 +407,8 @@ cudaError_t launch_qk_norm_rope(QkArgs &a, cudaStream_t s)
     const cudaError_t e = device_info(&di);
     if (e != cudaSuccess)
         return e;
-    int lanes = 2;
-    while (8 * lanes < a.D)
+    int lanes = 1, at = 0;
+    for (; 16 * lanes < a.D; ++at)
         lanes *= 2;
     const int per = 32 / lanes;
     const int steps = (a.Hq + per - 1) / per + (a.dtype >= 0 ? 2 : 1) * ((a.H + per - 1) / per);
@@ -362,11 +418,8 @@ cudaError_t launch_qk_norm_rope(QkArgs &a, cudaStream_t s)
     if (blocks > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     void (*const kernels[2][5])(QkArgs) = {
-        {qk_kernel<2, false>, qk_kernel<4, false>, qk_kernel<8, false>, qk_kernel<16, false>, qk_kernel<32, false>},
-        {qk_kernel<2, true>, qk_kernel<4, true>, qk_kernel<8, true>, qk_kernel<16, true>, qk_kernel<32, true>}};
-    int at = 0;
-    while (2 << at < lanes)
-        ++at;
+        {qk_kernel<1, false>, qk_kernel<2, false>, qk_kernel<4, false>, qk_kernel<8, false>, qk_kernel<16, false>},
+        {qk_kernel<1, true>, qk_kernel<2, true>, qk_kernel<4, true>, qk_kernel<8, true>, qk_kernel<16, true>}};
     const auto kernel = kernels[a.interleaved][at];
     return launch_pdl(kernel, (unsigned)blocks, kThreads, 0, s, a);
 }

@@ -534,7 +534,7 @@ typedef struct dvl_qk {
  *   of each pair (y1, y2) of the first rot values, t = position * freq turns:
  *   y1 cos t - y2 sin t,  y2 cos t + y1 sin t;   the other values stay.
  * Values are not normed or rotated.  The turns' fractional part is exact to
- * 2^-32 whatever the position; cos and sin are off by at most 2^-21 (less than
+ * 2^-32 whatever the position; cos and sin are off by at most 2^-20 (less than
  * a hundredth of a bf16 rounding).  q_out and k_out are rounded to bf16 once.
  * With a cache, row r is the newest-but-(end - 1 - r) token of its sequence b
  * (end: starts[b + 1]): its place is p = lengths[b] - (end - r), page
