@@ -11,6 +11,12 @@
 // writes is all the order there is to keep -- among the threads that touch the
 // same bytes.  Those are one block: a block owns a few columns (16 bytes each)
 // of a token, of one sequence, and walks its list, so blocks never meet.
+//
+// Measured (GB300, wall time a call back to back): half of 16 x 16,381 tokens of
+// 8 x 128 in 4 bits 66 us (228 MB, 0.51 of the copy rate: 32 steps of a read, a
+// barrier and a write, each about 2 us; with 8 loads a lane and 256 threads 70,
+// with 16 loads 124); a path of 7 of one request's tree 2.9 us and 64 requests'
+// 3.1, the host's side of the call.
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"
@@ -19,9 +25,9 @@
 namespace dvl {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 8;  // loads in flight per lane
+constexpr int kRows = 4;  // loads in flight per lane
 
 // Where a row of the list lies and goes in the block's columns, in bytes from
 // the pool's start; from < 0: nowhere.
@@ -52,42 +58,55 @@ __device__ __forceinline__ void keep_columns(const KeepArgs &a, const KeepPool &
         return (unsigned)page < (unsigned)a.pages ? page * pool.page + (pos - entry * a.page_size) * pool.token
                                                   : -1;
     };
-    auto look_up = [&](int i0, Move (&m)[kLook]) {
+    // the list's entries of a step, and from them its places
+    auto entries = [&](int64_t i0, int (&from)[kLook]) {
 #pragma unroll
         for (int k = 0; k < kLook; ++k) {
-            const int r = 32 * k + lane, i = i0 + warp * kMine + r;
+            const int r = 32 * k + lane;
+            const int64_t i = i0 + warp * kMine + r;
+            from[k] = -1;
+            if ((kMine >= 32 || r < kMine) && i < count)
+                from[k] = keep[i];
+        }
+    };
+    auto places = [&](int64_t i0, const int (&from)[kLook], Move (&m)[kLook]) {
+#pragma unroll
+        for (int k = 0; k < kLook; ++k) {
+            const int64_t src = (int64_t)first + from[k], dst = first + i0 + warp * kMine + 32 * k + lane;
             m[k].from = m[k].to = -1;
-            if ((kMine >= 32 || r < kMine) && i < count) {
-                const int from = keep[i];
-                const int64_t src = (int64_t)first + from, dst = (int64_t)first + i;
-                if (from >= 0 && src != dst && src < length && dst < length) {
-                    m[k].from = place(src);
-                    m[k].to = place(dst);
-                    if (m[k].to < 0)
-                        m[k].from = -1;
-                }
+            if (from[k] >= 0 && src != dst && src < length && dst < length) {
+                m[k].from = place(src);
+                m[k].to = place(dst);
+                if (m[k].to < 0)
+                    m[k].from = -1;
             }
         }
     };
+    constexpr int kStep = kWarps * kMine;
     Move now[kLook];
-    look_up(0, now);
-    for (int i0 = 0; i0 < count; i0 += kWarps * kMine) {
+    int from[kLook];
+    entries(0, from);
+    places(0, from, now);
+    entries(kStep, from);
+    for (int64_t i0 = 0; i0 < count; i0 += kStep) {
         U v[kRows];
         int64_t to[kRows];
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
             const int r = j * kAtOnce + lane / COLS;  // of the warp's rows
-            const int64_t from = __shfl_sync(kFull, now[j * kAtOnce / 32].from, r & 31);
+            const int64_t at_row = __shfl_sync(kFull, now[j * kAtOnce / 32].from, r & 31);
             to[j] = __shfl_sync(kFull, now[j * kAtOnce / 32].to, r & 31);
-            if (from < 0 || !mine)
+            if (at_row < 0 || !mine)
                 to[j] = -1;
             else
-                v[j] = *reinterpret_cast<const U *>(at + from);
+                v[j] = *reinterpret_cast<const U *>(at + at_row);
         }
-        // the next step's places are looked up while its rows are on their way
-        // (past the list's end none are)
-        if (i0 + kWarps * kMine < count)
-            look_up(i0 + kWarps * kMine, now);
+        // while its rows are on their way, the next step's places are looked up
+        // and the entries of the one after read (past the list's end: none)
+        if (i0 + kStep < count) {
+            places(i0 + kStep, from, now);
+            entries(i0 + 2 * kStep, from);
+        }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kRows; ++j)
@@ -129,8 +148,12 @@ cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s)
             n += (a.pool[p].cols + cols - 1) / cols;
         return n;
     };
+    // Columns per block: 32 (512 bytes a row) where a list is one step of a block
+    // or there are two blocks an SM, else 8 or 2: half of 16 x 16,381 4-bit tokens
+    // took 223 us with 64 blocks of 32 columns, 75 with 192 of 8 (2 columns, 32
+    // bytes a row, where four blocks an SM were asked for: 73).
     int cols = 32;
-    if (a.M > 8 * kWarps)
+    if (a.M > kRows * kWarps)
         while (cols > 2 && a.B * blocks(cols) < 2 * di.sms)
             cols /= 4;
     int64_t n = 0;
