@@ -570,10 +570,15 @@ dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64
     std::memset(&a, 0, sizeof a);
     const int64_t half = half_bytes(cache);
     const int row = (int)(cache->D * half / 2);  // bytes of a head of a token
-    a.n_pools = cache->dtype == DVL_NVFP4 ? 4 : 2;
-    for (int i = 0; i < a.n_pools; ++i) {
-        KeepPool &p = a.pool[i];
+    // values that are the keys themselves move with them, once
+    const bool shared = cache->k == cache->v && cache->k_page_stride == cache->v_page_stride &&
+                        cache->k_token_stride == cache->v_token_stride &&
+                        cache->k_head_stride == cache->v_head_stride;
+    for (int i = 0; i < (cache->dtype == DVL_NVFP4 ? 4 : 2); ++i) {
         const bool values = i & 1, scales = i >= 2;
+        if (values && shared && (!scales || cache->k_blocks == cache->v_blocks))
+            continue;
+        KeepPool &p = a.pool[a.n_pools++];
         const int64_t down = scales ? 16 : 2;
         p.base = static_cast<unsigned char *>(scales ? (values ? cache->v_blocks : cache->k_blocks)
                                                      : (values ? cache->v : cache->k));

@@ -346,11 +346,11 @@ dvl_status dvl_add_rmsnorm(const dvl_norm *args, void *stream);
  * lie any distance apart).
  * An NVFP4 cache holds E2M1 codes, two to a byte (low nibble = even d), one
  * E4M3 scale per 16 consecutive values of a row, and one fp32 scale for all
- * keys and one for all values: value = e2m1 * e4m3 * k_scale.  D and every
- * stride are multiples of 64, strides of D too (elements are 4-bit values: a
- * row is D / 2 bytes).  The scales lie as the codes do, in an eighth of the
- * room: the scales of a row that starts at byte x of k start at byte x / 8 of
- * k_blocks.  (The last two fields are read with DVL_NVFP4 alone.) */
+ * keys and one for all values: value = e2m1 * e4m3 * k_scale.  D is a multiple
+ * of 64 and every stride one of D (elements are 4-bit values: a row is D / 2
+ * bytes).  The scales lie as the codes do, in an eighth of the room: the scales
+ * of a row that starts at byte x of k start at byte x / 8 of k_blocks.  (The
+ * last two fields are read with DVL_NVFP4 alone.) */
 typedef struct dvl_kv_cache {
     int32_t dtype;            /* DVL_BF16, DVL_FP8 (E4M3 codes, one scale each) or
                                  DVL_NVFP4                                         */
@@ -546,8 +546,9 @@ typedef struct dvl_qk {
  * y stays one in bf16 and E4M3, and makes its 16 values NaN in NVFP4 (an
  * infinity becomes the largest number).
  * A place below 0 or past the table, or a page outside the pool, is not written
- * (q_out and k_out are).  Rows past starts[B] are left as they were, in all
- * outputs.  Two rows with one place in the cache leave either's values there.
+ * (q_out and k_out are).  Rows of no sequence (past starts[B], or before
+ * starts[0]) are left as they were, in all outputs.  Two rows with one place in the cache leave either's values there.
+ * With an E4M3 or NVFP4 cache both scales lie in [2^-100, 2^100].
  * Errors: DVL_ERR_INVALID_ARG (sizes, pointers or alignment outside the above;
  * a key-value head count or D other than the cache's; rows not a multiple of B
  * without starts; rot > 0 with neither cache nor positions; v without cache or
@@ -572,10 +573,11 @@ dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
  *            first, strictly rising (so keep[b][i] >= i).  A sequence whose row
  *            does not rise holds unspecified tokens in [first, first + counts).
  *   counts:  device int32 [B]: below 0 counts as 0, above M as M.
- *   M:       >= 0, any size.  lengths_out: device int32 [B], or NULL; shares no
+ *   M:       0 .. 2^31 - 65,537.  lengths_out: device int32 [B], or NULL; shares no
  *            byte with an input.
  * A place that is not below the sequence's length, or whose page id is outside
- * the pool, moves nothing.  Sequences share no page that is written.
+ * the pool, moves nothing.  Sequences share no page that is written; keys and
+ * values share no byte, unless they are the same pool.
  * Errors: DVL_ERR_INVALID_ARG, DVL_ERR_CUDA. */
 dvl_status dvl_cache_keep(const dvl_kv_cache *cache, const int32_t *table, int64_t table_stride,
                           int32_t table_width, const int32_t *lengths, const int32_t *first,

@@ -140,6 +140,31 @@ def test_keep_many_sequences_and_a_given_output(dvl):
     run(dvl, 9, seqs, 1, 64, 16, "fp8", out=torch.empty(500, dtype=torch.int32, device="cuda"))
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_keep_values_that_are_the_keys(dvl, kind):
+    # one pool for both: its rows move once (M past a block's step, so that rows
+    # that have moved would be moved again)
+    rng = np.random.default_rng(13)
+    seqs = [(0, 4000, path(rng, 4000, 2500)), (2, 900, path(rng, 900, 700))]
+    lens = [f + n for f, n, _ in seqs]
+    table, pages = tables(rng, lens, 16)
+    p = Pools(dvl, 13, pages, 16, 8, 64, kind)
+    k = p.raw[0].view(torch.bfloat16) if kind == "bf16" else p.raw[0]
+    more = dict(k_blocks=p.raw[2], v_blocks=p.raw[2]) if kind == "nvfp4" else {}
+    keep = np.full((2, 2500), -1)
+    for b, (_, _, x) in enumerate(seqs):
+        keep[b, :len(x)] = x
+    first, counts = [f for f, _, _ in seqs], [len(x) for _, _, x in seqs]
+    want = [C.kept(x, table, lens, first, keep, counts) for x in p.bytes()[::2]]
+    for _ in range(3):
+        q = Pools(dvl, 13, pages, 16, 8, 64, kind)
+        for x, y in zip(p.raw, q.raw):
+            x.copy_(y)
+        dvl.cache_keep(dvl.KVCache(k, k, **more), ints(table), ints(lens), ints(first), ints(keep), ints(counts))
+        for x, y in zip(p.bytes()[::2], want):
+            assert np.array_equal(x, y)
+
+
 def test_keep_strided_lists(dvl):
     rng = np.random.default_rng(10)
     lens = [50, 60]
