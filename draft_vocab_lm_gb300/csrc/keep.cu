@@ -13,9 +13,8 @@
 // of a token, of one sequence, and walks its list, so blocks never meet.
 //
 // Measured (GB300, wall time a call back to back): half of 16 x 16,381 tokens of
-// 8 x 128 in 4 bits 66 us (228 MB, 0.51 of the copy rate: 32 steps of a read, a
-// barrier and a write, each about 2 us; with 8 loads a lane and 256 threads 70,
-// with 16 loads 124); a path of 7 of one request's tree 2.9 us and 64 requests'
+// 8 x 128 in 4 bits 52 us (228 MB, 0.65 of the copy rate: 16 steps of a read, a
+// barrier and a write; with 512 threads and four loads a lane 59); a path of 7 of one request's tree 2.9 us and 64 requests'
 // 3.1, the host's side of the call.
 #include <cuda_runtime.h>
 
@@ -25,9 +24,9 @@
 namespace dvl {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRows = 4;  // loads in flight per lane
+constexpr int kRows = 8;  // loads in flight per lane
 
 // Where a row of the list lies and goes in the block's columns, in bytes from
 // the pool's start; from < 0: nowhere.
@@ -148,14 +147,14 @@ cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s)
             n += (a.pool[p].cols + cols - 1) / cols;
         return n;
     };
-    // Columns per block: 32 (512 bytes a row) where a list is one step of a block
-    // or there are two blocks an SM, else 8 or 2: half of 16 x 16,381 4-bit tokens
-    // took 223 us with 64 blocks of 32 columns, 75 with 192 of 8 (2 columns, 32
-    // bytes a row, where four blocks an SM were asked for: 73).
+    // Columns per block: 32 (512 bytes a row) where a list is one step of a block,
+    // else as many of 32, 8, 4 or 2 as leave two blocks an SM.  Half of 16 x 16,381
+    // 4-bit tokens: 64 blocks of 32 columns 223 us (an earlier form), 192 of 8 71,
+    // 384 of 4 (what the rule gives) 52, 768 of 2 70.
     int cols = 32;
     if (a.M > kRows * kWarps)
         while (cols > 2 && a.B * blocks(cols) < 2 * di.sms)
-            cols /= 4;
+            cols = cols == 32 ? 8 : cols / 2;
     int64_t n = 0;
     for (int p = 0; p < a.n_pools; ++p) {
         a.pool[p].first_block = (int)n;
@@ -164,7 +163,10 @@ cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s)
     if (n * a.B > 0x7fffffffLL)
         return cudaErrorInvalidConfiguration;
     a.blocks = (int)n;
-    const auto kernel = cols == 32 ? cache_keep_kernel<32> : cols == 8 ? cache_keep_kernel<8> : cache_keep_kernel<2>;
+    const auto kernel = cols == 32  ? cache_keep_kernel<32>
+                        : cols == 8 ? cache_keep_kernel<8>
+                        : cols == 4 ? cache_keep_kernel<4>
+                                    : cache_keep_kernel<2>;
     return launch_pdl(kernel, (unsigned)(n * a.B), kThreads, 0, s, a);
 }
 
