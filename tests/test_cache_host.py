@@ -1,6 +1,7 @@
 """qk_norm_rope, cache_keep and NVFP4 caches refuse bad arguments on the host,
 before anything is enqueued (no GPU here: the pointers are never dereferenced),
 and the tests' own references tell planted mistakes."""
+import concurrent.futures as cf
 import ctypes
 
 import numpy as np
@@ -116,8 +117,10 @@ def test_rope_allowed(L, kw):
     import torch
     if torch.cuda.is_available():
         pytest.skip("no pointers to give a device")
-    assert rope(L, cache=cache(), **kw) == NO_DEVICE
-    assert rope(L, cache=nvfp4(), **kw) == NO_DEVICE
+    # (on a thread of its own: the failure's description is the thread's)
+    with cf.ThreadPoolExecutor(1) as one:
+        assert one.submit(rope, L, cache=cache(), **kw).result() == NO_DEVICE
+        assert one.submit(rope, L, cache=nvfp4(), **kw).result() == NO_DEVICE
 
 
 def test_rope_in_place_of_a_neighbour_is_refused(L):
