@@ -500,7 +500,8 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
  * values start on 16-byte boundaries. */
 typedef struct dvl_qk {
     int64_t rows;             /* new tokens, 0 .. 2^31 - 1; 0 enqueues nothing     */
-    int32_t Hq, H, D;         /* query heads, key-value heads (the cache's), head
+    int32_t Hq, H, D;         /* query heads, key-value heads (the cache's), up to
+                                 65,536 each; head
                                  width: a multiple of 16, <= DVL_MAX_HEAD_DIM      */
     int32_t rot;              /* the first rot values of a head are rotated: a
                                  multiple of 16, <= D; 0: none                     */
