@@ -85,8 +85,9 @@
 // row without positions keeps the sum 0 and gives 0.  Positions that only
 // some rows see (the last T - 1) are added value by value for the rows that
 // see them, and their V rows zeroed before the MMA: 0 times a NaN or an
-// infinity in V would otherwise reach the rows that do not.  Rows past the
-// length are zeros from the copy.
+// infinity in V would otherwise reach the rows that do not.  (Over an NVFP4 cache
+// only those with a NaN among their scales: there is no other such value.)  Rows
+// past the length are zeros from the copy.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -1227,9 +1228,18 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
             if (a.T > 1 && pos0 + TOK > sees_least) {
                 const int from = max(max(sees_least, 0) - pos0, 0);
                 const int to = min(cur.len - pos0, TOK);
-                for (int tok = from; tok < to; ++tok) {
-                    float w[NS];
-                    if constexpr (kTurned) {
+                if constexpr (kTurned) {
+                    // Only where a scale is a NaN: codes are numbers, and there are
+                    // no infinities among the scales, so a weight of 0 does for the
+                    // others.
+                    const uint32_t scales = v_smem + TOK * S::kVPitch;
+                    unsigned nans = 0u;  // tokens, from `from` on
+                    for (int tok = from; tok < to; ++tok) {
+                        const uint32_t x = lds32(scales + tok * S::kBlocks + lane % (S::kBlocks / 4) * 4);
+                        if (!__any_sync(kFull, __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0u))
+                            continue;
+                        nans |= 1u << (tok - from);
+                        float w[NS];
 #pragma unroll
                         for (int j = 0; j < NS; ++j) {
                             const int at = 4 * (j >> 1) + (j & 1);
@@ -1242,55 +1252,62 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                         for (int n = 0; n < kOT; ++n)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float v = fp4_value(v_smem, tok, n / 4 * 64 + 8 * g + 2 * (n % 4) + e);
+                                const float v =
+                                    fp4_value(v_smem, tok, n / 4 * 64 + 8 * g + 2 * (n % 4) + e);
 #pragma unroll
-                                for (int j = 0; j < NS; ++j)
+                                for (int j = 0; j < NS; ++j) {
+                                    float &sum = o[n][4 * (j >> 1) + 2 * e + (j & 1)];
                                     if (pos0 + tok < sees[j])
-                                        o[n][4 * (j >> 1) + 2 * e + (j & 1)] =
-                                            fmaf(w[j], v, o[n][4 * (j >> 1) + 2 * e + (j & 1)]);
+                                        sum = fmaf(w[j], v, sum);
+                                }
                             }
-                        continue;
-                    } else {
-                    const int src = (lane & ~3) + ((tok & 7) >> 1);
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        float pair[kSN];
-#pragma unroll
-                        for (int n = 0; n < kSN; ++n)
-                            pair[n] = tok & 1 ? s[n][2 * j + 1] : s[n][2 * j];
-                        float mine = tok & 8 ? pair[1] : pair[0];
-                        if constexpr (kSN == 4)
-                            mine = tok & 16 ? (tok & 8 ? pair[3] : pair[2]) : mine;
-                        w[j] = __shfl_sync(kFull, F16 ? mine * kF16Weight : mine, src);
                     }
-#pragma unroll
-                    for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int d = out_col<FMT>(n, c, e);
-                            float v;
-                            if constexpr (FMT == kFp8)
-                                v = unpack1<true>((uint16_t)e4m3x2_f16x2(
-                                    lds8(v_smem + tok * S::kVPitch + d)));
-                            else
-                                v = unpack1<false>(lds16(v_smem + tok * S::kVPitch +
-                                                         (((d / 8) ^ (tok & 7)) << 4) + (d & 7) * 2));
-#pragma unroll
-                            for (int j = 0; j < NJ; ++j)
-                                if (pos0 + tok < sees[j])
-                                    o[n][2 * j + e] = fmaf(w[j], v, o[n][2 * j + e]);
-                        }
+                    if (nans != 0u) {  // a scale of 0 makes a token's values 0
+                        group_sync<kGroup>(group);
+                        for (int u = at; u < (to - from) * (S::kBlocks / 4); u += kGroup)
+                            if (nans >> u / (S::kBlocks / 4) & 1u)
+                                sts32(scales + from * S::kBlocks + u * 4, 0u);
+                        group_sync<kGroup>(group);
                     }
-                }
-                group_sync<kGroup>(group);
-                if constexpr (FMT == kFp4) {  // a scale of 0 makes its values 0
-                    for (int u = at; u < (to - from) * (S::kBlocks / 4); u += kGroup)
-                        sts32(v_smem + TOK * S::kVPitch + from * S::kBlocks + u * 4, 0u);
                 } else {
+                    for (int tok = from; tok < to; ++tok) {
+                        const int src = (lane & ~3) + ((tok & 7) >> 1);
+                        float w[NJ];
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            float pair[kSN];
+#pragma unroll
+                            for (int n = 0; n < kSN; ++n)
+                                pair[n] = tok & 1 ? s[n][2 * j + 1] : s[n][2 * j];
+                            float mine = tok & 8 ? pair[1] : pair[0];
+                            if constexpr (kSN == 4)
+                                mine = tok & 16 ? (tok & 8 ? pair[3] : pair[2]) : mine;
+                            w[j] = __shfl_sync(kFull, F16 ? mine * kF16Weight : mine, src);
+                        }
+#pragma unroll
+                        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int d = out_col<FMT>(n, c, e);
+                                float v;
+                                if constexpr (FMT == kFp8)
+                                    v = unpack1<true>((uint16_t)e4m3x2_f16x2(
+                                        lds8(v_smem + tok * S::kVPitch + d)));
+                                else
+                                    v = unpack1<false>(
+                                        lds16(v_smem + tok * S::kVPitch +
+                                              (((d / 8) ^ (tok & 7)) << 4) + (d & 7) * 2));
+#pragma unroll
+                                for (int j = 0; j < NJ; ++j)
+                                    if (pos0 + tok < sees[j])
+                                        o[n][2 * j + e] = fmaf(w[j], v, o[n][2 * j + e]);
+                            }
+                    }
+                    group_sync<kGroup>(group);
                     for (int u = at; u < (to - from) * (S::kVPitch / 16); u += kGroup)
                         sts128(v_smem + from * S::kVPitch + u * 16, make_uint4(0, 0, 0, 0));
+                    group_sync<kGroup>(group);
                 }
-                group_sync<kGroup>(group);
             }
 #pragma unroll
             for (int k = 0; k < TOK / 16; ++k) {
@@ -1426,24 +1443,23 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                                             o[n][4 * (j >> 1) + 2 + (j & 1)] * f[j],
                                             o[n + 1][4 * (j >> 1) + (j & 1)] * f[j],
                                             o[n + 1][4 * (j >> 1) + 2 + (j & 1)] * f[j]);
-                        continue;
                     } else {
 #pragma unroll
-                    for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += F16 ? 4 : 1) {
-                        if constexpr (F16) {
+                        for (int n0 = c0 / 8; n0 < (c0 + S::kRound) / 8; n0 += F16 ? 4 : 1) {
+                            if constexpr (F16) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                *reinterpret_cast<float4 *>(
-                                    dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT>(r))) =
-                                    make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
-                                                o[n0 + 2][2 * j + e] * f[j],
-                                                o[n0 + 3][2 * j + e] * f[j]);
-                        } else {
-                            *reinterpret_cast<float2 *>(
-                                dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT>(r))) =
-                                make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
+                                for (int e = 0; e < 2; ++e)
+                                    *reinterpret_cast<float4 *>(
+                                        dst + ((out_col<FMT>(n0, c, e) - c0) ^ swizzle<FMT>(r))) =
+                                        make_float4(o[n0][2 * j + e] * f[j], o[n0 + 1][2 * j + e] * f[j],
+                                                    o[n0 + 2][2 * j + e] * f[j],
+                                                    o[n0 + 3][2 * j + e] * f[j]);
+                            } else {
+                                *reinterpret_cast<float2 *>(
+                                    dst + ((out_col<FMT>(n0, c, 0) - c0) ^ swizzle<FMT>(r))) =
+                                    make_float2(o[n0][2 * j] * f[j], o[n0][2 * j + 1] * f[j]);
+                            }
                         }
-                    }
                     }
                 }
                 __syncthreads();

@@ -131,11 +131,12 @@ def test_attention4_masked_slots_may_hold_anything(dvl, T, D):
     assert torch.equal(clean[0], dirty[0]) and torch.equal(clean[1], dirty[1])
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("G", [2, 5, 8, 16])
-def test_attention4_later_tokens_do_not_reach_earlier_rows(dvl, G):
+def test_attention4_later_tokens_do_not_reach_earlier_rows(dvl, G, D):
     # the newest token's scales are NaN: only the rows that see it change
     T, lengths = 3, [3, 64, 65, 66, 130]
-    c = Case(8, lengths, T, 2 * G, 2, 128, 16)
+    c = Case(8, lengths, T, 2 * G, 2, D, 16)
     clean = c.call(dvl)
     for b, n in enumerate(lengths):
         for x in c.blocks:
