@@ -501,8 +501,8 @@ dvl_status dvl_beam_reorder(const dvl_state *states, int32_t n_states, const dvl
 typedef struct dvl_qk {
     int64_t rows;             /* new tokens, 0 .. 2^31 - 1; 0 enqueues nothing     */
     int32_t Hq, H, D;         /* query heads, key-value heads (the cache's), up to
-                                 65,536 each; head
-                                 width: a multiple of 16, <= DVL_MAX_HEAD_DIM      */
+                                 65,536 each; head width: a multiple of 16,
+                                 <= DVL_MAX_HEAD_DIM                               */
     int32_t rot;              /* the first rot values of a head are rotated: a
                                  multiple of 16, <= D; 0: none                     */
     int32_t interleaved;      /* pairs (2i, 2i + 1) instead of (i, i + rot / 2)    */
