@@ -936,6 +936,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     float o[kOT][kOE];
     float m[NS], l[NS];
     int sees[NS], sees_least = 0;
+    bool far = false;  // (NVFP4) some row's maximum is large: turned_weights()
     auto row_of = [&](int j) { return 16 * mt + (kTurned ? 8 * (j >> 1) + 2 * c + (j & 1) : 8 * j + g); };
     auto reset = [&]() {
 #pragma unroll
@@ -943,6 +944,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
             m[j] = kNegInf;
             l[j] = 0.f;
         }
+        far = false;
 #pragma unroll
         for (int n = 0; n < kOT; ++n)
 #pragma unroll
@@ -974,7 +976,12 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
     // tokens g and g + 8 of every 16 for query rows 2 c and 2 c + 1 -- and their
     // weights in units of 2^-15, also as the second product's operand.  The
     // lanes of a row compare their maxima only where one is above the running
-    // maximum, which after the first chunks is rare.
+    // maximum, which after the first chunks is rare.  A weight's exponent is one
+    // fma, s sc + (15 - m), of the unrounded product with roundings of m and of
+    // 15 - m: up to |m| = 2^20 it exceeds 15 by less than 1/8, and f16 holds
+    // 2^15.9.  From 2^23 on it would not (16.99, and at 2^28 the maximum's own
+    // weight could be 2^32 or 2^-32), so larger maxima subtract from the rounded
+    // product, which lies nowhere above m.
     auto turned_weights = [&](uint32_t k_smem, int pos0, auto &s, auto &pa) {
         constexpr int kTM = TOK / 16;
 #pragma unroll
@@ -1049,6 +1056,7 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
         }
         if (__any_sync(kFull, raised)) {
             float alpha[NS];
+            bool large = false;
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
                 big[j] = fmaxf(big[j], m[j]);
@@ -1058,7 +1066,9 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
                 alpha[j] = ex2(m[j] - (big[j] == kNegInf ? 0.f : big[j]));
                 m[j] = big[j];
                 l[j] *= alpha[j];
+                large |= fabsf(m[j]) >= 0x1p20f && m[j] != kNegInf;
             }
+            far = __any_sync(kFull, large);
 #pragma unroll
             for (int n = 0; n < kOT; ++n)
 #pragma unroll
@@ -1069,6 +1079,20 @@ __global__ void __launch_bounds__(Shape<DP, FMT, RT, TOK, P, G>::kThreads, BLOCK
 #pragma unroll
         for (int j = 0; j < NS; ++j)
             up[j] = m[j] == kNegInf ? 0.f : 15.f - m[j];
+        if (far) {
+#pragma unroll
+            for (int t = 0; t < kTM; ++t)
+#pragma unroll
+                for (int e = 0; e < kOE; ++e) {
+                    const int j = 2 * (e >> 2) + (e & 1);
+                    s[t][e] = __fmul_rn(s[t][e], sc[j]) - (m[j] == kNegInf ? 0.f : m[j]);
+                }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+                sc[j] = 1.f;
+                up[j] = 15.f;
+            }
+        }
 #pragma unroll
         for (int t = 0; t < kTM; ++t) {
 #pragma unroll

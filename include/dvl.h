@@ -389,8 +389,9 @@ size_t dvl_attention_workspace_bytes(const dvl_kv_cache *cache, int32_t T, int32
  * below 2^-29 of their row's largest are rounded to a grid of 2^-38 of it.  The
  * weights exp(s_j - m) are rounded before they meet V: to bf16 (2^-8
  * relative), or with an FP8 or NVFP4 cache to f16 (2^-11 relative down to 2^-29,
- * a grid of 2^-39 below).  The result does not depend on timing: the same call on the
- * same device gives the same bits.
+ * a grid of 2^-39 below).  Scores of any size that fp32 holds (in units of ln 2)
+ * keep their order; one above that makes its row NaN.  The result does not depend
+ * on timing: the same call on the same device gives the same bits.
  *   q:        device bf16 [B][T][Hq][D]; strides in elements for the first
  *             three, the last is 1; 16-byte aligned rows.
  *   table:    device int32 [B][table_width], row stride table_stride: the
