@@ -158,7 +158,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return e4m3x2(a, b) | (uint32_t)e4m3x2(c, d) << 16;
 }
 
-// A lane's sixteen values of a head in the cache's type.
+// A lane's sixteen values of a head in the cache's type.  NVFP4: the quotients of
+// the codes are rounded once, as middles between two codes are common among values
+// of 8 bits, and a product with the reciprocal can lie on either side of one.  That
+// product is corrected by its residual (P. Markstein, 1990: with a rounded
+// reciprocal the result is the rounded quotient), two operations a value, where
+// fp32 holds the residual: not for a block that saturates, nor for a tiny unit.
+// 16,381 rows of 40 + 2 x 8 heads of 128: 93 us, with divisions 100, uncorrected
+// 87; 192 rows 5.6, 6.1 and 4.8.
 // at: the place of the row's head in the pool, in bytes (of NVFP4: of codes).
 __device__ __forceinline__ void to_cache(const QkArgs &a, unsigned char *pool, unsigned char *blocks,
                                          int64_t at, const Chunks &c, bool put, const float (&y)[2][8],
@@ -197,12 +204,21 @@ __device__ __forceinline__ void to_cache(const QkArgs &a, unsigned char *pool, u
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float m = __uint_as_float(max(big[i], mate[i]));
-            const uint16_t s = e4m3x2(m * (inv_scale * (1.f / 6.f)), 0.f) & 0xff;  // NaN stays NaN
-            const float inv = s == 0 ? 0.f : 1.f / (e4m3_value(s) * scale);
+            const uint16_t s = e4m3x2(m / (6.f * scale), 0.f) & 0xff;  // NaN stays NaN
+            const float unit = e4m3_value(s) * scale;
             float z[8];
+            if (unit >= 0x1p-90f && m <= 8.f * unit) {
+                const float inv = 1.f / unit;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                z[e] = s == 0 ? 0.f : y[i][e] * inv;
+                for (int e = 0; e < 8; ++e) {
+                    const float z0 = y[i][e] * inv;
+                    z[e] = fmaf(fmaf(z0, unit, -y[i][e]), -inv, z0);  // (these signs keep -0)
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    z[e] = s == 0 ? 0.f : y[i][e] / unit;
+            }
             const uint32_t w = e2m1x8(z);
             if (put) {
                 *reinterpret_cast<uint32_t *>(pool + at + 4 * chunk[i]) = w;

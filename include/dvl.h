@@ -543,8 +543,9 @@ typedef struct dvl_qk {
  * table[b][p / page_size], slot p % page_size.  Keys and values go there in the
  * cache's type, rounded once from fp32: to bf16; to E4M3, RNE_e4m3(y / scale),
  * saturating at 448 (the quotient is a product with the fp32 reciprocal); or
- * to NVFP4: per 16 values s = RNE_e4m3(max |y| / (6 scale)), code =
- * RNE_e2m1(y / (s scale)), all codes 0 where s is 0, both saturating.  A NaN in
+ * to NVFP4 as dvl_quantize_head does: per 16 values s = RNE_e4m3(max |y| / (6
+ * scale)), code = RNE_e2m1(y / (s scale)), every fp32 operation rounded once, all
+ * codes 0 where s is 0, both saturating.  A NaN in
  * y stays one in bf16 and E4M3, and makes its 16 values NaN in NVFP4 (an
  * infinity becomes the largest number).
  * A place below 0 or past the table, or a page outside the pool, is not written
