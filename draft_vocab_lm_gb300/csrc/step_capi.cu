@@ -3,9 +3,11 @@
 // allocates, frees or synchronizes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstring>
+#include <utility>
 
 #include "dvl_attention.h"
 #include "dvl_step.h"
@@ -142,12 +144,49 @@ bool same(const HeadRows &x, const HeadRows &y, int64_t rows)
     return x.p == y.p && (rows == 1 || x.stride == y.stride) &&
            (x.heads == 1 || x.head_stride == y.head_stride) && x.heads == y.heads;
 }
-// Whether two of these tensors may share a byte: by rows where the heads of a
-// row lie together, else by the span of all.
+// Floor of x / d, d > 0.
+int64_t floor_div(int64_t x, int64_t d) { return x / d - (x % d < 0); }
+
+// The differences lo .. hi of two tensors' indices along an axis, `stride` bytes each.
+struct Axis {
+    int64_t lo, hi, stride;
+};
+// Whether runs of bx bytes of one tensor and of by bytes of another meet: whether
+// some off + i a.stride + j b.stride lies in (-by, bx), off the distance of the
+// first runs.  Only differences along the longer stride that the other axis can
+// make up for are tried: a few, where one axis lies within the other.
+bool runs_meet(int64_t off, int64_t bx, int64_t by, Axis a, Axis b)
+{
+    if (a.stride < b.stride)
+        std::swap(a, b);
+    if (b.stride == 0)
+        b = {0, 0, 1};
+    if (a.stride == 0)
+        a = {0, 0, 1};
+    const int64_t first = -floor_div(off + b.hi * b.stride + by - 1, a.stride);
+    const int64_t last = floor_div(bx - 1 - off - b.lo * b.stride, a.stride);
+    for (int64_t i = std::max(first, a.lo); i <= std::min(last, a.hi); ++i) {
+        const int64_t at = off + i * a.stride;
+        if (std::max(-floor_div(at + by - 1, b.stride), b.lo) <= std::min(floor_div(bx - 1 - at, b.stride), b.hi))
+            return true;
+    }
+    return false;
+}
+
+// Whether two of these tensors share a byte.  Where their strides differ: whether
+// they may, by rows where the heads of a row lie together, else by the span of all.
 bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
 {
     if (!x.p || !y.p)
         return false;
+    if ((rows == 1 || x.stride == y.stride) &&
+        (x.heads == 1 || y.heads == 1 || x.head_stride == y.head_stride)) {
+        const Axis r = {1 - rows, rows - 1, rows == 1 ? 0 : 2 * x.stride};
+        const Axis h = {1 - x.heads, y.heads - 1,
+                        x.heads > 1 ? 2 * x.head_stride : y.heads > 1 ? 2 * y.head_stride : 0};
+        const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
+        return runs_meet(off, 2 * D, 2 * D, r, h);
+    }
     auto bytes = [&](const HeadRows &t) {
         const int64_t row = 2 * ((t.heads - 1) * t.head_stride + D);
         const uintptr_t at = reinterpret_cast<uintptr_t>(t.p);
@@ -156,16 +195,7 @@ bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
         const int64_t span = row + 2 * (rows - 1) * t.stride;
         return Rows{at, 1, span, span};
     };
-    const Rows a = bytes(x), b = bytes(y);
-    if (a.rows == rows && b.rows == rows && a.stride == b.stride) {
-        // the same stride: the rows' places within it tell
-        if (a.end() <= b.at || b.end() <= a.at)
-            return false;
-        const Rows &lo = a.at <= b.at ? a : b, &hi = a.at <= b.at ? b : a;
-        const int64_t off = (int64_t)((hi.at - lo.at) % (uintptr_t)a.stride);
-        return off < lo.bytes || off + hi.bytes > a.stride;
-    }
-    return overlap(a, b);
+    return overlap(bytes(x), bytes(y));
 }
 
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)

@@ -556,7 +556,8 @@ typedef struct dvl_qk {
  * a key-value head count or D other than the cache's; rows not a multiple of B
  * without starts; rot > 0 with neither cache nor positions; v without cache or
  * the reverse; neither cache nor k_out; an output that overlaps itself, the other
- * or an input but its own),
+ * or an input but its own -- heads of one tensor may lie between another's where
+ * their strides are the same, else a row counts from its first head to its last),
  * DVL_ERR_CUDA. */
 dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
 
