@@ -157,6 +157,8 @@ struct Axis {
 // make up for are tried: a few, where one axis lies within the other.
 bool runs_meet(int64_t off, int64_t bx, int64_t by, Axis a, Axis b)
 {
+    if (off + a.hi * a.stride + b.hi * b.stride <= -by || off + a.lo * a.stride + b.lo * b.stride >= bx)
+        return false;  // (nearly every call)
     if (a.stride < b.stride)
         std::swap(a, b);
     if (b.stride == 0)
@@ -197,6 +199,70 @@ bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
     };
     return overlap(bytes(x), bytes(y));
 }
+
+// The outputs of a call, and whether what it reads reaches into them.  Nearly
+// nothing lies between their first and last bytes: that is asked first.
+class Written {
+    const HeadRows out_[2];
+    const int64_t rows_;
+    const int D_;
+    uintptr_t from_[2] = {}, end_[2] = {};
+
+public:
+    Written(const HeadRows &x, const HeadRows &y, int64_t rows, int D) : out_{x, y}, rows_(rows), D_(D)
+    {
+        for (int i = 0; i < 2; ++i)
+            if (out_[i].p && rows > 0) {
+                from_[i] = reinterpret_cast<uintptr_t>(out_[i].p);
+                end_[i] = from_[i] + 2 * ((rows - 1) * out_[i].stride + (out_[i].heads - 1) * out_[i].head_stride + D);
+            }
+    }
+    // `count` rows of `bytes` from p on, `stride` bytes apart.
+    bool meets(const void *p, int64_t count, int64_t bytes, int64_t stride) const
+    {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p), last = at + (count - 1) * stride;
+        for (int i = 0; i < 2; ++i)
+            if (at < end_[i] && last + bytes > from_[i] && p && count > 0 && bytes > 0 &&
+                look(i, at, count, bytes, stride))
+                return true;
+        return false;
+    }
+    // A cache's pages, each counted whole.
+    bool meets(const dvl_kv_cache &c) const
+    {
+        const int64_t half = half_bytes(&c);
+        for (int i = 0; i < (c.dtype == DVL_NVFP4 ? 4 : 2); ++i) {
+            const bool values = i & 1;
+            const int shift = i < 2 ? 1 : 4;
+            const int64_t page = values ? c.v_page_stride : c.k_page_stride,
+                          token = values ? c.v_token_stride : c.k_token_stride,
+                          head = values ? c.v_head_stride : c.k_head_stride;
+            if (meets(i < 2 ? (values ? c.v : c.k) : (values ? c.v_blocks : c.k_blocks), c.pages,
+                      ((c.page_size - 1) * token + (c.heads - 1) * head + c.D) * half >> shift, page * half >> shift))
+                return true;
+        }
+        return false;
+    }
+
+private:
+    bool look(int i, uintptr_t p, int64_t count, int64_t bytes, int64_t stride) const
+    {
+        const HeadRows &x = out_[i];
+        const Axis r = {1 - rows_, 0, rows_ == 1 ? 0 : 2 * x.stride};
+        const Axis h = {1 - x.heads, 0, x.heads == 1 ? 0 : 2 * x.head_stride};
+        const int64_t at = (int64_t)(p - from_[i]), end = (int64_t)(end_[i] - from_[i]);
+        if (count > 1 && stride <= bytes) {
+            bytes += (count - 1) * stride;
+            count = 1;
+        }
+        // only the rows that reach into the output's span
+        for (int64_t k = count > 1 ? std::max<int64_t>(0, floor_div(-at - bytes, stride) + 1) : 0;
+             k < count && at + k * stride < end; ++k)
+            if (runs_meet(at + k * stride, 2 * D_, bytes, r, h))
+                return true;
+        return false;
+    }
+};
 
 bool beam_sizes_ok(int32_t batch, int32_t beams, int32_t N)
 {
@@ -496,6 +562,10 @@ dvl_status dvl_qk_norm_rope(const dvl_qk *p, void *stream)
          meet(qo, ko, rows, p->D) || meet(ko, q, rows, p->D) ||
          (ko.p && !same(ko, k, rows) && meet(ko, k, rows, p->D)) || meet(ko, v, rows, p->D)))
         return DVL_ERR_INVALID_ARG;
+    const Written written(qo, ko, rows, p->D);
+    if (written.meets(p->q_weight, 1, 2 * p->D, 0) || written.meets(p->k_weight, 1, 2 * p->D, 0) ||
+        written.meets(p->freq, 1, 4 * p->rot, 0) || written.meets(p->positions, 1, 4 * rows, 0))
+        return DVL_ERR_INVALID_ARG;
     QkArgs a;
     std::memset(&a, 0, sizeof a);
     a.dtype = -1;
@@ -510,6 +580,9 @@ dvl_status dvl_qk_norm_rope(const dvl_qk *p, void *stream)
             (p->table_width < 1 || p->table_stride < 0 ||
              (int64_t)p->table_width * c->page_size > 0x7fffffffLL || !p->table || !aligned(p->table, 4) ||
              !p->lengths || !aligned(p->lengths, 4)))
+            return DVL_ERR_INVALID_ARG;
+        if (written.meets(*c) || written.meets(p->table, p->B, 4ll * p->table_width, 4 * p->table_stride) ||
+            written.meets(p->lengths, 1, 4ll * p->B, 0) || written.meets(p->starts, 1, 4ll * p->B + 4, 0))
             return DVL_ERR_INVALID_ARG;
         // reciprocals of the scales, and products with an E4M3 scale, stay normal numbers
         for (float s : {c->k_scale, c->v_scale})

@@ -556,9 +556,12 @@ typedef struct dvl_qk {
  * a key-value head count or D other than the cache's; rows not a multiple of B
  * without starts; rot > 0 with neither cache nor positions; v without cache or
  * the reverse; neither cache nor k_out; an output that overlaps itself, the other
- * or an input but its own -- heads of one tensor may lie between another's where
- * their strides are the same, else a row counts from its first head to its last),
- * DVL_ERR_CUDA. */
+ * or an input but its own (weights, frequencies, positions, table, lengths and
+ * starts count, and every page of the cache, whole) -- heads of one tensor may lie
+ * between another's where their strides are the same, else a row counts from its
+ * first head to its last), DVL_ERR_CUDA.  Which of the cache's places are written
+ * only the device knows: that its pools share no byte with an input, nor its keys
+ * with its values, is the caller's part. */
 dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
 
 /* Keep some of the newest tokens of every sequence, in order, without gaps:
