@@ -144,6 +144,38 @@ class KVCache:
         self._dev = k.get_device()
 
 
+_inverse = {}  # by its bits
+
+
+def _inverse_turn(bits: int) -> int:
+    """2^bits / (2 pi), within 1, from pi = 16 atan(1/5) - 4 atan(1/239) in integers."""
+    if bits not in _inverse:
+        one = 1 << (2 * bits + 64)
+
+        def atan(n):  # of 1 / n
+            power, total, k = one // n, 0, 0
+            while power:
+                total += (-1) ** k * (power // (2 * k + 1))
+                power //= n * n
+                k += 1
+            return total
+
+        _inverse[bits] = (one << bits) // (2 * (16 * atan(5) - 4 * atan(239)))
+    return _inverse[bits]
+
+
+def _turns(f: float) -> int:
+    """f radians in turns, modulo one, as a signed 64-bit fraction: position x turns,
+    modulo one turn, is then an integer product that wraps.  Exact but for its last
+    bit, which the quotient of two 64-bit floating-point numbers is not."""
+    m, d = f.as_integer_ratio()
+    # 64 bits of the fraction, as many as f has above one, and some to round with
+    bits = 96 + max(0, math.frexp(f)[1])
+    down = d << (bits - 64)
+    turns = (2 * m * _inverse_turn(bits) + down) // (2 * down)
+    return (turns + (1 << 63)) % (1 << 64) - (1 << 63)
+
+
 class Rope:
     """The rotation frequencies of a model, for qk_norm_rope.
 
@@ -162,12 +194,8 @@ class Rope:
         freqs = [float(f) for f in freqs]
         _need(len(freqs) == dim // 2 and all(math.isfinite(f) for f in freqs), "freqs must be dim / 2 finite numbers")
         self.dim, self.interleaved = dim, bool(interleaved)
-        # turns per position as 64-bit fractions: position x freq, modulo one
-        # turn, is then an integer product that wraps
-        turns = [round(math.ldexp(math.fmod(f / (2 * math.pi), 1.0), 64)) for f in freqs]
-        turns = [(t + (1 << 63)) % (1 << 64) - (1 << 63) for t in turns]
         # (the copy has ended when this returns: any stream may use it)
-        self.freq = torch.tensor(turns, dtype=torch.int64).to(device)
+        self.freq = torch.tensor([_turns(f) for f in freqs], dtype=torch.int64).to(device)
 
 
 def _workspace(n: int, device, stream):
