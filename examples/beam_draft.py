@@ -4,7 +4,8 @@ One step, for batch x beams rows:
 
     x = embed[token]
     h = add_rmsnorm(x)                          -> queries, keys, values (matmul)
-    keys, values -> the beam's next cache slot
+    qk_norm_rope(queries, keys, values)         keys, values -> the beam's next cache slot
+                                                (this layer neither norms nor rotates them)
     o = paged_attention(h's queries over the cache)
     h, _ = add_rmsnorm(o wo, residual=x)        residual addition and norm
     logits = h . W_trim^T                       (matmul; W_trim from trim_head)
@@ -88,23 +89,21 @@ class Beams:
         """tokens [batch]: the last token of each request's prompt."""
         self.history[:, :, 0] = tokens.view(-1, 1)
 
-    def append(self, k, v):
+    def append(self, q, k, v):
         """Write one token's keys and values [rows][kv_heads][D] to each row's next slot."""
-        at = self.lengths.view(-1).long()
-        page = self.table.view(-1, self.table.shape[2]).gather(1, (at // self.page).view(-1, 1)).view(-1).long()
-        for pool, x in ((self.k, k), (self.v, v)):
-            x = (x.float() / self.scale).to(pool.dtype) if pool.dtype != x.dtype else x
-            pool.view(torch.uint8)[page, at % self.page] = x.contiguous().view(torch.uint8)
         self.lengths += 1
+        dvl.qk_norm_rope(q, k, v, cache=self.cache, table=self.table.view(-1, self.table.shape[2]),
+                         lengths=self.lengths.view(-1), q_out=q)
 
     def step(self):
         m, rows = self.model, self.batch * self.beams
         x = m.embed[self.history[:, :, self.done].view(-1).long()]
         h, _, _, _ = dvl.add_rmsnorm(x, m.norm1)
         qkv = torch.matmul(h, m.wqkv.t()).view(rows, m.heads + 2 * m.kv_heads, m.D)
-        self.append(qkv[:, m.heads:m.heads + m.kv_heads], qkv[:, m.heads + m.kv_heads:])
-        o, _ = dvl.paged_attention(self.cache, qkv[:, :m.heads], self.table.view(rows, -1),
-                                   self.lengths.view(-1), want_lse=False, ws=self.ws)
+        q, k, v = qkv.split([m.heads, m.kv_heads, m.kv_heads], dim=1)
+        self.append(q, k, v)
+        o, _ = dvl.paged_attention(self.cache, q, self.table.view(rows, -1), self.lengths.view(-1),
+                                   want_lse=False, ws=self.ws)
         h, _, _, _ = dvl.add_rmsnorm(torch.matmul(o.view(rows, -1), m.wo.t()), m.norm2, x)
         logits = torch.matmul(h, m.w_trim.t()).view(self.batch, self.beams, -1)
         self.scores, parents, tokens = dvl.beam_select(logits, self.scores, self.beams, d2t=m.d2t,
