@@ -73,12 +73,13 @@
 // by their group's E4M3 scale as f16: the product has at most 6 significant bits
 // and lies in [2^-10, 2688] (or is 0), so it is exact; Q as with FP8.  A lane
 // holds 16 consecutive values of a token of K, one group, so that it needs one
-// scale for them.  Bound by the instructions, not by HBM: 837 of them for 32
-// tokens of a head of 128 (widening 144, scales 128, products 32; without the
-// multiplications by the scales 64 sequences took 158 us instead of 185), 62 % of
-// the issue slots, the ALU pipe 54 % and HBM 50 % busy.  Measured: 64 x <= 16,381
-// tokens, 40 / 8 heads of 128: 178 us (692 MB, 0.57 of the copy rate; the same in
-// FP8, with 1.78 times the bytes: 190-200).
+// scale for them.  Not bound by HBM: 842 instructions for 32 tokens of a head of
+// 128 (widening 144, scales 128, products 32, the rest finds pages, copies and
+// weighs; without the multiplications by the scales 64 sequences took 158 us
+// instead of 185).  61 % of the issue slots, the ALU pipe 54 % and HBM 48 % are
+// busy: with 2.8 warps a scheduler the rest is waiting for a warp's own last
+// result.  Measured: 64 x <= 16,381 tokens, 40 / 8 heads of 128: 180 us (692 MB,
+// 0.57 of the copy rate; the same in FP8, with 1.78 times the bytes: 187-200).
 //
 // Masks.  Row t sees n = length - (T - 1 - t) positions.  Scores at or past
 // n are replaced, not added to, so nothing a masked key holds can show; a

@@ -1,6 +1,6 @@
 // Host-side declarations of the drafting step's operators (norms, attention,
-// beam selection and reordering, kept tokens), shared by their argument checks and their
-// kernel files.
+// beam selection and reordering, kept tokens), shared by their argument checks
+// and their kernel files.
 #pragma once
 
 #include "dvl_internal.h"

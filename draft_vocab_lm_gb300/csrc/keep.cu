@@ -13,9 +13,13 @@
 // of a token, of one sequence, and walks its list, so blocks never meet.
 //
 // Measured (GB300, wall time a call back to back): half of 16 x 16,381 tokens of
-// 8 x 128 in 4 bits 52 us (228 MB, 0.65 of the copy rate: 16 steps of a read, a
-// barrier and a write; with 512 threads and four loads a lane 59); a path of 7 of one request's tree 2.9 us and 64 requests'
-// 3.1, the host's side of the call.
+// 8 x 128 in 4 bits 52 us (228 MB, 0.65 of the copy rate; with 512 threads and four
+// loads a lane 59), in E4M3 78 (0.71), in bf16 148 (0.77).  A block's 16 steps of a
+// read, a barrier and a write follow each other here; by the order above they need
+// not: what step s + 1 reads lies at or past what step s writes, so its loads could
+// be in flight across the barrier.  One such list: 18, 25 and 19 us, the same steps
+// on few blocks.  A path of 7 of one request's tree 3.2 us and 64 requests' 3.1 to
+// 3.3, the host's side of the call.
 #include <cuda_runtime.h>
 
 #include "dvl_device.cuh"
@@ -148,9 +152,13 @@ cudaError_t launch_cache_keep(KeepArgs &a, cudaStream_t s)
         return n;
     };
     // Columns per block: 32 (512 bytes a row) where a list is one step of a block,
-    // else as many of 32, 8, 4 or 2 as leave two blocks an SM.  Half of 16 x 16,381
-    // 4-bit tokens: 64 blocks of 32 columns 223 us (an earlier form), 192 of 8 71,
-    // 384 of 4 (what the rule gives) 52, 768 of 2 70.
+    // else as many of 32, 8, 4 or 2 as leave two blocks an SM.  Half of B x 16,381
+    // tokens of 8 x 128, us with 32, 8, 4 and 2 columns (* what the rule gives):
+    //   4 bits  16: 172, 72, 52*, 72   4: 123, 45, 42, 27*   1: 76, 21, 16, 18*
+    //   E4M3    16: 214, 86, 82*, 94   4: 163, 67, 47, 34*   1: 108, 30, 21, 25*
+    //   bf16    16: 251, 149*, 140, 180   4: 144, 67, 47, 55*   1: 91, 29, 28, 19*
+    // and of 64 x 4,095: 4 bits 66, 45*, 48, 72, bf16 142*, 129, 134, 198.  So it is
+    // within 18 % of the best of them.
     int cols = 32;
     if (a.M > kRows * kWarps)
         while (cols > 2 && a.B * blocks(cols) < 2 * di.sms)

@@ -20,17 +20,21 @@
 // with its own cos and sin, up to 16 warps an SM.
 //
 // Measured (GB300, wall time a call back to back): those 16,381 rows, bf16, 82
-// us (460 MB, 0.83 of the copy rate; 75 with the arithmetic left out); 192 rows
-// to an E4M3 cache 4.4 us; one row 3.1, the host's side of the call.  8,191 rows
-// of 16 + 2 x 2 heads of 256, a quarter rotated, E4M3, no norm: 37 us (0.62; a
-// row is four trips to memory there, and its end and the next row's start are
-// not overlapped within a warp; with one chunk to a lane 33).  Equal or slower:
-// 3 or 5 blocks an SM, two warps a row, loads of the next step before a step's
-// arithmetic, rows looked up 32 at a time.
+// us (460 MB, 0.83 of the copy rate; 75 with the arithmetic left out), E4M3 81,
+// NVFP4 93, without a cache 69; 192 rows to an E4M3 cache 4.4 us, to an NVFP4 one
+// 5.6; one row 3.1, the host's side of the call.  8,191 rows of 16 + 2 x 2 heads of
+// 256, a quarter rotated, E4M3, no norm: 37 us (0.62; with one chunk to a lane 33).
+// Ten steps of such a row are four batches of loads, because a batch ends with its
+// kind of head, and a row's end and the next one's start are not overlapped within
+// a warp.  Where a row has few heads its fixed cost (place, sines, three loops)
+// is the time and most lanes idle: 16,001 rows of 1 + 2 x 1 heads of 64 28 us (12
+// MB).  Equal or slower: 3 or 5 blocks an SM, two warps a row, loads of the next
+// step before a step's arithmetic, rows looked up 32 at a time.
 //
 // Angles.  freq is in turns per position, as a 64-bit fraction, so position x
 // freq modulo one turn is an integer product that wraps: its upper 32 bits are
-// the angle to 2^-32 of a turn however far the position, with no reduction.
+// the angle to 2^-32 of a turn however far the position, with no reduction (as
+// exact as the fraction is: half a unit of it is 2^-34 of a turn at 2^31).
 // cos and sin then come from the fast units, which are good to 2^-21 within
 // half a turn; the result is rounded to 8 bits or fewer.
 #include <cuda_runtime.h>
@@ -44,7 +48,13 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBlocks = 4;  // per SM: 128 registers a thread
-constexpr int kLoads = 5;  // steps whose values a lane has in flight, 32 bytes each
+// Steps whose values a lane has in flight, 32 bytes each.  A row's steps of a kind
+// of head go in batches of this many: with heads of 128 (four a step) 20 and 40
+// heads fill batches of 5, 16, 32 and 64 batches of 4.  16,381 rows with 16, 20, 28,
+// 32, 40 and 64 query heads: 5 54.9, 52.6, 64.1, 74.7, 82.3 and 115.0 us; 4 54.4,
+// 55.7, 63.2, 73.4, 84.9 and 112.9; 3, 6 and 8 slower than the better of the two.
+// Fewer rows, wide heads and few heads: 4 faster by 1 to 3 %.
+constexpr int kLoads = 5;
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {

@@ -177,7 +177,8 @@ cudaError_t launch_beam_reorder(ReorderArgs &a, cudaStream_t s)
         return cudaErrorInvalidConfiguration;
     if (blocks == 0)
         return cudaSuccess;
-    return launch_pdl(a.block_pieces ? beam_reorder_kernel<true> : beam_reorder_kernel<false>, (unsigned)blocks, kThreads, 0, s, a);
+    const auto kernel = a.block_pieces ? beam_reorder_kernel<true> : beam_reorder_kernel<false>;
+    return launch_pdl(kernel, (unsigned)blocks, kThreads, 0, s, a);
 }
 
 }  // namespace dvl

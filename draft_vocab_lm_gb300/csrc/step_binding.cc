@@ -21,8 +21,9 @@
 
 #include "dvl.h"
 
-// Weak: a stand-in for the library that lacks them still links with this
-// module (a call then says so).
+// Weak: a stand-in for the library that lacks them still links with this module.
+// (The package asks its own library for every entry point before it loads this, so
+// one that lacks them is refused there.)
 extern "C" {
 __attribute__((weak)) dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
 __attribute__((weak)) dvl_status dvl_cache_keep(const dvl_kv_cache *, const int32_t *, int64_t, int32_t,
@@ -978,6 +979,9 @@ PyMethodDef methods[] = {
                "cache, in place.\n\n"
                "table:   int32 [B][width]; lengths, first, counts: int32 [B].\n"
                "keep:    int32 [B][M], strictly rising in each row.\n"
+               "For a caller that verifies a tree by its own attention, or drops tokens of a\n"
+               "long cache: what is accepted of a chain, as paged_attention masks it, lies\n"
+               "without gaps already.\n"
                "Returns the new lengths, first + counts (int32 [B])."),
     {nullptr, nullptr, 0, nullptr}};
 

@@ -550,7 +550,9 @@ typedef struct dvl_qk {
  * infinity becomes the largest number).
  * A place below 0 or past the table, or a page outside the pool, is not written
  * (q_out and k_out are).  Rows of no sequence (past starts[B], or before
- * starts[0]) are left as they were, in all outputs.  Two rows with one place in the cache leave either's values there.
+ * starts[0]) are left as they were, in all outputs.  Two rows with one place in the
+ * cache leave either's values there.  Squares above fp32's range make y 0; where all
+ * lie below it and eps is 0, y is infinite or NaN.
  * With an E4M3 or NVFP4 cache both scales lie in [2^-100, 2^100].
  * Errors: DVL_ERR_INVALID_ARG (sizes, pointers or alignment outside the above;
  * a key-value head count or D other than the cache's; rows not a multiple of B
@@ -570,8 +572,10 @@ dvl_status dvl_qk_norm_rope(const dvl_qk *args, void *stream);
  * cache's scales), and
  *   lengths_out[b] = first[b] + counts[b].
  * After a verification first is the length before the drafted tokens and keep
- * names the accepted ones (a path of a tree); with first 0 or a few tokens, keep
- * names what remains of a long cache.  Tokens past the new length stay where
+ * names the accepted ones, a path of a tree that the caller verified by attention of
+ * its own (dvl_paged_attention masks a chain, of which what is accepted lies
+ * without gaps already); with first 0 or a few tokens, keep names what remains of a
+ * long cache.  Tokens past the new length stay where
  * they are, and so do the tables.
  *   lengths: device int32 [B]: cached tokens of each sequence.  Above
  *            table_width * page_size counts as that.
