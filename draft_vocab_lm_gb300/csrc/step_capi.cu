@@ -181,12 +181,12 @@ bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
 {
     if (!x.p || !y.p)
         return false;
+    const Axis r = {1 - rows, rows - 1, rows == 1 ? 0 : 2 * x.stride};
+    const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
     if ((rows == 1 || x.stride == y.stride) &&
         (x.heads == 1 || y.heads == 1 || x.head_stride == y.head_stride)) {
-        const Axis r = {1 - rows, rows - 1, rows == 1 ? 0 : 2 * x.stride};
         const Axis h = {1 - x.heads, y.heads - 1,
                         x.heads > 1 ? 2 * x.head_stride : y.heads > 1 ? 2 * y.head_stride : 0};
-        const int64_t off = (int64_t)(reinterpret_cast<uintptr_t>(y.p) - reinterpret_cast<uintptr_t>(x.p));
         return runs_meet(off, 2 * D, 2 * D, r, h);
     }
     auto bytes = [&](const HeadRows &t) {
@@ -197,7 +197,10 @@ bool meet(const HeadRows &x, const HeadRows &y, int64_t rows, int D)
         const int64_t span = row + 2 * (rows - 1) * t.stride;
         return Rows{at, 1, span, span};
     };
-    return overlap(bytes(x), bytes(y));
+    const Rows a = bytes(x), b = bytes(y);
+    if (a.rows == rows && b.rows == rows && a.stride == b.stride)
+        return runs_meet(off, a.bytes, b.bytes, r, {0, 0, 0});
+    return overlap(a, b);
 }
 
 // The outputs of a call, and whether what it reads reaches into them.  Nearly

@@ -84,3 +84,20 @@ def test_every_overlap_is_refused_and_with_one_stride_nothing_else(status):
             assert not all(nested), kw
         seen[got == 1] += 1
     assert min(seen) > 200
+
+
+def test_rows_side_by_side_with_heads_of_different_strides(status):
+    # rows of four query heads, then keys and values of two heads side by side
+    # (k, v, k, v); a million of them are no more work to compare than a few
+    kw = dict(cache=cache(), q=0x100000000, k=0x100000200, v=0x100000280, k_head_stride=128, v_head_stride=128)
+    for n in ("q", "k", "v", "q_out", "k_out"):
+        kw[n + "_stride"] = 512
+    for rows in (6, 3 << 18):
+        many = dict(kw, rows=rows)
+        assert status(**many, q_out=0x100000000) == NO_DEVICE
+        assert status(**many, q_out=0x900000000) == NO_DEVICE
+        assert status(**many, q_out=0x100000000, k_out=0x100000200, k_out_head_stride=128) == NO_DEVICE
+        assert status(**many, q_out=0x900000000, k_out=0x900000200, k_out_head_stride=128) == NO_DEVICE
+        assert status(**many, q_out=0x900000000, k_out=0x9000001f0, k_out_head_stride=128) == 1
+        assert status(**many, q_out=0x100000040) == 1
+        assert status(**many, q_out=0x100000000, k_out=0x100000280, k_out_head_stride=128) == 1
