@@ -14,7 +14,7 @@
 //
 // Measured (GB300, wall time a call back to back): half of 16 x 16,381 tokens of
 // 8 x 128 in 4 bits 52 us (228 MB, 0.65 of the copy rate; with 512 threads and four
-// loads a lane 59), in E4M3 78 (0.71), in bf16 148 (0.77).  A block's 16 steps of a
+// loads a lane 59), in E4M3 78-82 (0.7), in bf16 148 (0.77).  A block's 16 steps of a
 // read, a barrier and a write follow each other here; by the order above they need
 // not: what step s + 1 reads lies at or past what step s writes, so its loads could
 // be in flight across the barrier.  One such list: 18, 25 and 19 us, the same steps
